@@ -21,6 +21,15 @@
  * moe_permute_noalloc is moe_permute on a fixed per-device scratch array for
  * callers that cannot allocate.
  *
+ * Beside the path stand:
+ *
+ *   moe_route_grouped           routing with softmax or sigmoid scores, a bias
+ *                               for balance, expert groups and a scale
+ *   moe_linear                  dense product with bias, activation and
+ *                               residual (shared expert, projections)
+ *   moe_route_grouped_backward, moe_combine_backward, moe_linear_backward
+ *                               gradients of the three
+ *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer unless stated otherwise, and
  *     must be 16-byte aligned.  The caller owns all memory: the library never
@@ -287,6 +296,159 @@ moe_status moe_ffn_combine_fused(const void* x_perm, const int32_t* expert_count
 moe_status moe_combine(const float* y_perm, const int32_t* inv_perm, const float* topk_w,
                        int64_t T, int32_t k, int32_t H, int64_t R_cap, float* out,
                        void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Routing with scores, balance bias and groups                               */
+/* ------------------------------------------------------------------------- */
+
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum of exp(l) over the row's available experts */
+  MOE_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-l_e)) */
+} moe_score;
+
+/*
+ * moe_route_grouped -- moe_route_topk for routers that score by softmax or
+ * sigmoid, choose by score plus a per-expert balance bias, and restrict each
+ * token to the best groups of experts.
+ *
+ *   logits      [T, E] fp32, row-major.  An expert whose logit is -inf or NaN,
+ *               or whose bias is -inf or NaN, is not available to that token;
+ *               +inf counts as the largest finite fp32.
+ *   bias        [E] fp32 added to the scores for the choice only, or NULL.
+ *   n_group     the E experts form n_group groups of E / n_group consecutive
+ *               ids.  A group's score is the sum of the group_top (1 or 2)
+ *               largest s_e + bias_e of its available experts; the topk_group
+ *               best groups are kept (a group with no available expert ranks
+ *               last), the others' experts are not available.
+ *   topk_idx    [T, k] int32 out: the k best available experts in descending
+ *               s_e + bias_e; slots left over (fewer than k available experts,
+ *               a padding token whose logits are all -inf) hold -1, which
+ *               moe_permute treats as not local.
+ *   topk_w      [T, k] fp32 out: scale * s_e, divided by the sum of the row's
+ *               chosen s_e when renormalize != 0; 0 in the slots that hold -1.
+ *               The division is carried out on scaled scores, so it stays
+ *               exact where every chosen score underflows.
+ * Equal values are taken lowest id first, for groups and for experts.  Without
+ * a bias experts, and groups with group_top 1, are compared by their logits
+ * (both scores grow with them); s_e + bias_e and sums of two are compared in
+ * 64 bits.
+ * Requires 1 <= k <= topk_group * E / n_group, n_group divides E,
+ * 1 <= topk_group <= n_group, group_top in {1, 2} and at most E / n_group,
+ * scale finite; E <= 1024, k <= 32, n_group <= 64.
+ */
+moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k,
+                             int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                             int32_t renormalize, float scale, int32_t* topk_idx, float* topk_w,
+                             void* stream);
+
+/*
+ * moe_route_grouped_backward -- gradient of topk_w with respect to logits for
+ * a fixed choice topk_idx (the choice itself, and so the bias and the groups,
+ * has no gradient).
+ *
+ *   topk_idx    [T, k] int32 as moe_route_grouped writes it; slots outside
+ *               [0, E) take no part.
+ *   d_topk_w    [T, k] fp32: gradient of topk_w.
+ *   d_logits    [T, E] fp32 out: every element is written.  With g = scale *
+ *               d_topk_w and q_j = s_j / (sum of the chosen s):
+ *                 renormalised softmax   q_j (g_j - sum_i q_i g_i)   on the chosen
+ *                 renormalised sigmoid   q_j (g_j - sum_i q_i g_i) (1 - s_j)
+ *                 sigmoid                g_j s_j (1 - s_j)
+ *                 softmax                g_e s_e [e chosen] - s_e sum_i s_i g_i, every e
+ * Requires k <= E, E <= 1024, k <= 32, scale finite.
+ */
+moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                                      int64_t T, int32_t E, int32_t k, int32_t score, int32_t renormalize,
+                                      float scale, float* d_logits, void* stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine.
+ *
+ *   d_out       [T, H] fp32: gradient of out.
+ *   y_perm, inv_perm, topk_w: moe_combine's inputs; the rows that inv_perm
+ *               names are distinct, as moe_permute writes them.
+ *   d_y_perm    [R_cap, H] fp32 out: row inv_perm[t, j] = topk_w[t, j] * d_out[t, :];
+ *               rows no slot names are left untouched.
+ *   d_topk_w    [T, k] fp32 out: sum over h of d_out[t, h] * y_perm[inv_perm[t, j], h];
+ *               0 for a slot that is not local.
+ * Requires H % 4 == 0, k <= 32.
+ */
+moe_status moe_combine_backward(const float* d_out, const float* y_perm, const int32_t* inv_perm,
+                                const float* topk_w, int64_t T, int32_t k, int32_t H, int64_t R_cap,
+                                float* d_y_perm, float* d_topk_w, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Dense product with bias, activation and residual                           */
+/* ------------------------------------------------------------------------- */
+
+/* Activations of moe_linear beyond moe_act's two. */
+#define MOE_ACT_NONE 2 /* out = z */
+#define MOE_ACT_SILU 3 /* out = z / (1 + e^-z) */
+
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_F32 = 1
+} moe_dtype;
+
+/* Bytes of the optional device workspace of moe_linear on the current device:
+ * fp32 partial tiles of products whose reduction is split over workgroups (0
+ * when this size is not split; 0 on invalid arguments). */
+size_t moe_linear_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
+
+/*
+ * moe_linear -- dense projection: a shared expert's layers beside the routed
+ * ones (its down product added to the combined output through `residual`),
+ * or any other projection of the layer's tokens.
+ *
+ *   z   = x . w^T + bias          z_up = x . w_up^T + bias_up   (SwiGLU only)
+ *   out = act(z) + residual       SwiGLU: out = silu(z) * z_up + residual
+ *
+ *   x         [M, K] bf16;  w, w_up [N, K] bf16 (output-major, as moe_grouped_ffn's)
+ *   bias, bias_up  [N] fp32, or NULL (none); bias_up and w_up only for SwiGLU
+ *   residual  [M, N] of out's type, or NULL; may be out itself
+ *   z, z_up   [M, N] bf16 out, or NULL: the pre-activations, rounded to nearest
+ *             even, for moe_linear_backward (z_up only for SwiGLU)
+ *   out       [M, N] out_dtype (moe_dtype)
+ * Accumulation, bias, activation and residual are fp32; each output is rounded
+ * once.  Outputs must not overlap the inputs (residual == out excepted).
+ * ws / ws_bytes: optional device scratch (NULL / 0 is allowed) of at least
+ * moe_linear_workspace_bytes(); with it, small products split their reduction
+ * over workgroups and sum the fp32 partials in a fixed order, so results are
+ * deterministic, and differ from those without ws by fp32 summation order.  A
+ * non-NULL ws that is too small returns MOE_ERR_WORKSPACE.
+ * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1.  M == 0: nothing to do.
+ */
+moe_status moe_linear(const void* x, const void* w, const void* w_up, const float* bias, const float* bias_up,
+                      const void* residual, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,
+                      void* z, void* z_up, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of the device workspace moe_linear_backward needs on the current
+ * device (0 on invalid arguments). */
+size_t moe_linear_backward_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
+
+/*
+ * moe_linear_backward -- gradients of moe_linear (that of residual is d_out).
+ *
+ *   d_out     [M, N] out_dtype: gradient of out
+ *   x, w, w_up, act: moe_linear's;  z, z_up [M, N] bf16: what it kept (NULL for
+ *             MOE_ACT_NONE, z_up NULL except for SwiGLU)
+ *   d_x       [M, K] bf16 out, or NULL to skip:  dz . w (+ dz_up . w_up)
+ *   d_w, d_w_up  [N, K] bf16 out, or NULL:  dz^T . x, dz_up^T . x
+ *   d_bias, d_bias_up  [N] fp32 out, or NULL:  sums of dz, dz_up over the rows
+ * with dz = d_out * act'(z) (SwiGLU: dz = d_out * z_up * silu'(z),
+ * dz_up = d_out * silu(z)), computed in fp32; the products read it rounded to
+ * bf16 (their other operands are bf16 too), the sums take it unrounded.
+ * Accumulation is fp32, outputs are rounded once, and results are
+ * deterministic.  Outputs must not overlap the inputs or one another.
+ * ws / ws_bytes: device scratch of at least
+ * moe_linear_backward_workspace_bytes(); needed whenever M > 0.
+ * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1.  M == 0: the weight and
+ * bias gradients are set to zero.
+ */
+moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, const void* w_up, const void* z,
+                               const void* z_up, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,
+                               void* d_x, void* d_w, void* d_w_up, float* d_bias, float* d_bias_up, void* ws,
+                               size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

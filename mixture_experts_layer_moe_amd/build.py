@@ -17,7 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = ["moe_api.hip", "route_topk.hip", "permute.hip", "grouped_gemm.hip", "combine.hip"]
+SOURCES = ["moe_api.hip", "route_topk.hip", "permute.hip", "grouped_gemm.hip", "combine.hip",
+           "route_grouped.hip", "combine_backward.hip", "linear.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -37,7 +38,7 @@ def _run(cmd, verbose):
     return r.stdout
 
 
-def build(verbose: bool = False, jobs: int = 5, extra_flags=()) -> str:
+def build(verbose: bool = False, jobs: int = 8, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []
     cmds = []

@@ -2,6 +2,9 @@
 // The operations and their argument conventions are documented in include/moe.h.
 #include "../../include/moe.h"
 #include "common.h"
+#include "operators.h"
+
+#include <math.h>
 
 namespace {
 
@@ -283,6 +286,154 @@ moe_status moe_combine(const float* y_perm, const int32_t* inv_perm, const float
     return MOE_ERR_INVALID_ARG;
   return launched(moe::launch_combine(y_perm, inv_perm, topk_w, T, k, H, R_cap, out,
                                       static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k, int32_t score,
+                             int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
+                             int32_t* topk_idx, float* topk_w, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (n_group < 1 || n_group > E || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
+    return MOE_ERR_INVALID_ARG;
+  if (group_top < 1 || group_top > 2 || group_top > E / n_group || (int64_t)k > (int64_t)topk_group * (E / n_group))
+    return MOE_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || n_group > 64 || T > (int64_t)INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w)) return MOE_ERR_INVALID_ARG;
+  const moe::RouteArgs a{logits,  bias,       T,         E,     k,        score == MOE_SCORE_SIGMOID, renormalize != 0,
+                         n_group, topk_group, group_top, scale, topk_idx, topk_w};
+  return launched(moe::launch_route_grouped(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, int64_t T,
+                                      int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
+                                      float* d_logits, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || T > (int64_t)INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const void* ptrs[] = {logits, topk_idx, d_topk_w, d_logits};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const moe::RouteBwdArgs a{logits, topk_idx, d_topk_w, T, E, k, score == MOE_SCORE_SIGMOID, renormalize != 0, scale,
+                            d_logits};
+  return launched(moe::launch_route_grouped_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_combine_backward(const float* d_out, const float* y_perm, const int32_t* inv_perm, const float* topk_w,
+                                int64_t T, int32_t k, int32_t H, int64_t R_cap, float* d_y_perm, float* d_topk_w,
+                                void* stream) {
+  if (T < 0 || k < 1 || H < 1 || R_cap < 0) return MOE_ERR_INVALID_ARG;
+  if (H % 4 != 0 || k > 32 || T > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const void* ptrs[] = {d_out, y_perm, inv_perm, topk_w, d_y_perm, d_topk_w};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return launched(moe::launch_combine_backward(d_out, y_perm, inv_perm, topk_w, T, k, H, R_cap, d_y_perm, d_topk_w,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool act_ok(int32_t act) {
+  return act == MOE_ACT_GELU || act == MOE_ACT_SWIGLU || act == MOE_ACT_NONE || act == MOE_ACT_SILU;
+}
+
+// Sizes of moe_linear and moe_linear_backward.
+moe_status linear_sizes(int64_t M, int32_t N, int32_t K, int32_t act) {
+  if (M < 0 || N < 1 || K < 1 || !act_ok(act)) return MOE_ERR_INVALID_ARG;
+  if (K % 8 != 0 || N > (1 << 20) || K > (1 << 20) || M > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act) {
+  if (linear_sizes(M, N, K, act) != MOE_OK) return 0;
+  return moe::linear_ws_bytes(M, N, K, act);
+}
+
+moe_status moe_linear(const void* x, const void* w, const void* w_up, const float* bias, const float* bias_up,
+                      const void* residual, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype, void* z,
+                      void* z_up, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = linear_sizes(M, N, K, act);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  const bool dual = act == MOE_ACT_SWIGLU;
+  if (!dual && (w_up || bias_up || z_up)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !out || (dual && !w_up)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, w, w_up, bias, bias_up, residual, z, z_up, out, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (ws && ws_bytes < moe::linear_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
+  moe::LinearArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.w_up = static_cast<const uint16_t*>(w_up);
+  a.bias = bias;
+  a.bias_up = bias_up;
+  a.residual = residual;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.out_f32 = out_dtype == MOE_F32;
+  a.z = static_cast<uint16_t*>(z);
+  a.z_up = static_cast<uint16_t*>(z_up);
+  a.out = out;
+  a.ws = ws;
+  return launched(moe::launch_linear(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_linear_backward_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act) {
+  if (linear_sizes(M, N, K, act) != MOE_OK) return 0;
+  return moe::linear_backward_ws_bytes(M, N, K, act);
+}
+
+moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, const void* w_up, const void* z,
+                               const void* z_up, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,
+                               void* d_x, void* d_w, void* d_w_up, float* d_bias, float* d_bias_up, void* ws,
+                               size_t ws_bytes, void* stream) {
+  const moe_status st = linear_sizes(M, N, K, act);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  const bool dual = act == MOE_ACT_SWIGLU;
+  if (!dual && (w_up || z_up || d_w_up || d_bias_up)) return MOE_ERR_INVALID_ARG;
+  if (act == MOE_ACT_NONE && z) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {d_out, x, w, w_up, z, z_up, d_x, d_w, d_w_up, d_bias, d_bias_up, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (M > 0) {
+    if (!d_out || !ws || (act != MOE_ACT_NONE && !z) || (dual && !z_up)) return MOE_ERR_INVALID_ARG;
+    if (d_x && (!w || (dual && !w_up))) return MOE_ERR_INVALID_ARG;
+    if ((d_w || d_w_up) && !x) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe::linear_backward_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
+  }
+  moe::LinearBwdArgs a{};
+  a.d_out = d_out;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.w_up = static_cast<const uint16_t*>(w_up);
+  a.z = static_cast<const uint16_t*>(z);
+  a.z_up = static_cast<const uint16_t*>(z_up);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.out_f32 = out_dtype == MOE_F32;
+  a.d_x = static_cast<uint16_t*>(d_x);
+  a.d_w = static_cast<uint16_t*>(d_w);
+  a.d_w_up = static_cast<uint16_t*>(d_w_up);
+  a.d_bias = d_bias;
+  a.d_bias_up = d_bias_up;
+  a.ws = ws;
+  return launched(moe::launch_linear_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
