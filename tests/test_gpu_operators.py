@@ -210,7 +210,8 @@ def whole(shape, g, lim=3):
 
 SHAPES = [(1, 1, 8), (1, 256, 64), (2, 17, 24), (5, 64, 1000), (16, 48, 512), (17, 100, 136), (31, 33, 72), (64, 64, 64),
           (65, 130, 200), (100, 7, 4096), (128, 128, 128), (129, 257, 320), (200, 512, 8), (255, 96, 1032), (256, 256, 256),
-          (257, 1001, 456), (300, 64, 2048), (513, 384, 704), (1, 2048, 2056), (40, 1000, 3000), (700, 520, 136)]
+          (257, 1001, 456), (300, 64, 2048), (513, 384, 704), (1, 2048, 2056), (40, 1000, 3000), (700, 520, 136),
+          (1030, 1100, 264), (1300, 1029, 136), (2051, 1536, 72)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -245,7 +246,7 @@ def act_bound(act, zb, z, u=None, ub=None):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 40, 64), (3, 200, 328), (16, 128, 512), (50, 33, 72), (130, 190, 520), (300, 257, 136),
-                                   (600, 300, 1064)])
+                                   (600, 300, 1064), (1100, 1031, 72), (1029, 1152, 200)])
 @pytest.mark.parametrize("act", ["none", "gelu", "silu", "swiglu"])
 @pytest.mark.parametrize("odt", [BF, F32])
 def test_linear_activations(M, N, K, act, odt):
@@ -301,7 +302,8 @@ def test_linear_rows_do_not_touch_each_other():
 
 
 BWD = [(1, 1, 8), (1, 64, 64), (3, 40, 72), (17, 100, 136), (64, 64, 64), (65, 130, 200), (128, 256, 128), (129, 257, 320),
-       (300, 70, 264), (700, 257, 136), (70, 520, 1032), (260, 300, 520)]
+       (300, 70, 264), (700, 257, 136), (70, 520, 1032), (260, 300, 520),
+       (1030, 1100, 1064), (1100, 1027, 1288)]
 
 
 @pytest.mark.parametrize("M,N,K", BWD)
@@ -321,7 +323,7 @@ def test_linear_backward_whole_numbers(M, N, K, odt):
     assert torch.equal(d_b.cpu(), G.sum(0).float())
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (5, 33, 72), (130, 190, 264), (300, 257, 136), (520, 64, 520)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (5, 33, 72), (130, 190, 264), (300, 257, 136), (520, 64, 520), (1100, 1032, 1096)])
 @pytest.mark.parametrize("act", ["gelu", "silu", "swiglu"])
 @pytest.mark.parametrize("odt", [BF, F32])
 def test_linear_backward(M, N, K, act, odt):
