@@ -15,6 +15,7 @@
 // so no operand is transposed in memory.
 #include "operators.h"
 
+#include <atomic>
 #include <type_traits>
 
 namespace moe {
@@ -23,6 +24,7 @@ namespace {
 constexpr int BK = 64;  // reduction indices per stage
 
 typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
+typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
 __device__ __forceinline__ float bf2f(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
@@ -141,79 +143,113 @@ __device__ __forceinline__ void activate_all(int act, floatx4 (&v)[NV], const fl
   }
 }
 
-__device__ __forceinline__ uint2 pack4(floatx4 x) {
-  return uint2{(uint32_t)f2bf_bits(x[0]) | ((uint32_t)f2bf_bits(x[1]) << 16),
+__device__ __forceinline__ u32x2 pack4(floatx4 x) {
+  return u32x2{(uint32_t)f2bf_bits(x[0]) | ((uint32_t)f2bf_bits(x[1]) << 16),
                (uint32_t)f2bf_bits(x[2]) | ((uint32_t)f2bf_bits(x[3]) << 16)};
 }
 
-// The epilogue of NV rows, row0 + r * step, in the four columns from n (a multiple of 4, n < N): g and u hold the
-// products.  All of the rows' residuals are loaded before the first store, so NV rows are in flight.
-template <int NV>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t row0, int step, int64_t M, int n, int N,
-                                       floatx4 (&g)[NV], floatx4 (&u)[NV], floatx4 bias, floatx4 bias_up) {
-  const int cnt = N - n < 4 ? N - n : 4;
-  const bool vec = (N & 3) == 0;  // then a row's groups of four are aligned
-  floatx4 res[NV];
+// The rows from row0 on of a product's outputs, and what is added to them: buffer resources that end with row M, so
+// that rows past it are neither read nor written (and absent operands read as zeros).  Offsets stay far below 2^31:
+// a tile has at most 256 rows of at most 2^20 columns.
+struct Sink {
+  __amdgpu_buffer_rsrc_t out, z, z_up, res;
+  int N, act;
+  bool f32, vec, has_z, has_zu, has_res;
+
+  __device__ __forceinline__ Sink(const Epilogue& e, int64_t row0, int rows, int64_t M, int N_) : N(N_), act(e.act), f32(e.f32) {
+    const int64_t left = M - row0 < rows ? M - row0 : rows, at = row0 * N, n = left * N;
+    vec = (N & 3) == 0;  // then a row's groups of four are aligned
+    has_z = e.z != nullptr;
+    has_zu = e.z_up != nullptr;
+    has_res = e.residual != nullptr;
+    const int es = f32 ? 4 : 2;
+    out = make_rsrc(static_cast<char*>(e.out) + at * es, n * es);
+    res = make_rsrc(static_cast<const char*>(has_res ? e.residual : e.out) + at * es, has_res ? n * es : 0);
+    z = make_rsrc((has_z ? e.z : static_cast<uint16_t*>(e.out)) + at, has_z ? n * 2 : 0);
+    z_up = make_rsrc((has_zu ? e.z_up : static_cast<uint16_t*>(e.out)) + at, has_zu ? n * 2 : 0);
+  }
+};
+
+// Four values at element offset `at` (kOut: nowhere) of row-major data of type bf16; cnt of them exist.
+__device__ __forceinline__ void put_bf16(const Sink& k, __amdgpu_buffer_rsrc_t r, uint32_t at, int cnt, floatx4 x) {
+  const u32x2 h = pack4(x);
+  if (k.vec) {
+    __builtin_amdgcn_raw_buffer_store_b64(h, r, at == kOut ? kOut : at * 2, 0, 0);
+  } else {
 #pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    const int64_t row = row0 + r * step, at = row * N + n;
-    res[r] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (e.residual && row < M) {
-      if (e.f32) {
-        const float* p = static_cast<const float*>(e.residual) + at;
-        if (vec) res[r] = *reinterpret_cast<const floatx4*>(p);
-        else
-          for (int q = 0; q < cnt; ++q) res[r][q] = p[q];
-      } else {
-        const uint16_t* p = static_cast<const uint16_t*>(e.residual) + at;
-        if (vec) {
-          const uint2 h = *reinterpret_cast<const uint2*>(p);
-          res[r] = floatx4{bf2f((uint16_t)h.x), bf2f((uint16_t)(h.x >> 16)), bf2f((uint16_t)h.y), bf2f((uint16_t)(h.y >> 16))};
-        } else {
-          for (int q = 0; q < cnt; ++q) res[r][q] = bf2f(p[q]);
+    for (int q = 0; q < 4; ++q)
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(h[q >> 1] >> (16 * (q & 1))), r, at == kOut || q >= cnt ? kOut : (at + q) * 2, 0, 0);
+  }
+}
+
+// The epilogue of NV rows, r + q * step of the sink, in the four columns from n (a multiple of 4): g and u hold the
+// products.  All of the rows' residuals are loaded before the first store.  Branches are few and uniform: code that
+// runs once per tile is paid for by its instruction fetches.
+template <int NV>
+__device__ __forceinline__ void finish(const Sink& k, int r, int step, int n, floatx4 (&g)[NV], floatx4 (&u)[NV],
+                                       floatx4 bias, floatx4 bias_up) {
+  const int cnt = k.N - n;  // columns that exist
+  floatx4 res[NV];
+  uint32_t at[NV];
+#pragma unroll
+  for (int q = 0; q < NV; ++q) {
+    at[q] = cnt > 0 ? (uint32_t)((r + q * step) * k.N + n) : kOut;
+    res[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+    g[q] += bias;
+    u[q] += bias_up;
+  }
+  if (k.has_res) {
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+      if (!k.vec) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = cnt > e;
+          res[q][e] = k.f32 ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(k.res, in ? (at[q] + e) * 4 : kOut, 0, 0))
+                            : bf2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(k.res, in ? (at[q] + e) * 2 : kOut, 0, 0));
         }
+      } else if (k.f32) {
+        res[q] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(k.res, at[q] == kOut ? kOut : at[q] * 4, 0, 0));
+      } else {
+        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(k.res, at[q] == kOut ? kOut : at[q] * 2, 0, 0);
+        res[q] = floatx4{bf2f((uint16_t)h[0]), bf2f((uint16_t)(h[0] >> 16)), bf2f((uint16_t)h[1]), bf2f((uint16_t)(h[1] >> 16))};
       }
     }
   }
-  auto put = [&](uint16_t* o, floatx4 x, int64_t at) {
-    const uint2 h = pack4(x);
-    if (vec) *reinterpret_cast<uint2*>(o + at) = h;
-    else
-      for (int q = 0; q < cnt; ++q) o[at + q] = (uint16_t)((q & 2 ? h.y : h.x) >> (16 * (q & 1)));
-  };
+  if (k.has_z)
 #pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    g[r] += bias;
-    u[r] += bias_up;
-    const int64_t row = row0 + r * step;
-    if (row < M) {
-      if (e.z) put(e.z, g[r], row * N + n);
-      if (e.z_up) put(e.z_up, u[r], row * N + n);
-    }
-  }
-  activate_all<NV>(e.act, g, u);
+    for (int q = 0; q < NV; ++q) put_bf16(k, k.z, at[q], cnt, g[q]);
+  if (k.has_zu)
 #pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    const int64_t row = row0 + r * step, at = row * N + n;
-    const floatx4 v = g[r] + res[r];
-    if (row >= M) continue;
-    if (!e.f32) {
-      put(static_cast<uint16_t*>(e.out), v, at);
-    } else {
-      float* o = static_cast<float*>(e.out) + at;
-      if (vec) *reinterpret_cast<floatx4*>(o) = v;
-      else
-        for (int q = 0; q < cnt; ++q) o[q] = v[q];
-    }
+    for (int q = 0; q < NV; ++q) put_bf16(k, k.z_up, at[q], cnt, u[q]);
+  activate_all<NV>(k.act, g, u);
+#pragma unroll
+  for (int q = 0; q < NV; ++q) g[q] += res[q];
+  if (!k.f32) {
+#pragma unroll
+    for (int q = 0; q < NV; ++q) put_bf16(k, k.out, at[q], cnt, g[q]);
+  } else if (k.vec) {
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, g[q]), k.out, at[q] == kOut ? kOut : at[q] * 4, 0, 0);
+  } else {
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = g[q][e];  // (a vector element itself is not an object to bit_cast)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), k.out, cnt > e ? (at[q] + e) * 4 : kOut, 0, 0);
+      }
   }
 }
 
 // Four consecutive biases from column n, zeros past N or where there is none.
 __device__ __forceinline__ floatx4 load_bias(const float* b, int n, int N) {
-  floatx4 v = {0.f, 0.f, 0.f, 0.f};
-  if (b)
-    for (int q = 0; q < 4; ++q)
-      if (n + q < N) v[q] = b[n + q];
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(b, b ? (int64_t)N * 4 : 0);
+  floatx4 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    v[q] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, n + q < N ? (n + q) * 4 : kOut, 0, 0));
   return v;
 }
 
@@ -436,10 +472,13 @@ struct Tile {
     float* sm = reinterpret_cast<float*>(smem);
     constexpr int C4 = BN / 4, STEP = NW * 64 / C4, NV = 32 / STEP < 4 ? 32 / STEP : 4;  // a thread keeps its columns
     const int n = (threadIdx.x % C4) * 4;
+    const Sink sink(g.e, m0, BM, g.M, g.N);
     const floatx4 bias = load_bias(g.e.bias, n0 + n, g.N), bias_up = load_bias(g.e.bias_up, n0 + n, g.N);
 #pragma unroll 1
     for (int i = 0; i < TM / 2; ++i) {
-      __syncthreads();
+      // (barriers that wait for LDS alone: __syncthreads() would also wait for the last pass's stores, 1.5 us)
+      wait_lgkm0();
+      ring_barrier();
 #pragma unroll
       for (int ii = 0; ii < TM / 2; ++ii) {
         if (ii != i) continue;
@@ -451,11 +490,10 @@ struct Tile {
             *reinterpret_cast<floatx4*>(sm + (wm * 32 + h * 16 + (lane & 15)) * PITCH + c) = acc[j][2 * ii + h];
           }
       }
-      __syncthreads();
-      if (n0 + n >= g.N) continue;
+      wait_lgkm0();
+      ring_barrier();
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {  // the 32 rows of the upper and lower half of the tile
-        const int64_t row0 = m0 + h * (BM / 2) + i * 32;
 #pragma unroll 1
         for (int r0 = 0; r0 < 32; r0 += NV * STEP) {
           floatx4 v[NV], u[NV];
@@ -474,7 +512,7 @@ struct Tile {
               if (NMAT == 2) *reinterpret_cast<floatx4*>(o + BN) = u[r];
             }
           } else {
-            finish<NV>(g.e, row0 + rt, STEP, g.M, n0 + n, g.N, v, u, bias, bias_up);
+            finish<NV>(sink, h * (BM / 2) + i * 32 + rt, STEP, n0 + n, v, u, bias, bias_up);
           }
         }
       }
@@ -485,82 +523,333 @@ struct Tile {
 constexpr int kXcds = 8;
 constexpr int kGroupM = 8;  // row tiles per rasterisation group
 
-// Workgroup -> tile: workgroups go round-robin to the XCDs, and each XCD's run of tiles is contiguous in an order
-// of groups of kGroupM row tiles, column by column, so that tiles that run together share operand panels in its L2.
-__device__ __forceinline__ void tile_of(int bid, int G, int mt, int nt, int& ti, int& tj) {
-  const int q = G / kXcds, r = G % kXcds, x = bid % kXcds;
-  const int vid = x * q + (x < r ? x : r) + bid / kXcds;
+// Workgroup -> slice and tile: workgroups go round-robin to the XCDs, and each XCD's run is contiguous in an order of
+// slices, and in a slice of groups of kGroupM row tiles, column by column, so that tiles that run together share operand panels in its L2.
+__device__ __forceinline__ void tile_of(int bid, int G, int mt, int nt, int tiles, int& slice, int& ti, int& tj) {
+  const int each = G / kXcds, more = G % kXcds, x = bid % kXcds;
+  int vid = x * each + (x < more ? x : more) + bid / kXcds;
+  slice = vid / tiles;
+  vid -= slice * tiles;
   const int per = kGroupM * nt, grp = vid / per, rem = vid % per;
   const int rows = mt - grp * kGroupM < kGroupM ? mt - grp * kGroupM : kGroupM;
   tj = rem / rows;
   ti = grp * kGroupM + rem % rows;
 }
 
-// 256-row tiles: 8 wavefronts, two per SIMD; 128-row tiles: 4, and two workgroups per CU.
-constexpr int waves(int BM) { return BM == 256 ? 8 : 4; }
+// Tile kinds: rows, columns staged per stage (of one matrix, or half of each of two), wavefronts, workgroups per CU.
+struct Kind {
+  int bm, bn, nw, per_cu;
+};
+constexpr Kind kKinds[] = {{256, 256, 8, 1}, {128, 128, 4, 2}, {64, 128, 4, 3}};
+constexpr int kNumKinds = 3;
 
-template <int BM, int BN, bool A_COLS, bool B_COLS, int NMAT>
-__global__ __launch_bounds__(waves(BM) * 64, 2) void gemm_kernel(Gemm g) {
-  using T = Tile<BM, BN, A_COLS, B_COLS, NMAT, waves(BM)>;
-  __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
-  int ti, tj;
-  tile_of(blockIdx.x, gridDim.x, g.mt, g.nt, ti, tj);
-  T::run(smem, g, (int64_t)ti * BM, tj * BN, 0, g.nk, nullptr);
+template <int KIND, bool A_COLS, bool B_COLS, int NMAT>
+using KindTile = Tile<kKinds[KIND].bm, kKinds[KIND].bn / NMAT, A_COLS, B_COLS, NMAT, kKinds[KIND].nw>;
+
+// One product of a launch: its tiles times S slices of the reduction, slice q covering stages
+// [q nk / S, (q + 1) nk / S).  With S > 1 slice q of tile t leaves fp32 sums at part + (q tiles + t) (tile floats),
+// which reduce_kernel adds in order.
+struct Job {
+  Gemm g;
+  int S;
+  int first;  // first workgroup
+  float* part;
+};
+
+template <int KIND, bool A_COLS, bool B_COLS, int NMAT>
+__device__ __forceinline__ void run_job(char* smem, const Job& j, int bid) {
+  using T = KindTile<KIND, A_COLS, B_COLS, NMAT>;
+  constexpr int BM = kKinds[KIND].bm, BN = kKinds[KIND].bn / NMAT;
+  const int tiles = j.g.mt * j.g.nt;
+  int ti, tj, q;
+  tile_of(bid, tiles * j.S, j.g.mt, j.g.nt, tiles, q, ti, tj);
+  const int k0 = (int)((int64_t)q * j.g.nk / j.S), k1 = (int)((int64_t)(q + 1) * j.g.nk / j.S);
+  float* part = j.S > 1 ? j.part + ((int64_t)q * tiles + ti * j.g.nt + tj) * (BM * NMAT * BN) : nullptr;
+  T::run(smem, j.g, (int64_t)ti * BM, tj * BN, k0, k1, part);
+}
+
+template <int KIND, int NMAT>
+__global__ __launch_bounds__(kKinds[KIND].nw * 64, KIND == 2 ? 3 : 2) void forward_kernel(Job j) {
+  __shared__ __attribute__((aligned(1024))) char smem[KindTile<KIND, false, false, NMAT>::SMEM];
+  run_job<KIND, false, false, NMAT>(smem, j, blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: stream the weights
+// ---------------------------------------------------------------------------
+// M <= 16.  A workgroup owns 16 weight rows -- 16 output columns, or 8 of the gate's and the same 8 of the up
+// matrix's -- and its NK wavefronts a share of K each, so nothing is exchanged before the end.  A load takes 128
+// bytes of each of 8 rows: with 64 bytes of 16 rows, the MFMA's own layout, whole lines are asked for twice and a CU
+// draws 20 GB/s instead of 28 (1 x 28672 x 8192: 92 against 67 us).  So a wavefront passes its operands through LDS
+// of its own, which needs no barrier (its LDS accesses complete in order).  U steps of 64 reduction indices are in
+// flight.  The wavefronts' sums meet in LDS and are added in order.
+template <bool DUAL, int NK, int U>
+__global__ __launch_bounds__(NK * 64) void skinny_kernel(Gemm g) {
+  constexpr int COLS = DUAL ? 8 : 16;  // output columns
+  __shared__ __attribute__((aligned(1024))) char smem[NK * 4096];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* sw = smem + wave * 4096;  // weight rows, then token rows: 16 x 128 B each, chunks swizzled
+  char* sx = sw + 2048;
+  const int n0 = blockIdx.x * COLS;
+  const int K = (int)g.b.R, steps = (K + BK - 1) / BK, M = (int)g.M;
+  const int s0 = (int)((int64_t)wave * steps / NK), s1 = (int)((int64_t)(wave + 1) * steps / NK);
+  const int cols = g.N - n0 < COLS ? g.N - n0 : COLS;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(g.a.p, (int64_t)M * K * 2);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(g.b.p + (int64_t)n0 * K, (int64_t)cols * K * 2);
+  const __amdgpu_buffer_rsrc_t ru = DUAL ? make_rsrc(g.b_up.p + (int64_t)n0 * K, (int64_t)cols * K * 2) : rw;
+  const int r = lane >> 3;
+  const int k0 = ((lane & 7) ^ swz(r)) * 8, k1 = ((lane & 7) ^ swz(r + 8)) * 8;  // this lane's chunk of rows r, r + 8
+  const uint32_t w0 = r < cols ? (r * K + k0) * 2 : kOut;
+  const uint32_t w1 = DUAL ? (r < cols ? (r * K + k1) * 2 : kOut) : (r + 8 < cols ? ((r + 8) * K + k1) * 2 : kOut);
+  const uint32_t x0 = r < M ? (r * K + k0) * 2 : kOut, x1 = r + 8 < M ? ((r + 8) * K + k1) * 2 : kOut;
+  struct Step {
+    u32x4 w0, w1, x0, x1;
+  };
+  auto load = [&](Step& b, int s) {
+    const int kk = s * BK;
+    const bool in0 = s < s1 && kk + k0 < K, in1 = s < s1 && kk + k1 < K;
+    b.w0 = __builtin_amdgcn_raw_buffer_load_b128(rw, in0 && w0 != kOut ? w0 + kk * 2 : kOut, 0, 2);
+    b.w1 = __builtin_amdgcn_raw_buffer_load_b128(ru, in1 && w1 != kOut ? w1 + kk * 2 : kOut, 0, 2);
+    b.x0 = __builtin_amdgcn_raw_buffer_load_b128(rx, in0 && x0 != kOut ? x0 + kk * 2 : kOut, 0, 0);
+    if (M > 8) b.x1 = __builtin_amdgcn_raw_buffer_load_b128(rx, in1 && x1 != kOut ? x1 + kk * 2 : kOut, 0, 0);
+  };
+  if (M <= 8) *reinterpret_cast<u32x4*>(sx + 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Step& b) {
+    *reinterpret_cast<u32x4*>(sw + lane * 16) = b.w0;
+    *reinterpret_cast<u32x4*>(sw + 1024 + lane * 16) = b.w1;
+    *reinterpret_cast<u32x4*>(sx + lane * 16) = b.x0;
+    if (M > 8) *reinterpret_cast<u32x4*>(sx + 1024 + lane * 16) = b.x1;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fragment<false, 16>(sw, 0, ks, lane), fragment<false, 16>(sx, 0, ks, lane),
+                                                    acc, 0, 0, 0);
+  };
+  Step b[U];
+#pragma unroll
+  for (int q = 0; q < U; ++q) load(b[q], s0 + q);
+  for (int s = s0; s < s1; s += U)
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      multiply(b[q]);
+      load(b[q], s + q + U);
+    }
+  __syncthreads();
+  floatx4* part = reinterpret_cast<floatx4*>(smem);
+  part[wave * 64 + lane] = acc;
+  __syncthreads();
+  // Lane l of a partial sum: token row l % 16, weight rows 4 (l / 16) + 0..3.
+  if (threadIdx.x < (DUAL ? 32 : 64)) {
+    floatx4 v[1] = {part[lane]}, u[1] = {part[DUAL ? lane + 32 : lane]};
+    for (int q = 1; q < NK; ++q) {
+      v[0] += part[q * 64 + lane];
+      u[0] += part[q * 64 + (DUAL ? lane + 32 : lane)];
+    }
+    const int n = n0 + (lane >> 4) * 4;
+    const Sink sink(g.e, 0, 16, g.M, g.N);
+    finish<1>(sink, lane & 15, 0, n, v, u, load_bias(g.e.bias, n, g.N), load_bias(g.e.bias_up, n, g.N));
+  }
 }
 
 // ---------------------------------------------------------------------------
 // dz, and the bias gradients
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 64;  // rows per block of dz_kernel
+constexpr int kDzRows = 32;  // rows per block of dz_kernel
 
-// dz (SwiGLU: dz and dz_up, dz_up at column offset Np) rounded to bf16, [M, ld] with zeros in columns
-// [N, Np) of each, and the block's column sums of the unrounded values, part[block row][mats][N].
+// VEC consecutive values of row-major [., N] data as floats (VEC = 8: 16-byte aligned).
+template <int VEC>
+__device__ __forceinline__ void load_values(float (&v)[VEC], const void* p, bool f32, int64_t at) {
+  if constexpr (VEC == 1) {
+    v[0] = f32 ? static_cast<const float*>(p)[at] : bf2f(static_cast<const uint16_t*>(p)[at]);
+  } else if (f32) {
+    const floatx4* q = reinterpret_cast<const floatx4*>(static_cast<const float*>(p) + at);
+    const floatx4 a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+    const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = bf2f((uint16_t)a[e]);
+      v[2 * e + 1] = bf2f((uint16_t)(a[e] >> 16));
+    }
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_values(uint16_t* o, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    *o = f2bf_bits(v[0]);
+  } else {
+    u32x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = (uint32_t)f2bf_bits(v[2 * e]) | ((uint32_t)f2bf_bits(v[2 * e + 1]) << 16);
+    *reinterpret_cast<u32x4*>(o) = h;
+  }
+}
+
+// dz (SwiGLU: dz and dz_up, dz_up at column offset Np) rounded to bf16, [M, ld] with zeros in columns [N, Np) of
+// each, and the block's column sums of the unrounded values, part[block row][mats][N].  HBM-bound: reads d_out, z
+// (and z_up), writes dz once.  64 threads side by side of VEC columns (8 where rows are 16-byte aligned, N % 8 ==
+// 0), four rows apart; each thread has the loads of U rows in flight (two of eight columns: more would
+// halve the occupancy that hides them).
+template <int VEC>
 __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ d_out, bool f32,
                                                  const uint16_t* __restrict__ z, const uint16_t* __restrict__ z_up,
                                                  int act, int64_t M, int N, int Np, int ld, uint16_t* __restrict__ dz,
                                                  float* __restrict__ part) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= Np) return;
-  const int64_t r0 = (int64_t)blockIdx.y * kDzRows, r1 = r0 + kDzRows < M ? r0 + kDzRows : M;
-  const bool dual = act == ACT_SWIGLU;
-  float s0 = 0.f, s1 = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    float d = 0.f, du = 0.f;
-    if (n < N) {
-      const int64_t at = r * N + n;
-      const float go = f32 ? static_cast<const float*>(d_out)[at] : bf2f(static_cast<const uint16_t*>(d_out)[at]);
-      if (act == ACT_NONE) {
-        d = go;
-      } else {
-        const float zz = bf2f(z[at]);
-        d = go * activate_grad(act, zz);
-        if (dual) {
-          d *= bf2f(z_up[at]);
-          du = go * activate(act, zz);
-        }
+  constexpr int U = VEC == 8 ? 2 : 8;
+  const int n = (blockIdx.x * 64 + (threadIdx.x & 63)) * VEC, rg = threadIdx.x >> 6;
+  const int64_t r0 = (int64_t)blockIdx.y * kDzRows;
+  const bool dual = act == ACT_SWIGLU, in = n < N;
+  float s0[VEC], s1[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) s0[e] = s1[e] = 0.f;
+#pragma unroll 1
+  for (int q0 = 0; q0 < kDzRows / 4; q0 += U) {
+    float g[U][VEC], a[U][VEC], b[U][VEC];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int64_t r = r0 + (q0 + q) * 4 + rg;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[q][e] = a[q][e] = b[q][e] = 0.f;
+      if (in && r < M) {
+        load_values<VEC>(g[q], d_out, f32, r * N + n);
+        if (act != ACT_NONE) load_values<VEC>(a[q], z, false, r * N + n);
+        if (dual) load_values<VEC>(b[q], z_up, false, r * N + n);
       }
     }
-    dz[r * ld + n] = f2bf_bits(d);
-    if (dual) dz[r * ld + Np + n] = f2bf_bits(du);
-    s0 += d;
-    s1 += du;
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f(g[q][e], a[q][e], b[q][e]);
+    };
+    // g becomes dz and b becomes dz_up.
+    switch (act) {
+      case ACT_NONE: break;
+      case ACT_GELU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_GELU, zz); }); break;
+      case ACT_SILU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_SILU, zz); }); break;
+      default:
+        each([](float& d, float& zz, float& u) {
+          const float go = d;
+          d = go * activate_grad(ACT_SWIGLU, zz) * u;
+          u = go * activate(ACT_SWIGLU, zz);
+        });
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int64_t r = r0 + (q0 + q) * 4 + rg;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        s0[e] += g[q][e];
+        s1[e] += b[q][e];
+      }
+      if (n < Np && r < M) {
+        store_values<VEC>(dz + r * ld + n, g[q]);
+        if (dual) store_values<VEC>(dz + r * ld + Np + n, b[q]);
+      }
+    }
   }
-  if (part && n < N) {
-    float* p = part + (int64_t)blockIdx.y * (dual ? 2 : 1) * N;
-    p[n] = s0;
-    if (dual) p[N + n] = s1;
+  if (!part) return;
+  __shared__ float sums[4][2][64 * VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    sums[rg][0][(threadIdx.x & 63) * VEC + e] = s0[e];
+    sums[rg][1][(threadIdx.x & 63) * VEC + e] = s1[e];
+  }
+  __syncthreads();
+  const int mats = dual ? 2 : 1;
+  for (int c = threadIdx.x; c < mats * 64 * VEC; c += 256) {
+    const int m = c / (64 * VEC), x = c % (64 * VEC), col = blockIdx.x * 64 * VEC + x;
+    if (col < N)
+      part[((int64_t)blockIdx.y * mats + m) * N + col] =
+          (sums[0][m][x] + sums[1][m][x]) + (sums[2][m][x] + sums[3][m][x]);
   }
 }
 
-// Sums the blocks' column sums in order.
-__global__ __launch_bounds__(256) void bias_sum_kernel(const float* __restrict__ part, int64_t blocks, int N, int mats,
-                                                       float* __restrict__ d_bias, float* __restrict__ d_bias_up) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= mats * N) return;
-  float s = 0.f;
-  for (int64_t b = 0; b < blocks; ++b) s += part[b * mats * N + c];
-  float* o = c < N ? d_bias : d_bias_up;
-  if (o) o[c < N ? c : c - N] = s;
+// Column sums of dz_kernel's blocks: 64 columns a workgroup (of 256 threads or more), a quarter of the row blocks
+// each, added in order.
+struct BiasSums {
+  const float* part;
+  int64_t rows;  // row blocks
+  int N, mats;
+  float *d_bias, *d_bias_up;
+};
+__device__ __forceinline__ void bias_sum(char* smem, const BiasSums& b, int bid) {
+  float* sm = reinterpret_cast<float*>(smem);
+  const int c = bid * 64 + (threadIdx.x & 63), qr = threadIdx.x >> 6;
+  if (qr < 4) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t r0 = qr * b.rows / 4, r1 = (qr + 1) * b.rows / 4;
+    if (c < b.mats * b.N) {
+      int64_t r = r0;
+      for (; r + 4 <= r1; r += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += b.part[(r + e) * b.mats * b.N + c];
+      for (; r < r1; ++r) s[0] += b.part[r * b.mats * b.N + c];
+    }
+    sm[qr * 64 + (threadIdx.x & 63)] = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  __syncthreads();
+  if (qr == 0 && c < b.mats * b.N) {
+    float* o = c < b.N ? b.d_bias : b.d_bias_up;
+    if (o) o[c < b.N ? c : c - b.N] = (sm[threadIdx.x] + sm[64 + threadIdx.x]) + (sm[128 + threadIdx.x] + sm[192 + threadIdx.x]);
+  }
+}
+
+// The backward pass's products in one launch, so that the tiles of one fill the CUs that another leaves idle: the
+// weight gradients (both operands columns; jobs 0 .. nw - 1), the input gradient (rows, columns; the last job) and
+// the bias gradients (from workgroup bias_first on).
+struct BackwardJobs {
+  Job j[3];
+  int n, nw, bias_first;
+  BiasSums bias;
+};
+
+template <int KIND>
+__global__ __launch_bounds__(kKinds[KIND].nw * 64, KIND == 2 ? 3 : 2) void backward_kernel(BackwardJobs b) {
+  using TW = KindTile<KIND, true, true, 1>;
+  using TX = KindTile<KIND, false, true, 1>;
+  __shared__ __attribute__((aligned(1024))) char smem[TW::SMEM > TX::SMEM ? TW::SMEM : TX::SMEM];
+  if ((int)blockIdx.x >= b.bias_first) {
+    bias_sum(smem, b.bias, blockIdx.x - b.bias_first);
+    return;
+  }
+  int q = 0;
+  while (q + 1 < b.n && (int)blockIdx.x >= b.j[q + 1].first) ++q;
+  const int bid = blockIdx.x - b.j[q].first;
+  if (q < b.nw) run_job<KIND, true, true, 1>(smem, b.j[q], bid);
+  else run_job<KIND, false, true, 1>(smem, b.j[q], bid);
+}
+
+// Adds the slices of a job's tiles in order and applies its epilogue; one group of four outputs per thread.
+__device__ __forceinline__ void reduce_job(const Job& j, int bm, int bn, int nmat) {
+  const int n4 = (j.g.N + 3) / 4;
+  const int64_t o = blockIdx.x * 256ll + threadIdx.x;
+  if (j.S <= 1 || o >= j.g.M * n4) return;
+  const int64_t row = o / n4;
+  const int n = (int)(o - row * n4) * 4;
+  const int64_t tiles = (int64_t)j.g.mt * j.g.nt, size = (int64_t)bm * nmat * bn;
+  const float* p = j.part + (row / bm * j.g.nt + n / bn) * size + (row % bm) * (nmat * bn) + n % bn;
+  floatx4 v[1] = {*reinterpret_cast<const floatx4*>(p)}, u[1] = {{0.f, 0.f, 0.f, 0.f}};
+  if (nmat == 2) u[0] = *reinterpret_cast<const floatx4*>(p + bn);
+#pragma unroll 4
+  for (int q = 1; q < j.S; ++q) {
+    v[0] += *reinterpret_cast<const floatx4*>(p + q * tiles * size);
+    if (nmat == 2) u[0] += *reinterpret_cast<const floatx4*>(p + q * tiles * size + bn);
+  }
+  const int64_t row0 = blockIdx.x * 256ll / n4;  // the block's first row
+  const Sink sink(j.g.e, row0, 257, j.g.M, j.g.N);
+  finish<1>(sink, (int)(row - row0), 0, n, v, u, load_bias(j.g.e.bias, n, j.g.N), load_bias(j.g.e.bias_up, n, j.g.N));
+}
+__global__ __launch_bounds__(256) void reduce_kernel(Job j, int bm, int bn, int nmat) { reduce_job(j, bm, bn, nmat); }
+// All split jobs of a backward pass (blockIdx.y: the job).
+__global__ __launch_bounds__(256) void reduce_jobs_kernel(BackwardJobs b, int bm, int bn) {
+  reduce_job(b.j[blockIdx.y], bm, bn, 1);
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint32_t* p, int64_t words) {
@@ -570,24 +859,113 @@ __global__ __launch_bounds__(256) void zero_kernel(uint32_t* p, int64_t words) {
 int round_up(int v, int a) { return (v + a - 1) / a * a; }
 int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-template <int BM, int BN, bool A_COLS, bool B_COLS, int NMAT>
-hipError_t run_gemm(Gemm g, hipStream_t s) {
-  const int64_t mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
-  if (mt * nt > INT32_MAX) return hipErrorInvalidValue;
-  g.mt = (int)mt;
-  g.nt = (int)nt;
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, A_COLS, B_COLS, NMAT>), dim3((unsigned)(mt * nt)), dim3(waves(BM) * 64), 0, s, g);
-  return hipGetLastError();
+int stages(int64_t R) { return (int)((R + BK - 1) / BK); }
+
+// How a launch runs: its tile kind and, per product, the slices of the reduction.
+struct Size {
+  int64_t M;
+  int N, nk;
+};
+struct Plan {
+  int kind;
+  int S[3];
+  int64_t tiles[3];
+  size_t part_bytes[3];  // fp32 sums of a split product
+};
+
+// CUs of the current device (256 if it cannot be asked), looked up once per device.
+int device_cus() {
+  static std::atomic<int> known[64];
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  cus = known[dev].load(std::memory_order_relaxed);
+  if (cus > 0) return cus;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) return 256;
+  known[dev].store(cus, std::memory_order_relaxed);
+  return cus;
 }
 
-int stages(int64_t R) { return (int)((R + BK - 1) / BK); }
+constexpr int kMaxSlices = 16;
+
+// Picks the tile kind and slices with the least estimated time: a CU runs its share of the launch's workgroups,
+// per_cu of them at a time, a stage of r workgroups taking max(latency, r * rate), plus a fixed cost per workgroup;
+// a split adds the second launch and its traffic.
+Plan make_plan(const Size* z, int n, int nmat, bool split) {
+  constexpr double kRate[] = {1.45, 0.45, 0.26};     // us a stage and workgroup, CU full
+  constexpr double kLatency[] = {1.2, 0.6, 0.5};     // us a stage, at least
+  constexpr double kFixed[] = {9.0, 5.0, 4.0};       // us a workgroup: first stage's latency and epilogue
+  constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
+  const int cus = device_cus();
+  Plan best{};
+  double best_t = 1e30;
+  for (int kind = 0; kind < kNumKinds; ++kind) {
+    const int bm = kKinds[kind].bm, bn = kKinds[kind].bn / nmat, occ = kKinds[kind].per_cu;
+    for (int S = 1; S <= (split ? kMaxSlices : 1); ++S) {
+      Plan p{};
+      p.kind = kind;
+      double blocks = 0, work = 0, bytes = 0;
+      int longest = 0;
+      bool any = false;
+      for (int q = 0; q < n; ++q) {
+        p.tiles[q] = ((z[q].M + bm - 1) / bm) * ((z[q].N + bn - 1) / bn);
+        const int most = z[q].nk / 4 < 1 ? 1 : z[q].nk / 4;  // at least four stages a slice
+        p.S[q] = S < most ? S : most;
+        any |= p.S[q] == S;
+        const int per = (z[q].nk + p.S[q] - 1) / p.S[q];
+        blocks += (double)p.tiles[q] * p.S[q];
+        work += (double)p.tiles[q] * p.S[q] * per;
+        longest = per > longest ? per : longest;
+        if (p.S[q] > 1) {
+          p.part_bytes[q] = (size_t)p.tiles[q] * p.S[q] * bm * nmat * bn * 4;
+          bytes += 2.0 * p.part_bytes[q];
+        }
+      }
+      if (!any || blocks > 2.0e9) continue;
+      const double per_block = work / blocks;          // stages of an average workgroup
+      int64_t left = (int64_t)((blocks + cus - 1) / cus);  // workgroups of the fullest CU
+      double t = 0;
+      while (left > 0) {
+        const int r = left < occ ? (int)left : occ;
+        const double stage = kLatency[kind] > r * kRate[kind] ? kLatency[kind] : r * kRate[kind];
+        t += (t == 0 ? longest : per_block) * stage + kFixed[kind];
+        left -= r;
+      }
+      if (bytes > 0) t += kSecond + bytes / kBytes;
+      if (t < best_t) {
+        best_t = t;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+size_t part_bytes(const Plan& p, int n) {
+  size_t b = 0;
+  for (int q = 0; q < n; ++q) b += p.part_bytes[q];
+  return b;
+}
+
+void set_tiles(Gemm& g, int kind, int nmat) {
+  g.mt = (int)((g.M + kKinds[kind].bm - 1) / kKinds[kind].bm);
+  g.nt = (g.N + kKinds[kind].bn / nmat - 1) / (kKinds[kind].bn / nmat);
+}
+
+unsigned reduce_blocks(const Job& j) { return (unsigned)((j.g.M * ((j.g.N + 3) / 4) + 255) / 256); }
+
+constexpr int kSkinnyRows = 16;  // up to here moe_linear streams the weights
 
 }  // namespace
 
-size_t linear_ws_bytes(int64_t, int, int, int) { return 0; }
+size_t linear_ws_bytes(int64_t M, int N, int K, int act) {
+  if (M <= kSkinnyRows) return 0;
+  const Size z{M, N, stages(K)};
+  return part_bytes(make_plan(&z, 1, act == ACT_SWIGLU ? 2 : 1, true), 1);
+}
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
-  Gemm g{};
+  Job j{};
+  Gemm& g = j.g;
   g.a = {a.x, nullptr, a.K, a.M, a.K};
   g.b = {a.w, nullptr, a.K, a.N, a.K};
   g.b_up = {a.w_up, nullptr, a.K, a.N, a.K};
@@ -595,20 +973,68 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   g.N = a.N;
   g.nk = g.seg = stages(a.K);
   g.e = {a.bias, a.bias_up, a.residual, a.out, a.z, a.z_up, a.act, a.out_f32};
-  const bool big = a.M >= 1024 && a.N >= 1024;
-  if (a.act == ACT_SWIGLU) return big ? run_gemm<256, 128, false, false, 2>(g, s) : run_gemm<128, 64, false, false, 2>(g, s);
-  return big ? run_gemm<256, 256, false, false, 1>(g, s) : run_gemm<128, 128, false, false, 1>(g, s);
+  const bool dual = a.act == ACT_SWIGLU;
+  const int nmat = dual ? 2 : 1;
+  if (a.M <= kSkinnyRows) {
+    if (dual) hipLaunchKernelGGL((skinny_kernel<true, 8, 2>), dim3((a.N + 7) / 8), dim3(512), 0, s, g);
+    else hipLaunchKernelGGL((skinny_kernel<false, 8, 2>), dim3((a.N + 15) / 16), dim3(512), 0, s, g);
+    return hipGetLastError();
+  }
+  const Size z{a.M, a.N, g.nk};
+  const Plan p = make_plan(&z, 1, nmat, a.ws != nullptr);
+  if (p.tiles[0] < 1) return hipErrorInvalidValue;
+  set_tiles(g, p.kind, nmat);
+  j.S = p.S[0];
+  j.part = static_cast<float*>(a.ws);
+  const dim3 grid((unsigned)(p.tiles[0] * j.S)), block(kKinds[p.kind].nw * 64);
+#define MOE_FORWARD(KIND_)                                                             \
+  do {                                                                                 \
+    if (dual) hipLaunchKernelGGL((forward_kernel<KIND_, 2>), grid, block, 0, s, j);    \
+    else hipLaunchKernelGGL((forward_kernel<KIND_, 1>), grid, block, 0, s, j);         \
+  } while (0)
+  if (p.kind == 0) MOE_FORWARD(0);
+  else if (p.kind == 1) MOE_FORWARD(1);
+  else MOE_FORWARD(2);
+#undef MOE_FORWARD
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && j.S > 1) {
+    hipLaunchKernelGGL(reduce_kernel, dim3(reduce_blocks(j)), dim3(256), 0, s, j, kKinds[p.kind].bm,
+                       kKinds[p.kind].bn / nmat, nmat);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
-// Workspace of the backward pass: dz [M, ld] bf16, then the bias gradients' block sums.
+// Workspace of the backward pass: dz [M, ld] bf16, the bias gradients' block sums, the split products' sums.
+struct BackwardLayout {
+  int mats, Np, ld;
+  int64_t blocks;  // row blocks of dz_kernel
+  size_t sums, parts, total;
+  Plan plan;
+};
+
+// Products in the order of the launch: the weight gradients, then the input gradient.
+static BackwardLayout backward_layout(int64_t M, int N, int K, int act) {
+  BackwardLayout l{};
+  l.mats = act == ACT_SWIGLU ? 2 : 1;
+  l.Np = round_up(N, BK);
+  l.ld = l.mats * l.Np;
+  l.blocks = (M + kDzRows - 1) / kDzRows;
+  l.sums = (size_t)align_up(M * l.ld * 2, 256);
+  l.parts = l.sums + (size_t)align_up(l.blocks * l.mats * N * 4, 256);
+  Size z[3];
+  for (int m = 0; m < l.mats; ++m) z[m] = {N, K, stages(M)};
+  z[l.mats] = {M, K, l.mats * stages(N)};
+  l.plan = make_plan(z, l.mats + 1, 1, true);
+  l.total = l.parts + part_bytes(l.plan, l.mats + 1);
+  return l;
+}
+
 size_t linear_backward_ws_bytes(int64_t M, int N, int K, int act) {
-  const int mats = act == ACT_SWIGLU ? 2 : 1;
-  const int64_t ld = (int64_t)mats * round_up(N, BK);
-  return (size_t)(align_up(M * ld * 2, 256) + align_up((M + kDzRows - 1) / kDzRows * mats * N * 4, 256));
+  return M == 0 ? 0 : backward_layout(M, N, K, act).total;
 }
 
 hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
-  const int mats = a.act == ACT_SWIGLU ? 2 : 1;
   if (a.M == 0) {
     const int64_t n = (int64_t)a.N * a.K / 2;  // words of a weight gradient (K % 8 == 0)
     struct { void* p; int64_t words; } z[] = {{a.d_w, n}, {a.d_w_up, n}, {a.d_bias, a.N}, {a.d_bias_up, a.N}};
@@ -621,29 +1047,57 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
       }
     return e;
   }
-  const int Np = round_up(a.N, BK), ld = mats * Np;
+  const BackwardLayout l = backward_layout(a.M, a.N, a.K, a.act);
+  const int mats = l.mats, Np = l.Np, ld = l.ld;
   uint16_t* dz = static_cast<uint16_t*>(a.ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + align_up(a.M * ld * 2, 256));
-  const int64_t blocks = (a.M + kDzRows - 1) / kDzRows;
-  const bool sums = a.d_bias || a.d_bias_up;
-  // At most 65535 block rows per launch.
-  constexpr int64_t kMaxBlocks = 65535;
-  for (int64_t b = 0; b < blocks; b += kMaxBlocks) {
-    const int64_t nb = blocks - b < kMaxBlocks ? blocks - b : kMaxBlocks, r = b * kDzRows;
-    const int64_t rows = a.M - r;
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(a.ws) + l.sums);
+  char* parts = static_cast<char*>(a.ws) + l.parts;
+  const bool bias = a.d_bias || a.d_bias_up;
+  constexpr int64_t kMaxBlocks = 65535;  // row blocks per launch
+  for (int64_t b = 0; b < l.blocks; b += kMaxBlocks) {
+    const int64_t nb = l.blocks - b < kMaxBlocks ? l.blocks - b : kMaxBlocks, r = b * kDzRows;
     const char* d_out = static_cast<const char*>(a.d_out) + r * a.N * (a.out_f32 ? 4 : 2);
-    hipLaunchKernelGGL(dz_kernel, dim3((Np + 255) / 256, (unsigned)nb), dim3(256), 0, s, d_out, a.out_f32,
-                       a.z ? a.z + r * a.N : nullptr, a.z_up ? a.z_up + r * a.N : nullptr, a.act, rows, a.N, Np, ld,
-                       dz + r * ld, sums ? part + b * mats * a.N : nullptr);
+    const uint16_t *z = a.z ? a.z + r * a.N : nullptr, *z_up = a.z_up ? a.z_up + r * a.N : nullptr;
+    float* part = bias ? sums + b * mats * a.N : nullptr;
+    if (a.N % 8 == 0)
+      hipLaunchKernelGGL(dz_kernel<8>, dim3((Np + 511) / 512, (unsigned)nb), dim3(256), 0, s, d_out, a.out_f32, z, z_up,
+                         a.act, a.M - r, a.N, Np, ld, dz + r * ld, part);
+    else
+      hipLaunchKernelGGL(dz_kernel<1>, dim3((Np + 63) / 64, (unsigned)nb), dim3(256), 0, s, d_out, a.out_f32, z, z_up,
+                         a.act, a.M - r, a.N, Np, ld, dz + r * ld, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (sums)
-    hipLaunchKernelGGL(bias_sum_kernel, dim3((mats * a.N + 255) / 256), dim3(256), 0, s, part, blocks, a.N, mats,
-                       a.d_bias, a.d_bias_up);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  Gemm g{};
-  g.e.act = ACT_NONE;
+
+  BackwardJobs jobs{};
+  int64_t blocks = 0;
+  auto add = [&](const Gemm& g, int q) {  // product q of the plan
+    Job& j = jobs.j[jobs.n++];
+    j.g = g;
+    j.g.e.act = ACT_NONE;
+    set_tiles(j.g, l.plan.kind, 1);
+    j.S = l.plan.S[q];
+    j.first = (int)blocks;
+    size_t off = 0;
+    for (int i = 0; i < q; ++i) off += l.plan.part_bytes[i];
+    j.part = reinterpret_cast<float*>(parts + off);
+    blocks += l.plan.tiles[q] * j.S;
+  };
+  for (int m = 0; m < mats; ++m) {
+    uint16_t* d_w = m ? a.d_w_up : a.d_w;
+    if (!d_w) continue;
+    Gemm g{};
+    g.a = {dz + m * Np, nullptr, ld, Np, a.M};
+    g.b = {a.x, nullptr, a.K, a.K, a.M};
+    g.M = a.N;
+    g.N = a.K;
+    g.nk = g.seg = stages(a.M);
+    g.e.out = d_w;
+    add(g, m);
+  }
+  jobs.nw = jobs.n;
   if (a.d_x) {
+    Gemm g{};
     g.a = {dz, nullptr, ld, a.M, ld};
     g.b = {a.w, a.w_up, a.K, a.K, a.N};
     g.M = a.M;
@@ -651,24 +1105,27 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
     g.seg = stages(a.N);
     g.nk = mats * g.seg;
     g.e.out = a.d_x;
-    const bool big = a.M >= 1024 && a.K >= 1024;
-    e = big ? run_gemm<256, 256, false, true, 1>(g, s) : run_gemm<128, 128, false, true, 1>(g, s);
-    if (e != hipSuccess) return e;
+    add(g, mats);
   }
-  for (int m = 0; m < mats; ++m) {
-    uint16_t* d_w = m ? a.d_w_up : a.d_w;
-    if (!d_w) continue;
-    g.a = {dz + m * Np, nullptr, ld, Np, a.M};
-    g.b = {a.x, nullptr, a.K, a.K, a.M};
-    g.M = a.N;
-    g.N = a.K;
-    g.nk = g.seg = stages(a.M);
-    g.e.out = d_w;
-    const bool big = a.N >= 1024 && a.K >= 1024;
-    e = big ? run_gemm<256, 256, true, true, 1>(g, s) : run_gemm<128, 128, true, true, 1>(g, s);
-    if (e != hipSuccess) return e;
+  jobs.bias_first = (int)blocks;
+  jobs.bias = {sums, l.blocks, a.N, mats, a.d_bias, a.d_bias_up};
+  if (bias) blocks += (mats * (int64_t)a.N + 63) / 64;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const Kind& kind = kKinds[l.plan.kind];
+  const dim3 grid((unsigned)blocks), block(kind.nw * 64);
+  if (l.plan.kind == 0) hipLaunchKernelGGL(backward_kernel<0>, grid, block, 0, s, jobs);
+  else if (l.plan.kind == 1) hipLaunchKernelGGL(backward_kernel<1>, grid, block, 0, s, jobs);
+  else hipLaunchKernelGGL(backward_kernel<2>, grid, block, 0, s, jobs);
+  hipError_t e = hipGetLastError();
+  unsigned most = 0;
+  for (int q = 0; q < jobs.n; ++q)
+    if (jobs.j[q].S > 1 && reduce_blocks(jobs.j[q]) > most) most = reduce_blocks(jobs.j[q]);
+  if (e == hipSuccess && most > 0) {
+    hipLaunchKernelGGL(reduce_jobs_kernel, dim3(most, jobs.n), dim3(256), 0, s, jobs, kind.bm, kind.bn);
+    e = hipGetLastError();
   }
-  return hipSuccess;
+  return e;
 }
 
 }  // namespace moe
