@@ -170,76 +170,87 @@ struct Sink {
   }
 };
 
-// Four values at element offset `at` (kOut: nowhere) of row-major data of type bf16; cnt of them exist.
-__device__ __forceinline__ void put_bf16(const Sink& k, __amdgpu_buffer_rsrc_t r, uint32_t at, int cnt, floatx4 x) {
+// Four values of one row, cnt of which exist (<= 0: none), at byte offset `at` of row-major data of ES-byte values.
+// VEC: rows are whole groups of four, one access each; else value by value.
+template <bool VEC, int ES>
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, int cnt, floatx4 x) {
   const u32x2 h = pack4(x);
-  if (k.vec) {
-    __builtin_amdgcn_raw_buffer_store_b64(h, r, at == kOut ? kOut : at * 2, 0, 0);
+  if constexpr (VEC) {
+    const uint32_t o = cnt > 0 ? at : kOut;
+    if constexpr (ES == 2) __builtin_amdgcn_raw_buffer_store_b64(h, r, o, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, o, 0, 0);
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(h[q >> 1] >> (16 * (q & 1))), r, at == kOut || q >= cnt ? kOut : (at + q) * 2, 0, 0);
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t o = q < cnt ? at + q * ES : kOut;
+      const float v = x[q];  // (a vector element itself is no object to bit_cast)
+      if constexpr (ES == 2) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(h[q >> 1] >> (16 * (q & 1))), r, o, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, o, 0, 0);
+    }
   }
+}
+template <bool VEC, int ES>
+__device__ __forceinline__ floatx4 get4(__amdgpu_buffer_rsrc_t r, uint32_t at, int cnt) {
+  floatx4 v;
+  if constexpr (VEC) {
+    const uint32_t o = cnt > 0 ? at : kOut;
+    if constexpr (ES == 2) {
+      const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0);
+      v = floatx4{bf2f((uint16_t)h[0]), bf2f((uint16_t)(h[0] >> 16)), bf2f((uint16_t)h[1]), bf2f((uint16_t)(h[1] >> 16))};
+    } else {
+      v = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t o = q < cnt ? at + q * ES : kOut;
+      v[q] = ES == 2 ? bf2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0))
+                     : __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
+    }
+  }
+  return v;
 }
 
 // The epilogue of NV rows, r + q * step of the sink, in the four columns from n (a multiple of 4): g and u hold the
-// products.  All of the rows' residuals are loaded before the first store.  Branches are few and uniform: code that
-// runs once per tile is paid for by its instruction fetches.
-template <int NV>
+// products.  All of the rows' residuals are loaded before the first store.
+template <bool VEC, int ES, int NV>
 __device__ __forceinline__ void finish(const Sink& k, int r, int step, int n, floatx4 (&g)[NV], floatx4 (&u)[NV],
                                        floatx4 bias, floatx4 bias_up) {
   const int cnt = k.N - n;  // columns that exist
+  const uint32_t at = (uint32_t)(r * k.N + n), next = (uint32_t)(step * k.N);  // elements
   floatx4 res[NV];
-  uint32_t at[NV];
 #pragma unroll
   for (int q = 0; q < NV; ++q) {
-    at[q] = cnt > 0 ? (uint32_t)((r + q * step) * k.N + n) : kOut;
     res[q] = floatx4{0.f, 0.f, 0.f, 0.f};
     g[q] += bias;
     u[q] += bias_up;
   }
-  if (k.has_res) {
+  if (k.has_res)
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      if (!k.vec) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool in = cnt > e;
-          res[q][e] = k.f32 ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(k.res, in ? (at[q] + e) * 4 : kOut, 0, 0))
-                            : bf2f((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(k.res, in ? (at[q] + e) * 2 : kOut, 0, 0));
-        }
-      } else if (k.f32) {
-        res[q] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(k.res, at[q] == kOut ? kOut : at[q] * 4, 0, 0));
-      } else {
-        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(k.res, at[q] == kOut ? kOut : at[q] * 2, 0, 0);
-        res[q] = floatx4{bf2f((uint16_t)h[0]), bf2f((uint16_t)(h[0] >> 16)), bf2f((uint16_t)h[1]), bf2f((uint16_t)(h[1] >> 16))};
-      }
-    }
-  }
+    for (int q = 0; q < NV; ++q) res[q] = get4<VEC, ES>(k.res, (at + q * next) * ES, cnt);
   if (k.has_z)
 #pragma unroll
-    for (int q = 0; q < NV; ++q) put_bf16(k, k.z, at[q], cnt, g[q]);
+    for (int q = 0; q < NV; ++q) put4<VEC, 2>(k.z, (at + q * next) * 2, cnt, g[q]);
   if (k.has_zu)
 #pragma unroll
-    for (int q = 0; q < NV; ++q) put_bf16(k, k.z_up, at[q], cnt, u[q]);
+    for (int q = 0; q < NV; ++q) put4<VEC, 2>(k.z_up, (at + q * next) * 2, cnt, u[q]);
   activate_all<NV>(k.act, g, u);
 #pragma unroll
-  for (int q = 0; q < NV; ++q) g[q] += res[q];
-  if (!k.f32) {
-#pragma unroll
-    for (int q = 0; q < NV; ++q) put_bf16(k, k.out, at[q], cnt, g[q]);
-  } else if (k.vec) {
-#pragma unroll
-    for (int q = 0; q < NV; ++q)
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, g[q]), k.out, at[q] == kOut ? kOut : at[q] * 4, 0, 0);
+  for (int q = 0; q < NV; ++q) put4<VEC, ES>(k.out, (at + q * next) * ES, cnt, g[q] + res[q]);
+}
+
+// Calls f(VEC, ES) with the sink's access width and output size: one uniform choice ahead of a loop, because code
+// that runs once per tile is paid for by its branches and instruction fetches.
+template <typename F>
+__device__ __forceinline__ void with_layout(const Sink& k, F f) {
+  using std::bool_constant;
+  using std::integral_constant;
+  if (k.vec) {
+    if (k.f32) f(bool_constant<true>{}, integral_constant<int, 4>{});
+    else f(bool_constant<true>{}, integral_constant<int, 2>{});
   } else {
-#pragma unroll
-    for (int q = 0; q < NV; ++q)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = g[q][e];  // (a vector element itself is not an object to bit_cast)
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), k.out, cnt > e ? (at[q] + e) * 4 : kOut, 0, 0);
-      }
+    if (k.f32) f(bool_constant<false>{}, integral_constant<int, 4>{});
+    else f(bool_constant<false>{}, integral_constant<int, 2>{});
   }
 }
 
@@ -492,29 +503,38 @@ struct Tile {
       }
       wait_lgkm0();
       ring_barrier();
+      // The 32 rows of the upper and of the lower half of the tile, NV rows of this thread's columns at a time.
+      auto rows = [&](auto f) {
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // the 32 rows of the upper and lower half of the tile
+        for (int h = 0; h < 2; ++h)
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += NV * STEP) {
-          floatx4 v[NV], u[NV];
-          const int rt = r0 + threadIdx.x / C4;
-#pragma unroll
-          for (int r = 0; r < NV; ++r) {
-            const float* p = sm + (h * 32 + rt + r * STEP) * PITCH + n;
-            v[r] = *reinterpret_cast<const floatx4*>(p);
-            u[r] = NMAT == 2 ? *reinterpret_cast<const floatx4*>(p + BN) : floatx4{0.f, 0.f, 0.f, 0.f};
-          }
-          if (part) {
+          for (int r0 = 0; r0 < 32; r0 += NV * STEP) {
+            floatx4 v[NV], u[NV];
+            const int rt = r0 + threadIdx.x / C4;
 #pragma unroll
             for (int r = 0; r < NV; ++r) {
-              float* o = part + (int64_t)(h * (BM / 2) + i * 32 + rt + r * STEP) * (NMAT * BN) + n;
-              *reinterpret_cast<floatx4*>(o) = v[r];
-              if (NMAT == 2) *reinterpret_cast<floatx4*>(o + BN) = u[r];
+              const float* p = sm + (h * 32 + rt + r * STEP) * PITCH + n;
+              v[r] = *reinterpret_cast<const floatx4*>(p);
+              u[r] = NMAT == 2 ? *reinterpret_cast<const floatx4*>(p + BN) : floatx4{0.f, 0.f, 0.f, 0.f};
             }
-          } else {
-            finish<NV>(sink, h * (BM / 2) + i * 32 + rt, STEP, n0 + n, v, u, bias, bias_up);
+            f(h * (BM / 2) + i * 32 + rt, v, u);
           }
-        }
+      };
+      if (part) {
+        rows([&](int r, floatx4 (&v)[NV], floatx4 (&u)[NV]) {
+#pragma unroll
+          for (int q = 0; q < NV; ++q) {
+            float* o = part + (int64_t)(r + q * STEP) * (NMAT * BN) + n;
+            *reinterpret_cast<floatx4*>(o) = v[q];
+            if (NMAT == 2) *reinterpret_cast<floatx4*>(o + BN) = u[q];
+          }
+        });
+      } else {
+        with_layout(sink, [&](auto vec, auto es) {
+          rows([&](int r, floatx4 (&v)[NV], floatx4 (&u)[NV]) {
+            finish<decltype(vec)::value, decltype(es)::value, NV>(sink, r, STEP, n0 + n, v, u, bias, bias_up);
+          });
+        });
       }
     }
   }
@@ -647,7 +667,10 @@ __global__ __launch_bounds__(NK * 64) void skinny_kernel(Gemm g) {
     }
     const int n = n0 + (lane >> 4) * 4;
     const Sink sink(g.e, 0, 16, g.M, g.N);
-    finish<1>(sink, lane & 15, 0, n, v, u, load_bias(g.e.bias, n, g.N), load_bias(g.e.bias_up, n, g.N));
+    with_layout(sink, [&](auto vec, auto es) {
+      finish<decltype(vec)::value, decltype(es)::value, 1>(sink, lane & 15, 0, n, v, u, load_bias(g.e.bias, n, g.N),
+                                                           load_bias(g.e.bias_up, n, g.N));
+    });
   }
 }
 
@@ -844,7 +867,10 @@ __device__ __forceinline__ void reduce_job(const Job& j, int bm, int bn, int nma
   }
   const int64_t row0 = blockIdx.x * 256ll / n4;  // the block's first row
   const Sink sink(j.g.e, row0, 257, j.g.M, j.g.N);
-  finish<1>(sink, (int)(row - row0), 0, n, v, u, load_bias(j.g.e.bias, n, j.g.N), load_bias(j.g.e.bias_up, n, j.g.N));
+  with_layout(sink, [&](auto vec, auto es) {
+    finish<decltype(vec)::value, decltype(es)::value, 1>(sink, (int)(row - row0), 0, n, v, u, load_bias(j.g.e.bias, n, j.g.N),
+                                                         load_bias(j.g.e.bias_up, n, j.g.N));
+  });
 }
 __global__ __launch_bounds__(256) void reduce_kernel(Job j, int bm, int bn, int nmat) { reduce_job(j, bm, bn, nmat); }
 // All split jobs of a backward pass (blockIdx.y: the job).
@@ -891,9 +917,9 @@ constexpr int kMaxSlices = 16;
 // per_cu of them at a time, a stage of r workgroups taking max(latency, r * rate), plus a fixed cost per workgroup;
 // a split adds the second launch and its traffic.
 Plan make_plan(const Size* z, int n, int nmat, bool split) {
-  constexpr double kRate[] = {1.45, 0.45, 0.26};     // us a stage and workgroup, CU full
-  constexpr double kLatency[] = {1.2, 0.6, 0.5};     // us a stage, at least
-  constexpr double kFixed[] = {9.0, 5.0, 4.0};       // us a workgroup: first stage's latency and epilogue
+  constexpr double kRate[] = {1.5, 0.53, 0.32};      // us a stage and workgroup, CU full
+  constexpr double kLatency[] = {1.15, 0.58, 0.42};  // us a stage, at least
+  constexpr double kFixed[] = {9.0, 5.0, 3.5};       // us a workgroup: first stage's latency and epilogue
   constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
   const int cus = device_cus();
   Plan best{};
