@@ -11,62 +11,12 @@
 // and sums of two scores are 64-bit: two of them that differ by less than an
 // fp32 rounding are met every few thousand tokens.
 //
-// One wavefront per token; lane l holds experts l, l + 64, ...
 #include "operators.h"
 
 #include <float.h>
 
 namespace moe {
 namespace {
-
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
-}
-__device__ __forceinline__ float wave_sum_f(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
-__device__ __forceinline__ double wave_max_d(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmax(v, __shfl_xor(v, off));
-  return v;
-}
-__device__ __forceinline__ double wave_sum_d(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
-__device__ __forceinline__ double sigmoid_d(double x) { return 1.0 / (1.0 + exp(-x)); }
-__device__ __forceinline__ int wave_min_i(int v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = min(v, __shfl_xor(v, off));
-  return v;
-}
-
-// e / Eg for e < 1024: magic = ceil(2^22 / Eg), exact because e * Eg < 2^22.
-__device__ __forceinline__ int group_of(int e, uint32_t magic) { return (int)(((uint32_t)e * magic) >> 22); }
-
-// A row's gate weights.  Lane j < k holds slot j's id (-1: empty) and logit; m is the row's largest available
-// logit and z the sum of e^(l - m) over the available experts (used by the plain softmax only).
-// Renormalised, both scores are scaled by a common factor that keeps the largest at least 1/2 before the sum:
-// softmax by e^-(largest chosen logit), sigmoid(l) = e^min(l, 0) / (1 + e^-|l|) by e^-min(largest chosen logit, 0).
-__device__ __forceinline__ float gate_weight(int lane, int k, int id, float l, float m, float z, bool sigmoid,
-                                             bool renormalize, float scale) {
-  const bool has = lane < k && id >= 0;
-  float s = 0.f;
-  if (renormalize) {
-    float top = wave_max_f(has ? l : -FLT_MAX);
-    if (sigmoid) top = fminf(top, 0.f);
-    if (has) s = sigmoid ? expf(fminf(l, 0.f) - top) / (1.f + expf(-fabsf(l))) : expf(l - top);
-    const float sum = wave_sum_f(s);
-    return has ? scale * (s / sum) : 0.f;
-  }
-  if (has) s = sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - m) / z;
-  return scale * s;
-}
 
 constexpr int kTokens = 4;  // wavefronts per block
 
@@ -77,172 +27,78 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One token by one wavefront, with 64-bit keys throughout; lane l holds experts l, l + 64, ...  sk: E doubles of LDS
-// of this wavefront's own (used when groups are dropped).
-template <int PL>
-__device__ void route_exact(const RouteArgs& a, int64_t t, int lane, uint32_t magic, double* sk) {
-  const int E = a.E;
-  float l[PL];
-  double key[PL];
-  bool ok[PL];
-  float m = -FLT_MAX;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + i * kWave;
-    const float v = (e < E) ? a.logits[t * E + e] : -INFINITY;
-    const float b = (a.bias && e < E) ? a.bias[e] : 0.f;
-    ok[i] = v > -INFINITY && b > -INFINITY;  // false for NaN
-    l[i] = fminf(v, FLT_MAX);
-    if (ok[i]) m = fmaxf(m, l[i]);
-  }
-  m = wave_max_f(m);
-  float z = 1.f;
-  if (!a.sigmoid && !a.renormalize) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s += ok[i] ? expf(l[i] - m) : 0.f;
-    z = wave_sum_f(s);
-  }
-  if (!a.bias) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) key[i] = l[i];
-  } else {
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      key[i] = ok[i] ? (a.sigmoid ? sigmoid_d(l[i]) : exp((double)l[i] - (double)m)) : 0.0;
-      s += key[i];
-    }
-    if (!a.sigmoid) {
-      const double zz = wave_sum_d(s);
-#pragma unroll
-      for (int i = 0; i < PL; ++i) key[i] /= zz;
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = lane + i * kWave;
-      if (ok[i]) key[i] += (double)fminf(a.bias[e], FLT_MAX);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < PL; ++i)
-    if (!ok[i]) key[i] = -INFINITY;
-
-  if (a.n_group > 1 && a.topk_group < a.n_group) {
-    const int Eg = E / a.n_group;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + i * kWave < E) sk[lane + i * kWave] = key[i];
-    wave_lds_order();
-    double g = -INFINITY, g2 = -INFINITY;
-    if (lane < a.n_group)
-      for (int q = 0; q < Eg; ++q) {
-        const double v = sk[lane * Eg + q];
-        if (v > g) {
-          g2 = g;
-          g = v;
-        } else if (v > g2) {
-          g2 = v;
-        }
-      }
-    if (a.group_top == 2 && g > -INFINITY) {
-      if (!a.bias) {  // the two best logits' scores (softmax: up to the common denominator)
-        g = a.sigmoid ? sigmoid_d(g) : exp(g - (double)m);
-        if (g2 > -INFINITY) g2 = a.sigmoid ? sigmoid_d(g2) : exp(g2 - (double)m);
-      }
-      if (g2 > -INFINITY) g += g2;
-    }
-    int ahead = 0;  // groups ranked before this lane's
-    for (int h = 0; h < a.n_group; ++h) {
-      const double o = __shfl(g, h);
-      ahead += (o > g || (o == g && h < lane)) ? 1 : 0;
-    }
-    const unsigned long long kept = __ballot(lane < a.n_group && ahead < a.topk_group);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = lane + i * kWave;
-      if (e < E && !((kept >> group_of(e, magic)) & 1)) key[i] = -INFINITY;
-    }
-  }
-
-  int sel = -1;
-  float sl = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    double bv = -INFINITY;
-    int bi = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (key[i] > bv) {
-        bv = key[i];
-        bi = lane + i * kWave;
-      }
-    const double top = wave_max_d(bv);
-    if (top == -INFINITY) break;  // wave-uniform: no expert is left
-    bi = wave_min_i(bv == top ? bi : 0x7fffffff);
-    float lw = 0.f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + i * kWave == bi) {
-        key[i] = -INFINITY;
-        lw = l[i];
-      }
-    lw = __shfl(lw, bi & 63);
-    if (lane == j) {
-      sel = bi;
-      sl = lw;
-    }
-  }
-  const float w = gate_weight(lane, a.k, sel, sl, m, z, a.sigmoid, a.renormalize, a.scale);
-  if (lane < a.k) {
-    a.idx[t * a.k + lane] = sel;
-    a.w[t * a.k + lane] = w;
-  }
-}
-
-template <int PL>
-__global__ __launch_bounds__(kTokens* kWave) void route_exact_kernel(RouteArgs a, uint32_t magic) {
-  extern __shared__ double s_key[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + wv;
-  if (t < a.T) route_exact<PL>(a, t, lane, magic, s_key + wv * a.E);  // wave-uniform
-}
-
-// ---------------------------------------------------------------------------
-// fp32 keys with a check: LT lanes per token, 64 / LT tokens per wavefront
-// ---------------------------------------------------------------------------
-// Reductions over the LT lanes of a token, result in every lane: the four steps inside a row of 16 lanes by DPP
-// (quad swaps, half mirror, mirror), the rows of a 64-lane token by readlane.
+// Values of another lane: by DPP inside a row of 16 lanes, or of a given lane.
 template <int CTRL>
-__device__ __forceinline__ float dppf(float v) {
-  const int x = __builtin_bit_cast(int, v);
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false));
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ float lanef(float v, int l) {
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(int, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp<CTRL>((int)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float of_lane(float v, int l) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
 }
-template <int LT, typename F>
-__device__ __forceinline__ float reduce(float v, F f) {
-  v = f(v, dppf<0xB1>(v));
-  v = f(v, dppf<0x4E>(v));
-  v = f(v, dppf<0x141>(v));
-  v = f(v, dppf<0x140>(v));
-  if constexpr (LT == 64) v = f(f(lanef(v, 0), lanef(v, 16)), f(lanef(v, 32), lanef(v, 48)));
+__device__ __forceinline__ double of_lane(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Reductions over the LT lanes of a token, result in every lane: four steps inside a row of 16 lanes (quad swaps,
+// half mirror, mirror), then the four rows of a 64-lane token.
+template <int LT, typename K, typename F>
+__device__ __forceinline__ K reduce(K v, F f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  if constexpr (LT == 64) v = f(f(of_lane(v, 0), of_lane(v, 16)), f(of_lane(v, 32), of_lane(v, 48)));
   return v;
 }
-template <int LT>
-__device__ __forceinline__ float max_of(float v) {
-  return reduce<LT>(v, [](float a, float b) { return fmaxf(a, b); });
+__device__ __forceinline__ float max2(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double max2(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float min2(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double min2(double a, double b) { return fmin(a, b); }
+template <int LT, typename K>
+__device__ __forceinline__ K max_of(K v) {
+  return reduce<LT>(v, [](K a, K b) { return max2(a, b); });
 }
-template <int LT>
-__device__ __forceinline__ float sum_of(float v) {
-  return reduce<LT>(v, [](float a, float b) { return a + b; });
+template <int LT, typename K>
+__device__ __forceinline__ K sum_of(K v) {
+  return reduce<LT>(v, [](K a, K b) { return a + b; });
 }
 
-// 1 / (1 + e^-z) and e^z with the hardware exp2 and reciprocal (about 1 ulp each).
-__device__ __forceinline__ float exp_fast(float z) { return __builtin_amdgcn_exp2f(z * 1.4426950408889634f); }
-__device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-z)); }
+// e^z from the hardware exp2, with the rounding of z / ln 2 carried along: about 2 ulp whatever z.
+__device__ __forceinline__ float exp_of(float z) {
+  z = __builtin_amdgcn_fmed3f(z, -200.f, 100.f);  // (0 and infinity already)
+  const float t = z * 1.4426950408889634f;
+  return __builtin_amdgcn_exp2f(t) * fmaf(fmaf(z, 1.4426950408889634f, -t), 0.69314718055994531f, 1.f);
+}
+__device__ __forceinline__ double exp_of(double z) { return exp(z); }
+__device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ double inverse(double v) { return 1.0 / v; }
+// 1 / (1 + e^-z)
+template <typename K>
+__device__ __forceinline__ K sigmoid_of(K z) {
+  return inverse((K)1 + exp_of(-z));
+}
 
-// Compare-exchange network of a descending sort (Batcher's odd-even merge sort), N a power of two.
+// Scaled score of a chosen logit for renormalised weights: both scores times a common factor that keeps the largest
+// of the row at least 1/2: softmax e^(l - top), sigmoid(l) = e^min(l, 0) / (1 + e^-|l|) with e^min(l, 0) scaled by
+// e^-top, top = min(largest chosen logit, 0).
+__device__ __forceinline__ float scaled_score(bool sigmoid, float l, float top) {
+  return sigmoid ? exp_of(fminf(l, 0.f) - top) * inverse(1.f + exp_of(-fabsf(l))) : exp_of(l - top);
+}
+
+// Compare-exchange network of a sort (Batcher's odd-even merge sort), N a power of two.
 template <int N, typename F>
 __device__ __forceinline__ void sort_network(F swap) {
 #pragma unroll
@@ -256,31 +112,158 @@ __device__ __forceinline__ void sort_network(F swap) {
           if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) swap(j + i, j + i + q);
 }
 
-// Each group of E / n_group experts sits on LG = 2^lg_bits lanes, PL experts a lane, in order.  The best of a lane
-// are sorted in registers, so a round of the selection is a maximum over the lanes' heads.
+// Where a lane's experts lie: each group of Eg = E / n_group experts sits on 2^lg_bits lanes, PL experts a lane, in
+// order (n_group is 1 where no group is dropped).
+struct Place {
+  int n_group, lg_bits;
+  bool vec4;  // rows and groups are whole 16-byte pieces
+};
+
+// Chooses the k experts of a token held by LT lanes into ids[0, k) (-1: none), given this lane's logits x (-inf: not
+// available), and returns whether keys of type K leave the choice in doubt.  m: the row's largest logit, or 0 for
+// sigmoid.  The best of a lane are sorted in registers, so a round of the selection is a maximum over the heads.
 //
-// Keys are fp32: logits without a bias (exact), else score + bias, off by at most delta = 1.25e-6 + 2.4e-7 max |key|
-// (score: exp2 and reciprocal 1 ulp each, their argument's rounding passes on at most 0.23 of it, the softmax's
-// common denominator moves all scores together; bias: one rounding).  Where the choice could come out differently
-// within that -- two keys in a row within 2 delta (equal logits, whose order is by id, among them), or the last kept
-// and the first dropped group within 5 delta -- the token goes to route_exact.  For scores spread over (0, 1) that
-// is a few tokens in a thousand; 64-bit keys throughout cost 45 us at 16384 x 256 against REPLACE_US.
-template <int LT, int PL, int PX>
-__global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs a, uint32_t magic, int n_group,
-                                                                       int lg_bits, bool vec4) {
-  extern __shared__ double s_key[];
-  __shared__ int s_id[kTokens][64 / LT][32];
-  constexpr int TPW = 64 / LT;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l = lane & (LT - 1), sub = lane / LT;
-  const int64_t t0 = ((int64_t)blockIdx.x * kTokens + wv) * TPW, t = t0 + sub;
-  const bool live = t < a.T;
-  const int E = a.E, Eg = E / n_group, k = a.k;
-  const int g = l >> lg_bits, s0 = (l & ((1 << lg_bits) - 1)) * PL;  // this lane's group, first expert in it
-  const int e0 = g * Eg + s0, ne = (live && g < n_group) ? min(PL, Eg - s0) : 0;  // (negative: none)
-  const float* row = a.logits + t * E;
-  float x[PL], key[PL];
+// K = float: keys are logits without a bias (exact), else score + bias, off by at most delta = 1.25e-6 + 2.4e-7
+// max |key| (score: exp2 and reciprocal 1 ulp each, the softmax's common denominator 5e-7 of it; bias: one
+// rounding).  Two keys in a row within 2 delta (equal ones, whose order is by id, among them), or the last kept and
+// the first dropped group within 5 delta, leave it in doubt.
+// K = double: nothing does; equal keys go by id.
+template <int LT, int PL, typename K>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const Place& pl, int l, int lane, int e0, const float (&x)[PL],
+                                       const float (&b)[PL], float m, int* ids, float& z) {
+  constexpr bool F32 = sizeof(K) == 4;
+  const K none = -INFINITY;
+  const int k = a.k;
+  K key[PL];
   int id[PL];
-  if (vec4 && ne == PL && PL % 4 == 0) {
+#pragma unroll
+  for (int i = 0; i < PL; ++i) id[i] = e0 + i;
+  K zz = 1;
+  if (!a.sigmoid && (a.bias || !a.renormalize)) {
+    K s = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s += x[i] > -INFINITY ? exp_of((K)x[i] - (K)m) : (K)0;
+    zz = sum_of<LT>(s);
+    z = (float)zz;
+  }
+  const K iz = inverse(zz);
+  auto score = [&](K v) { return a.sigmoid ? sigmoid_of(v) : exp_of(v - (K)m) * iz; };
+  float delta = 0.f;
+  if (a.bias) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const bool ok = x[i] > -INFINITY;
+      key[i] = ok ? score((K)x[i]) + (K)b[i] : none;
+      if (F32) big = fmaxf(big, ok ? fabsf((float)key[i]) : 0.f);
+    }
+    if (F32) delta = 1.25e-6f + 2.4e-7f * max_of<LT>(big);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) key[i] = x[i];
+  }
+  sort_network<PL>([&](int i, int j) {
+    const bool swap = key[j] > key[i] || (!F32 && key[j] == key[i] && id[j] < id[i]);
+    const K ki = key[i];
+    const int ii = id[i];
+    key[i] = swap ? key[j] : ki;
+    key[j] = swap ? ki : key[j];
+    id[i] = swap ? id[j] : ii;
+    id[j] = swap ? ii : id[j];
+  });
+
+  bool doubt = false;
+  if (pl.n_group > 1) {
+    K g1 = key[0], g2 = PL > 1 ? key[PL > 1 ? 1 : 0] : none;
+    auto merge = [&](K o1, K o2) {
+      g2 = max2(min2(g1, o1), max2(g2, o2));
+      g1 = max2(g1, o1);
+    };
+    if (pl.lg_bits >= 1) merge(dpp<0xB1>(g1), dpp<0xB1>(g2));
+    if (pl.lg_bits >= 2) merge(dpp<0x4E>(g1), dpp<0x4E>(g2));
+    if (pl.lg_bits >= 3) merge(dpp<0x141>(g1), dpp<0x141>(g2));
+    if (pl.lg_bits >= 4) merge(dpp<0x140>(g1), dpp<0x140>(g2));
+    if (LT == 64 && pl.lg_bits >= 5) merge(__shfl_xor(g1, 16), __shfl_xor(g2, 16));
+    float gd = delta;
+    if (a.group_top == 2) {
+      if (!a.bias) {
+        gd = 1.5e-6f;
+        g1 = g1 > none ? score(g1) : g1;
+        g2 = g2 > none ? score(g2) : g2;
+      }
+      if (g2 > none) g1 += g2;
+    }
+    int ahead = 0;  // lanes of better groups
+    if constexpr (LT == 16) {
+#define MOE_ROR(N) ahead += dpp<0x120 + N>(g1) > g1 ? 1 : 0;
+      MOE_ROR(1) MOE_ROR(2) MOE_ROR(3) MOE_ROR(4) MOE_ROR(5) MOE_ROR(6) MOE_ROR(7) MOE_ROR(8)
+      MOE_ROR(9) MOE_ROR(10) MOE_ROR(11) MOE_ROR(12) MOE_ROR(13) MOE_ROR(14) MOE_ROR(15)
+#undef MOE_ROR
+    } else {
+      const int mine = l >> pl.lg_bits;
+      for (int h = 0; h < pl.n_group; ++h) {
+        const K o = of_lane(g1, h << pl.lg_bits);
+        ahead += (o > g1 || (!F32 && o == g1 && h < mine) ? 1 : 0) << pl.lg_bits;
+      }
+    }
+    const bool keep = ahead < (a.topk_group << pl.lg_bits);
+    if (F32) {
+      // Lanes of no group hold -inf and are ahead of nothing.  Equal groups can leave more than topk_group kept.
+      const bool in = keep && g1 > none;
+      const K low = -max_of<LT>(in ? -g1 : none), high = max_of<LT>(keep ? none : g1);
+      const K kept = sum_of<LT>(in ? (K)1 : (K)0);
+      doubt = low - high <= (K)(5.f * gd) || kept > (K)(a.topk_group << pl.lg_bits);
+    }
+    if (!keep)
+#pragma unroll
+      for (int i = 0; i < PL; ++i) key[i] = none;
+  }
+
+  if (l < k) ids[l] = -1;
+  wave_lds_order();
+  K prev = INFINITY;
+  const K tol = 2.f * delta;
+  for (int j = 0; j <= k; ++j) {  // a round more than slots: the first that misses has to miss clearly
+    const K top = max_of<LT>(key[0]);
+    if (F32) doubt = doubt || (top > none && prev - top <= tol);
+    prev = top;
+    if (j == k) break;
+    const unsigned long long at = __ballot(key[0] == top && top > none);
+    const uint32_t mine = LT == 64 ? 0 : (uint32_t)(at >> (lane & 48)) & 0xffffu;
+    const bool win = LT == 64 ? at != 0 && lane == __builtin_ctzll(at) : mine != 0 && l == __builtin_ctz(mine);
+    if (win) {
+      ids[j] = id[0];
+      // What lies deeper than k + 1 in a lane's list is not looked at.
+      constexpr int D = PL < 9 ? PL : 9;
+#pragma unroll
+      for (int i = 0; i + 1 < D; ++i) {
+        key[i] = key[i + 1];
+        id[i] = id[i + 1];
+      }
+      if (PL > D && k > 8) {
+#pragma unroll
+        for (int i = D - 1; i + 1 < PL; ++i) {
+          key[i] = key[i + 1];
+          id[i] = id[i + 1];
+        }
+        key[PL - 1] = none;
+      } else {
+        key[D - 1] = none;
+      }
+    }
+  }
+  wave_lds_order();
+  return doubt;
+}
+
+// This lane's logits and biases of token t: experts e0 .. of group l >> lg_bits.
+template <int PL>
+__device__ __forceinline__ int load_experts(const RouteArgs& a, const Place& pl, int64_t t, bool live, int l, float (&x)[PL],
+                                            float (&b)[PL]) {
+  const int Eg = a.E / pl.n_group, g = l >> pl.lg_bits, s0 = (l & ((1 << pl.lg_bits) - 1)) * PL;
+  const int e0 = g * Eg + s0, ne = (live && g < pl.n_group) ? min(PL, Eg - s0) : 0;  // (negative: none)
+  const float* row = a.logits + t * a.E;
+  if (PL % 4 == 0 && pl.vec4 && ne == PL) {
 #pragma unroll
     for (int i = 0; i < PL; i += 4) {
       const floatx4 v = *reinterpret_cast<const floatx4*>(row + e0 + i);
@@ -291,148 +274,88 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs
 #pragma unroll
     for (int i = 0; i < PL; ++i) x[i] = i < ne ? row[e0 + i] : -INFINITY;
   }
-  float m = -FLT_MAX;
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    id[i] = e0 + i;
     x[i] = x[i] > -INFINITY ? fminf(x[i], FLT_MAX) : -INFINITY;  // NaN: not available
+    b[i] = 0.f;
   }
-  float b[PL];
   if (a.bias) {
+    if (PL % 4 == 0 && pl.vec4 && ne == PL) {
+#pragma unroll
+      for (int i = 0; i < PL; i += 4) {
+        const floatx4 v = *reinterpret_cast<const floatx4*>(a.bias + e0 + i);
+#pragma unroll
+        for (int q = 0; q < 4 && i + q < PL; ++q) b[i + q] = v[q];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) b[i] = i < ne ? a.bias[e0 + i] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      b[i] = i < ne ? a.bias[e0 + i] : 0.f;
       if (!(b[i] > -INFINITY)) x[i] = -INFINITY;
       b[i] = fminf(b[i], FLT_MAX);
     }
   }
-  float z = 1.f;
+  return e0;
+}
+
+// One token by a whole wavefront, with 64-bit keys; only the ids.
+template <int PL>
+__device__ void choose_exact(const RouteArgs& a, const Place& pl, int64_t t, int lane, int* ids) {
+  float x[PL], b[PL], m = 0.f, z = 1.f;
+  const int e0 = load_experts<PL>(a, pl, t, true, lane, x, b);
   if (!a.sigmoid) {
+    m = -FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
+    m = max_of<64>(m);
+  }
+  choose<64, PL, double>(a, pl, lane, lane, e0, x, b, m, ids, z);
+}
+
+// LT lanes per token, 64 / LT tokens per wavefront.  Tokens that fp32 keys leave in doubt are chosen again in 64 bits
+// (PX experts a lane): at 16384 x 256 a few in a thousand; 64-bit keys for all took 45 us there.
+template <int LT, int PL, int PX>
+__global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs a, Place pl, int exact_bits) {
+  __shared__ int s_id[kTokens][64 / LT][32];
+  constexpr int TPW = 64 / LT;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l = lane & (LT - 1), sub = lane / LT;
+  const int64_t t0 = ((int64_t)blockIdx.x * kTokens + wv) * TPW, t = t0 + sub;
+  const bool live = t < a.T;
+  float x[PL], b[PL], m = 0.f, z = 1.f;
+  const int e0 = load_experts<PL>(a, pl, t, live, l, x, b);
+  if (!a.sigmoid) {
+    m = -FLT_MAX;
 #pragma unroll
     for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
     m = max_of<LT>(m);
-    if (a.bias || !a.renormalize) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < PL; ++i) s += exp_fast(x[i] - m);
-      z = sum_of<LT>(s);
-    }
   }
-  auto score = [&](float v) { return a.sigmoid ? sigmoid_fast(v) : exp_fast(v - m) / z; };
-  float delta = 0.f;
-  if (a.bias) {
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const bool ok = x[i] > -INFINITY;
-      key[i] = ok ? score(x[i]) + b[i] : -INFINITY;
-      big = fmaxf(big, ok ? fabsf(key[i]) : 0.f);
-    }
-    delta = 1.25e-6f + 2.4e-7f * max_of<LT>(big);
-  } else {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) key[i] = x[i];
-  }
-  sort_network<PL>([&](int i, int j) {
-    const bool swap = key[j] > key[i];
-    const float ki = key[i];
-    const int ii = id[i];
-    key[i] = swap ? key[j] : ki;
-    key[j] = swap ? ki : key[j];
-    id[i] = swap ? id[j] : ii;
-    id[j] = swap ? ii : id[j];
-  });
-
-  bool unsure = false;
-  if (n_group > 1) {  // the launcher passes one group where all are kept
-    float g1 = key[0], g2 = PL > 1 ? key[PL > 1 ? 1 : 0] : -INFINITY;
-    auto merge = [&](float o1, float o2) {
-      g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
-      g1 = fmaxf(g1, o1);
-    };
-    if (lg_bits >= 1) merge(dppf<0xB1>(g1), dppf<0xB1>(g2));
-    if (lg_bits >= 2) merge(dppf<0x4E>(g1), dppf<0x4E>(g2));
-    if (lg_bits >= 3) merge(dppf<0x141>(g1), dppf<0x141>(g2));
-    if (lg_bits >= 4) merge(dppf<0x140>(g1), dppf<0x140>(g2));
-    if (LT == 64 && lg_bits >= 5) merge(__shfl_xor(g1, 16), __shfl_xor(g2, 16));
-    float gd = delta;
-    if (a.group_top == 2) {
-      if (!a.bias) {
-        gd = 1.5e-6f;
-        g1 = g1 > -INFINITY ? score(g1) : g1;
-        g2 = g2 > -INFINITY ? score(g2) : g2;
-      }
-      if (g2 > -INFINITY) g1 += g2;
-    }
-    int ahead = 0;  // lanes of better groups
-    if constexpr (LT == 16) {
-#define MOE_ROR(N) ahead += dppf<0x120 + N>(g1) > g1 ? 1 : 0;
-      MOE_ROR(1) MOE_ROR(2) MOE_ROR(3) MOE_ROR(4) MOE_ROR(5) MOE_ROR(6) MOE_ROR(7) MOE_ROR(8)
-      MOE_ROR(9) MOE_ROR(10) MOE_ROR(11) MOE_ROR(12) MOE_ROR(13) MOE_ROR(14) MOE_ROR(15)
-#undef MOE_ROR
-    } else {
-      for (int h = 0; h < n_group; ++h) ahead += (lanef(g1, h << lg_bits) > g1 ? 1 : 0) << lg_bits;
-    }
-    const bool keep = ahead < (a.topk_group << lg_bits);
-    // Lanes of no group hold -inf and are ahead of nothing.
-    const float low = -max_of<LT>(keep && g1 > -INFINITY ? -g1 : -INFINITY), high = max_of<LT>(keep ? -INFINITY : g1);
-    unsure = low - high <= 5.f * gd;
-    // Equal groups can leave more than topk_group kept (none is ahead of the other).
-    const float kept = sum_of<LT>(keep && g1 > -INFINITY ? 1.f : 0.f);
-    unsure = unsure || kept > (float)(a.topk_group << lg_bits);
-    if (!keep)
-#pragma unroll
-      for (int i = 0; i < PL; ++i) key[i] = -INFINITY;
-  }
-
   int* ids = s_id[wv][sub];
-  if (l < k) ids[l] = -1;
-  wave_lds_order();
-  float prev = INFINITY;
-  const float tol = 2.f * delta;
-  for (int j = 0; j <= k; ++j) {  // one round more than slots: the first that misses has to miss clearly
-    const float top = max_of<LT>(key[0]);
-    unsure = unsure || (top > -INFINITY && prev - top <= tol);
-    prev = top;
-    if (j == k) break;
-    const unsigned long long at = __ballot(key[0] == top && top > -INFINITY);
-    const uint32_t mine = LT == 64 ? 0 : (uint32_t)(at >> (lane & 48)) & 0xffffu;
-    const bool win = LT == 64 ? at != 0 && lane == __builtin_ctzll(at) : mine != 0 && l == __builtin_ctz(mine);
-    if (win) {
-      ids[j] = id[0];
-#pragma unroll
-      for (int i = 0; i + 1 < PL; ++i) {
-        key[i] = key[i + 1];
-        id[i] = id[i + 1];
-      }
-      key[PL - 1] = -INFINITY;
-    }
-  }
-  wave_lds_order();
-  // Slot j's id on lane j (k <= LT).
-  const int sel = l < k ? ids[l] : -1;
-  const bool has = live && sel >= 0;
-  const float sl = has ? fminf(row[sel], FLT_MAX) : 0.f;
-  float s = 0.f, w = 0.f;
-  if (a.renormalize) {
-    float top = max_of<LT>(has ? sl : -FLT_MAX);
-    if (a.sigmoid) top = fminf(top, 0.f);
-    if (has) s = a.sigmoid ? expf(fminf(sl, 0.f) - top) / (1.f + expf(-fabsf(sl))) : expf(sl - top);
-    const float sum = sum_of<LT>(s);
-    w = has ? a.scale * (s / sum) : 0.f;
-  } else if (has) {
-    w = a.scale * (a.sigmoid ? 1.f / (1.f + expf(-sl)) : expf(sl - m) / z);
-  }
-  const unsigned long long doubt = __ballot(unsure && live);
-  const bool mine_sure = LT == 64 ? doubt == 0 : ((doubt >> (lane & 48)) & 0xffffu) == 0;
-  if (live && l < k && mine_sure) {
-    a.idx[t * k + l] = sel;
-    a.w[t * k + l] = w;
-  }
-  if (doubt != 0)
+  const bool doubt = choose<LT, PL, float>(a, pl, l, lane, e0, x, b, m, ids, z);
+  const unsigned long long again = __ballot(doubt && live);
+  if (again != 0) {
+    const Place px{pl.n_group, exact_bits, pl.vec4};
     for (int q = 0; q < TPW; ++q)
-      if (LT == 64 || ((doubt >> (16 * q)) & 0xffffu) != 0)
-        route_exact<PX>(a, t0 + q, lane, magic, s_key + wv * E);
+      if (LT == 64 || ((again >> (16 * q)) & 0xffffu) != 0) choose_exact<PX>(a, px, t0 + q, lane, s_id[wv][q]);
+  }
+  // Slot j's id on lane j (k <= LT).
+  const int sel = l < a.k ? ids[l] : -1;
+  const bool has = live && sel >= 0;
+  const float lg = has ? fminf(a.logits[t * a.E + sel], FLT_MAX) : 0.f;
+  float w = 0.f;
+  if (a.renormalize) {
+    float top = max_of<LT>(has ? lg : -FLT_MAX);
+    if (a.sigmoid) top = fminf(top, 0.f);
+    const float s = has ? scaled_score(a.sigmoid, lg, top) : 0.f, sum = sum_of<LT>(s);
+    w = has ? a.scale * (s * inverse(sum)) : 0.f;
+  } else if (has) {
+    w = a.scale * (a.sigmoid ? sigmoid_of(lg) : exp_of(lg - m) * inverse(z));
+  }
+  if (live && l < a.k) {
+    a.idx[t * a.k + l] = sel;
+    a.w[t * a.k + l] = w;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -492,12 +415,12 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_backward_kernel(
     for (int i = 0; i < PL; ++i)
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        o[i][q] = exp_fast(o[i][q] - m);
+        o[i][q] = exp_of(o[i][q] - m);
         s += o[i][q];
       }
     float z = sum_of<LT>(s);
-    z = z > 0.f ? 1.f / z : 0.f;  // no expert is available: every term is zero
-    d = has ? g * (exp_fast(lg - m) * z) : 0.f;
+    z = z > 0.f ? inverse(z) : 0.f;  // no expert is available: every term is zero
+    d = has ? g * (exp_of(lg - m) * z) : 0.f;
     const float rest = sum_of<LT>(d) * z;
 #pragma unroll
     for (int i = 0; i < PL; ++i)
@@ -507,14 +430,12 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_backward_kernel(
     if (a.renormalize) {
       float top = max_of<LT>(has ? lg : -FLT_MAX);
       if (a.sigmoid) top = fminf(top, 0.f);
-      float s = 0.f;
-      if (has) s = a.sigmoid ? expf(fminf(lg, 0.f) - top) / (1.f + expf(-fabsf(lg))) : expf(lg - top);
-      const float sum = sum_of<LT>(s);
-      const float q = has ? s / sum : 0.f;
+      const float s = has ? scaled_score(a.sigmoid, lg, top) : 0.f, sum = sum_of<LT>(s);
+      const float q = has ? s * inverse(sum) : 0.f;
       d = q * (g - sum_of<LT>(has ? q * g : 0.f));
-      if (a.sigmoid && has) d *= 1.f / (1.f + expf(lg));  // 1 - s
+      if (a.sigmoid && has) d *= sigmoid_of(-lg);  // 1 - s
     } else if (has) {
-      d = g * (1.f / (1.f + expf(-lg))) * (1.f / (1.f + expf(lg)));
+      d = g * sigmoid_of(lg) * sigmoid_of(-lg);
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i)
@@ -522,13 +443,28 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_backward_kernel(
       for (int q = 0; q < V; ++q) o[i][q] = 0.f;
   }
   if (!has) d = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = LT == 64 ? __builtin_amdgcn_readlane(id, j) : __shfl(id, (lane & 48) + j);
-    const float v = LT == 64 ? lanef(d, j) : __shfl(d, (lane & 48) + j);
+  if constexpr (LT == 64) {
+    for (int j = 0; j < k; ++j) {  // the id is uniform: a scalar choice of the register, one lane's addition
+      const int e = __builtin_amdgcn_readlane(id, j);
+      const float v = of_lane(d, j);
+      if (e < 0) continue;
+      const float add = lane == (e / V & 63) ? v : 0.f;
+      const int at = e / (V * 64) * V + e % V;
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
+      for (int i = 0; i < PL; ++i)
 #pragma unroll
-      for (int q = 0; q < V; ++q) o[i][q] += V * (l + LT * i) + q == e ? v : 0.f;
+        for (int q = 0; q < V; ++q)
+          if (at == i * V + q) o[i][q] += add;
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const int e = __shfl(id, (lane & 48) + j);
+      const float v = __shfl(d, (lane & 48) + j);
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+#pragma unroll
+        for (int q = 0; q < V; ++q) o[i][q] += V * (l + LT * i) + q == e ? v : 0.f;
+    }
   }
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
@@ -547,46 +483,35 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_backward_kernel(
 hipError_t launch_route_grouped(const RouteArgs& a, hipStream_t s) {
   const int n_group = a.topk_group < a.n_group ? a.n_group : 1;  // groups restrict the choice only if some are dropped
   const int Eg = a.E / n_group;
-  const uint32_t magic = ((1u << 22) + a.E / a.n_group - 1) / (a.E / a.n_group);
-  const size_t lds = n_group > 1 ? (size_t)kTokens * a.E * sizeof(double) : 0;
-  auto lanes_per_group = [&](int lt) {  // log2, or -1
-    if (n_group > lt) return -1;
-    int bits = 0;
+  auto bits_of = [&](int lt) {  // log2 of the lanes a group gets, or -1
+    int bits = -1;
     while (n_group << (bits + 1) <= lt) ++bits;
     return bits;
   };
   auto per_lane = [&](int bits) { return bits < 0 ? 1 << 20 : (Eg + (1 << bits) - 1) >> bits; };
-  const int b16 = lanes_per_group(16), b64 = lanes_per_group(64), p16 = per_lane(b16), p64 = per_lane(b64);
-  const int px = (a.E + kWave - 1) / kWave;
-  const bool aligned = a.E % 4 == 0 && Eg % 4 == 0;
+  const int b16 = bits_of(16), b64 = bits_of(64), p16 = per_lane(b16), p64 = per_lane(b64);  // p64 <= 32
+  const bool vec4 = a.E % 4 == 0 && Eg % 4 == 0;
   // 16 lanes a token share the rounds of the selection between four tokens; 64 have fewer experts a lane to sort,
   // which is quicker until the tokens fill the chip.
-  if (p16 <= 16 && a.k <= 16 && (p16 <= 4 || a.T > 2048)) {
-    const dim3 grid((unsigned)((a.T + 4 * kTokens - 1) / (4 * kTokens))), block(kTokens * kWave);
-#define MOE_ROUTE(PL_, PX_) \
-  hipLaunchKernelGGL((route_grouped_kernel<16, PL_, PX_>), grid, block, lds, s, a, magic, n_group, b16, aligned)
-    if (p16 <= 1) MOE_ROUTE(1, 1);
-    else if (p16 <= 2) MOE_ROUTE(2, 1);
-    else if (p16 <= 4) MOE_ROUTE(4, 1);
-    else if (p16 <= 8) MOE_ROUTE(8, 2);
-    else MOE_ROUTE(16, 4);
-#undef MOE_ROUTE
-    return hipGetLastError();
+  const bool small = p16 <= 16 && a.k <= 16 && (p16 <= 4 || a.T > 2048);
+  const int per_block = kTokens * (small ? 4 : 1);
+  const dim3 grid((unsigned)((a.T + per_block - 1) / per_block)), block(kTokens * kWave);
+  const Place pl{n_group, small ? b16 : b64, vec4};
+#define MOE_ROUTE(LT_, PL_, PX_) hipLaunchKernelGGL((route_grouped_kernel<LT_, PL_, PX_>), grid, block, 0, s, a, pl, b64)
+  if (small) {
+    if (p16 <= 1) MOE_ROUTE(16, 1, 1);
+    else if (p16 <= 2) MOE_ROUTE(16, 2, 1);
+    else if (p16 <= 4) MOE_ROUTE(16, 4, 1);
+    else if (p16 <= 8) MOE_ROUTE(16, 8, 2);
+    else MOE_ROUTE(16, 16, 4);
+  } else {
+    if (p64 <= 1) MOE_ROUTE(64, 1, 1);
+    else if (p64 <= 2) MOE_ROUTE(64, 2, 2);
+    else if (p64 <= 4) MOE_ROUTE(64, 4, 4);
+    else if (p64 <= 8) MOE_ROUTE(64, 8, 8);
+    else if (p64 <= 16) MOE_ROUTE(64, 16, 16);
+    else MOE_ROUTE(64, 32, 32);
   }
-  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kTokens * kWave);
-  if (p64 <= 8) {
-#define MOE_ROUTE(PL_, PX_) \
-  hipLaunchKernelGGL((route_grouped_kernel<64, PL_, PX_>), grid, block, lds, s, a, magic, n_group, b64, aligned)
-    if (p64 <= 1) MOE_ROUTE(1, 1);
-    else if (p64 <= 2) MOE_ROUTE(2, 2);
-    else if (p64 <= 4) MOE_ROUTE(4, 4);
-    else MOE_ROUTE(8, 8);
-#undef MOE_ROUTE
-    return hipGetLastError();
-  }
-#define MOE_ROUTE(PL_) hipLaunchKernelGGL(route_exact_kernel<PL_>, grid, block, lds, s, a, magic)
-  if (px <= 4) MOE_ROUTE(4);
-  else MOE_ROUTE(16);
 #undef MOE_ROUTE
   return hipGetLastError();
 }
