@@ -361,121 +361,187 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs
 // ---------------------------------------------------------------------------
 // Gradient of the gate weights
 // ---------------------------------------------------------------------------
-// HBM-bound: reads the chosen logits (the plain softmax's gradient: all of them), writes every gradient once.  LT
-// lanes per token; lane l holds V consecutive experts (4: 16-byte accesses, E % 4 == 0) from V (l + LT i), i < PL.
-// The chosen experts' terms are handed to the lanes that hold them one by one, so that repeated ids add up in order.
-template <int LT, int V, int PL>
-__global__ __launch_bounds__(kTokens* kWave) void route_grouped_backward_kernel(RouteBwdArgs a) {
-  const int lane = threadIdx.x & 63, l = lane & (LT - 1);
-  const int64_t t = ((int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6)) * (64 / LT) + lane / LT;
-  const bool live = t < a.T;
+// Slot l of a token: its expert (-1: none), scale * d_topk_w, and the expert's logit.
+struct Slot {
+  int id;
+  float g, lg;
+};
+__device__ __forceinline__ Slot load_slot(const RouteBwdArgs& a, int64_t t, bool live, int l) {
+  Slot s{-1, 0.f, -INFINITY};
+  if (live && l < a.k) {
+    s.id = a.idx[t * a.k + l];
+    s.g = a.scale * a.d_w[t * a.k + l];
+    if (s.id < 0 || s.id >= a.E) s.id = -1;
+    if (s.id >= 0) {
+      const float v = a.logits[t * a.E + s.id];
+      s.lg = fminf(v, FLT_MAX);
+      if (!(v > -INFINITY)) s.id = -1;  // an expert that is not available has score 0
+    }
+  }
+  return s;
+}
+
+// A slot's term of the gradient; the token's LT lanes together.  m, iz: largest logit and 1 / sum e^(l - m) of the
+// row (plain softmax).
+template <int LT>
+__device__ __forceinline__ float slot_term(const RouteBwdArgs& a, const Slot& s, float m, float iz) {
+  const bool has = s.id >= 0;
+  if (a.renormalize) {
+    float top = max_of<LT>(has ? s.lg : -FLT_MAX);
+    if (a.sigmoid) top = fminf(top, 0.f);
+    const float v = has ? scaled_score(a.sigmoid, s.lg, top) : 0.f, sum = sum_of<LT>(v);
+    const float q = has ? v * inverse(sum) : 0.f;
+    const float d = q * (s.g - sum_of<LT>(has ? q * s.g : 0.f));
+    return a.sigmoid && has ? d * sigmoid_of(-s.lg) : d;  // 1 - s
+  }
+  if (!has) return 0.f;
+  return a.sigmoid ? s.g * sigmoid_of(s.lg) * sigmoid_of(-s.lg) : s.g * (exp_of(s.lg - m) * iz);
+}
+
+// V consecutive logits from e, -inf where there are none.
+template <int V>
+__device__ __forceinline__ void load_row(float (&x)[V], const float* row, int e, bool in) {
+#pragma unroll
+  for (int q = 0; q < V; ++q) x[q] = -INFINITY;
+  if (in) {
+    if constexpr (V == 4) {
+      const floatx4 v = *reinterpret_cast<const floatx4*>(row + e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = v[q];
+    } else {
+      x[0] = row[e];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < V; ++q) x[q] = x[q] > -INFINITY ? fminf(x[q], FLT_MAX) : -INFINITY;
+}
+template <int V>
+__device__ __forceinline__ void store_row(float* row, int e, const float (&o)[V]) {
+  if constexpr (V == 4)
+    __builtin_nontemporal_store(floatx4{o[0], o[1], o[2], o[3]}, reinterpret_cast<floatx4*>(row + e));
+  else
+    row[e] = o[0];
+}
+
+// HBM-bound: reads the chosen logits (the plain softmax's gradient: all of them), writes every gradient once.  TW
+// tokens per wavefront: their slots side by side, 64 / TW lanes each, so that one chain of dependent loads (slot, then
+// its logit) serves them all; then row by row over the whole wavefront, lane l holding V consecutive experts (4:
+// 16-byte accesses, E % 4 == 0) from V (l + 64 i), i < PL.  The chosen experts' terms reach the lanes that hold them
+// through a row of the wavefront's own in LDS, all slots at once: handed over one by one they cost 25 instructions a
+// slot, 9.5 us at 16384 x 256 x 8 against 5.1.  A slot first leaves its number at its expert; one that finds
+// another there shares its id, and then the wavefront's slots are added one after the other.
+template <int TW, int V, int PL>
+__global__ __launch_bounds__(kTokens* kWave) void route_rows_backward_kernel(RouteBwdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float s_rows[];  // [kTokens][TW][Ep]
+  constexpr int LT = 64 / TW, Ep = 64 * V * PL;
+  const int lane = threadIdx.x & 63, sub = lane / LT;
+  float* rows = s_rows + (threadIdx.x >> 6) * (TW * Ep);
+  const int64_t t0 = ((int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6)) * TW;
   const int E = a.E, k = a.k;
-  const float* row = a.logits + t * E;
-  int id = -1;
-  float g = 0.f, lg = -INFINITY;
-  if (live && l < k) {
-    id = a.idx[t * k + l];
-    g = a.scale * a.d_w[t * k + l];
-    if (id < 0 || id >= E) id = -1;
-    if (id >= 0) {
-      const float v = row[id];
-      lg = fminf(v, FLT_MAX);
-      if (!(v > -INFINITY)) id = -1;  // an expert that is not available has score 0
-    }
-  }
-  const bool has = id >= 0;
   const bool dense = !a.sigmoid && !a.renormalize;
-  float o[PL][V];
-  float d = 0.f;
-  if (dense) {
-    float m = -FLT_MAX;
+  float o[TW][PL][V];
+  if (dense)
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = V * (l + LT * i);
+    for (int w = 0; w < TW; ++w)
 #pragma unroll
-      for (int q = 0; q < V; ++q) o[i][q] = -INFINITY;
-      if (live && e < E) {
-        if constexpr (V == 4) {
-          const floatx4 v = *reinterpret_cast<const floatx4*>(row + e);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) o[i][q] = v[q];
-        } else {
-          o[i][0] = row[e];
-        }
+      for (int i = 0; i < PL; ++i) {
+        const int e = V * (lane + 64 * i);
+        load_row<V>(o[w][i], a.logits + (t0 + w) * E, e, t0 + w < a.T && e < E);
       }
+  const Slot s = load_slot(a, t0 + sub, t0 + sub < a.T, lane & (LT - 1));
+  float m = 0.f, iz = 0.f;
+  if (dense)
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
-        o[i][q] = o[i][q] > -INFINITY ? fminf(o[i][q], FLT_MAX) : -INFINITY;
-        m = fmaxf(m, o[i][q]);
-      }
-    }
-    m = max_of<LT>(m);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-#pragma unroll
-      for (int q = 0; q < V; ++q) {
-        o[i][q] = exp_of(o[i][q] - m);
-        s += o[i][q];
-      }
-    float z = sum_of<LT>(s);
-    z = z > 0.f ? inverse(z) : 0.f;  // no expert is available: every term is zero
-    d = has ? g * (exp_of(lg - m) * z) : 0.f;
-    const float rest = sum_of<LT>(d) * z;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-#pragma unroll
-      for (int q = 0; q < V; ++q) o[i][q] *= -rest;
-  } else {
-    if (a.renormalize) {
-      float top = max_of<LT>(has ? lg : -FLT_MAX);
-      if (a.sigmoid) top = fminf(top, 0.f);
-      const float s = has ? scaled_score(a.sigmoid, lg, top) : 0.f, sum = sum_of<LT>(s);
-      const float q = has ? s * inverse(sum) : 0.f;
-      d = q * (g - sum_of<LT>(has ? q * g : 0.f));
-      if (a.sigmoid && has) d *= sigmoid_of(-lg);  // 1 - s
-    } else if (has) {
-      d = g * sigmoid_of(lg) * sigmoid_of(-lg);
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-#pragma unroll
-      for (int q = 0; q < V; ++q) o[i][q] = 0.f;
-  }
-  if (!has) d = 0.f;
-  if constexpr (LT == 64) {
-    for (int j = 0; j < k; ++j) {  // the id is uniform: a scalar choice of the register, one lane's addition
-      const int e = __builtin_amdgcn_readlane(id, j);
-      const float v = of_lane(d, j);
-      if (e < 0) continue;
-      const float add = lane == (e / V & 63) ? v : 0.f;
-      const int at = e / (V * 64) * V + e % V;
+    for (int w = 0; w < TW; ++w) {
+      float mw = -FLT_MAX, zw = 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i)
 #pragma unroll
-        for (int q = 0; q < V; ++q)
-          if (at == i * V + q) o[i][q] += add;
+        for (int q = 0; q < V; ++q) mw = fmaxf(mw, o[w][i][q]);
+      mw = max_of<64>(mw);
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          o[w][i][q] = exp_of(o[w][i][q] - mw);
+          zw += o[w][i][q];
+        }
+      zw = sum_of<64>(zw);
+      zw = zw > 0.f ? inverse(zw) : 0.f;  // no expert is available: every term is zero
+      m = sub == w ? mw : m;
+      iz = sub == w ? zw : iz;
     }
+  const float d = slot_term<LT>(a, s, m, iz);
+  const float rest = dense ? -sum_of<LT>(d) * iz : 0.f;
+  const bool has = s.id >= 0;
+  float* at = rows + sub * Ep + (has ? s.id : 0);
+  if (has) *at = __builtin_bit_cast(float, lane);
+  wave_lds_order();
+  const bool shared = __ballot(has && __builtin_bit_cast(int, *at) != lane) != 0;
+  wave_lds_order();
+#pragma unroll
+  for (int w = 0; w < TW; ++w)
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+#pragma unroll
+      for (int q = 0; q < V; ++q) rows[w * Ep + V * (lane + 64 * i) + q] = 0.f;
+  wave_lds_order();
+  if (!shared) {
+    if (has) *at = d;
   } else {
     for (int j = 0; j < k; ++j) {
-      const int e = __shfl(id, (lane & 48) + j);
-      const float v = __shfl(d, (lane & 48) + j);
-#pragma unroll
-      for (int i = 0; i < PL; ++i)
-#pragma unroll
-        for (int q = 0; q < V; ++q) o[i][q] += V * (l + LT * i) + q == e ? v : 0.f;
+      if (has && (lane & (LT - 1)) == j) *at += d;
+      wave_lds_order();
     }
   }
+  wave_lds_order();
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = V * (l + LT * i);
-    if (live && e < E) {
-      if constexpr (V == 4)
-        __builtin_nontemporal_store(floatx4{o[i][0], o[i][1], o[i][2], o[i][3]}, reinterpret_cast<floatx4*>(a.d_logits + t * E + e));
-      else
-        a.d_logits[t * E + e] = o[i][0];
+  for (int w = 0; w < TW; ++w) {
+    if (t0 + w >= a.T) break;  // wave-uniform
+    const float rw = dense ? of_lane(rest, w * LT) : 0.f;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int e = V * (lane + 64 * i);
+      float v[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] = rows[w * Ep + e + q] + (dense ? o[w][i][q] * rw : 0.f);
+      if (e < E) store_row<V>(a.d_logits + (t0 + w) * E, e, v);
     }
   }
+}
+
+// E <= 64, E % 4 == 0 and k <= 16: 16 lanes a token throughout, four experts a lane.
+__global__ __launch_bounds__(kTokens* kWave) void route_small_backward_kernel(RouteBwdArgs a) {
+  const int lane = threadIdx.x & 63, l = lane & 15, e = 4 * l;
+  const int64_t t = ((int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6)) * 4 + (lane >> 4);
+  const bool live = t < a.T, in = live && e < a.E;
+  const bool dense = !a.sigmoid && !a.renormalize;
+  float o[4];
+  load_row<4>(o, a.logits + t * a.E, e, in && dense);
+  const Slot s = load_slot(a, t, live, l);
+  float m = 0.f, iz = 0.f;
+  if (dense) {
+    m = max_of<16>(fmaxf(fmaxf(fmaxf(o[0], o[1]), fmaxf(o[2], o[3])), -FLT_MAX));
+    float z = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[q] = exp_of(o[q] - m);
+      z += o[q];
+    }
+    z = sum_of<16>(z);
+    iz = z > 0.f ? inverse(z) : 0.f;
+  }
+  const float d = slot_term<16>(a, s, m, iz);
+  const float rest = -sum_of<16>(d) * iz;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = dense ? o[q] * rest : 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    const int id = __shfl(s.id, (lane & 48) + j);
+    const float v = __shfl(d, (lane & 48) + j);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] += e + q == id ? v : 0.f;
+  }
+  if (in) store_row<4>(a.d_logits + t * a.E, e, o);
 }
 
 }  // namespace
@@ -519,17 +585,24 @@ hipError_t launch_route_grouped(const RouteArgs& a, hipStream_t s) {
 hipError_t launch_route_grouped_backward(const RouteBwdArgs& a, hipStream_t s) {
   const dim3 block(kTokens * kWave);
   const auto grid = [&](int per_wave) { return dim3((unsigned)((a.T + per_wave * kTokens - 1) / (per_wave * kTokens))); };
-#define MOE_ROUTE(LT_, V_, PL_) \
-  hipLaunchKernelGGL((route_grouped_backward_kernel<LT_, V_, PL_>), grid(64 / LT_), block, 0, s, a)
+  // Four tokens a wavefront while their slots fit and the tokens fill the chip.
+#define MOE_ROUTE(V_, PL_)                                                                                  \
+  do {                                                                                                      \
+    const size_t row = (size_t)kTokens * 64 * V_ * PL_ * sizeof(float);                                     \
+    if (a.k <= 16 && a.T > 2048)                                                                            \
+      hipLaunchKernelGGL((route_rows_backward_kernel<4, V_, PL_>), grid(4), block, 4 * row, s, a);          \
+    else                                                                                                    \
+      hipLaunchKernelGGL((route_rows_backward_kernel<1, V_, PL_>), grid(1), block, row, s, a);              \
+  } while (0)
   if (a.E % 4 == 0) {
-    if (a.E <= 64 && a.k <= 16) MOE_ROUTE(16, 4, 1);
-    else if (a.E <= 256) MOE_ROUTE(64, 4, 1);
-    else if (a.E <= 512) MOE_ROUTE(64, 4, 2);
-    else MOE_ROUTE(64, 4, 4);
+    if (a.E <= 64 && a.k <= 16) hipLaunchKernelGGL(route_small_backward_kernel, grid(4), block, 0, s, a);
+    else if (a.E <= 256) MOE_ROUTE(4, 1);
+    else if (a.E <= 512) MOE_ROUTE(4, 2);
+    else MOE_ROUTE(4, 4);
   } else {
-    if (a.E <= 64) MOE_ROUTE(64, 1, 1);
-    else if (a.E <= 256) MOE_ROUTE(64, 1, 4);
-    else MOE_ROUTE(64, 1, 16);
+    if (a.E <= 64) MOE_ROUTE(1, 1);
+    else if (a.E <= 256) MOE_ROUTE(1, 4);
+    else MOE_ROUTE(1, 16);
   }
 #undef MOE_ROUTE
   return hipGetLastError();

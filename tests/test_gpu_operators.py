@@ -92,6 +92,19 @@ def test_route_shapes(T, E, G, tg, gt, k, score, biased):
     check_route(l, k, b, score=score, n_group=G, topk_group=tg, group_top=gt, renormalize=(T + E) % 2 == 0, scale=2.5)
 
 
+@pytest.mark.parametrize("E,G,tg,gt,k", [(256, 8, 4, 2, 8), (160, 8, 3, 2, 6), (256, 1, 1, 1, 16), (90, 3, 2, 1, 10), (192, 16, 5, 2, 9)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_many_tokens(E, G, tg, gt, k, score, biased):
+    """Enough tokens for the form that shares a wavefront between four of them, with padding rows and masked experts."""
+    g = gen(E)
+    l = torch.randn(2051, E, generator=g) * 1.5
+    l[::17] = -INF
+    l[torch.rand(l.shape, generator=g) < 0.1] = -INF
+    b = torch.randn(E, generator=g) * 0.1 if biased else None
+    check_route(l, k, b, score=score, n_group=G, topk_group=tg, group_top=gt, renormalize=biased, scale=2.5)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("G,tg,gt", [(1, 1, 1), (4, 2, 2), (4, 2, 1)])
@@ -139,7 +152,8 @@ def test_route_equals_the_plain_routing():
     torch.testing.assert_close(a[1], b[1], rtol=2e-6, atol=0)
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (5, 8, 2), (33, 64, 6), (257, 160, 6), (3, 1024, 32), (9, 1, 1), (17, 37, 11)])
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (5, 8, 2), (33, 64, 6), (257, 160, 6), (3, 1024, 32), (9, 1, 1), (17, 37, 11),
+                                   (2051, 256, 8), (2050, 130, 5), (2049, 260, 17)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route_backward(T, E, k, score, renorm):
