@@ -11,7 +11,6 @@ buffers, e.g. under graph capture) or are allocated on the input's device.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -341,52 +340,49 @@ def moe_combine(y_perm: torch.Tensor, inv_perm: torch.Tensor, topk_w: torch.Tens
 # launch on the tensors' device, whichever device is current.
 # ---------------------------------------------------------------------------
 
-def _take(t: Optional[torch.Tensor], name: str, dtype, shape, dev, optional: bool = False):
-    """Address of a checked argument (None for an absent optional one)."""
+def _take(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int, optional: bool = False):
+    """Address of a checked argument on device number `dev` (None for an absent optional one)."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _first(t: torch.Tensor, name: str, ndim: int) -> torch.device:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _matrix(t: torch.Tensor, name: str):
+    """(rows, columns) of a two-dimensional argument."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
-    return t.device
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return t.shape
 
 
-def _launch(fn: str, dev: torch.device, *args):
-    if dev.index != torch.cuda.current_device():
+def _launch(fn, name: str, dev: int, *args):
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _launch(fn, dev, *args)
-    status = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
-        raise MoEError(fn, status)
+        raise MoEError(name, status)
 
 
-def _on_stream(call):
-    """Adds a keyword `stream`: the call's allocations and launches then belong to that stream."""
-    @functools.wraps(call)
-    def wrapped(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        for t in (*args, *kw.values()):
-            if isinstance(t, torch.Tensor) and t.device != stream.device:
-                raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return wrapped
+def _on(stream, call, *args, **kw):
+    """The call with `stream` current, so that its allocations belong to that stream as its launches do."""
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor) and t.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _choice(table: dict, key, name: str) -> int:
@@ -395,58 +391,59 @@ def _choice(table: dict, key, name: str) -> int:
     return table[key]
 
 
-@_on_stream
 def moe_route_grouped(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
                       n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
                       scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None,
-                      topk_w: Optional[torch.Tensor] = None):
+                      topk_w: Optional[torch.Tensor] = None, stream=None):
     """Top-k routing by score + bias inside the best groups; returns (topk_idx, topk_w)."""
-    dev = _first(logits, "logits", 2)
-    T, E = logits.shape
+    if stream is not None:
+        return _on(stream, moe_route_grouped, logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale,
+                   topk_idx, topk_w)
+    T, E = _matrix(logits, "logits")
+    dev = logits.get_device()
     if topk_idx is None:
-        topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
     if topk_w is None:
-        topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-    _launch("moe_route_grouped", dev, _take(logits, "logits", torch.float32, (T, E), dev),
-            _take(bias, "bias", torch.float32, (E,), dev, True), T, E, k, _choice(SCORES, score, "score"), n_group,
-            topk_group, group_top, int(bool(renormalize)), scale, _take(topk_idx, "topk_idx", torch.int32, (T, k), dev),
-            _take(topk_w, "topk_w", torch.float32, (T, k), dev))
+        topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    f32 = torch.float32
+    _launch((_lib or lib()).moe_route_grouped, "moe_route_grouped", dev, _take(logits, "logits", f32, (T, E), dev),
+            _take(bias, "bias", f32, (E,), dev, True), T, E, k, _choice(SCORES, score, "score"), n_group, topk_group,
+            group_top, 1 if renormalize else 0, scale, _take(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+            _take(topk_w, "topk_w", f32, (T, k), dev))
     return topk_idx, topk_w
 
 
-@_on_stream
 def moe_route_grouped_backward(logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor,
                                score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
-                               d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+                               d_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_route_grouped's topk_w with respect to logits, for its choice topk_idx."""
-    dev = _first(logits, "logits", 2)
-    _first(topk_idx, "topk_idx", 2)
-    T, E = logits.shape
-    k = topk_idx.shape[1]
+    if stream is not None:
+        return _on(stream, moe_route_grouped_backward, logits, topk_idx, d_topk_w, score, renormalize, scale, d_logits)
+    T, E = _matrix(logits, "logits")
+    dev, k = logits.get_device(), _matrix(topk_idx, "topk_idx")[1]
     if d_logits is None:
         d_logits = torch.empty_like(logits)
-    _launch("moe_route_grouped_backward", dev, _take(logits, "logits", torch.float32, (T, E), dev),
-            _take(topk_idx, "topk_idx", torch.int32, (T, k), dev), _take(d_topk_w, "d_topk_w", torch.float32, (T, k), dev),
-            T, E, k, _choice(SCORES, score, "score"), int(bool(renormalize)), scale,
-            _take(d_logits, "d_logits", torch.float32, (T, E), dev))
+    f32 = torch.float32
+    _launch((_lib or lib()).moe_route_grouped_backward, "moe_route_grouped_backward", dev,
+            _take(logits, "logits", f32, (T, E), dev), _take(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+            _take(d_topk_w, "d_topk_w", f32, (T, k), dev), T, E, k, _choice(SCORES, score, "score"),
+            1 if renormalize else 0, scale, _take(d_logits, "d_logits", f32, (T, E), dev))
     return d_logits
 
 
-@_on_stream
 def moe_combine_backward(d_out: torch.Tensor, y_perm: torch.Tensor, inv_perm: torch.Tensor, topk_w: torch.Tensor,
-                         d_y_perm: Optional[torch.Tensor] = None, d_topk_w: Optional[torch.Tensor] = None):
+                         d_y_perm: Optional[torch.Tensor] = None, d_topk_w: Optional[torch.Tensor] = None, stream=None):
     """Gradients of moe_combine: (d_y_perm, d_topk_w); rows of d_y_perm that no slot names are left as they were."""
-    dev = _first(d_out, "d_out", 2)
-    _first(y_perm, "y_perm", 2)
-    _first(inv_perm, "inv_perm", 2)
-    T, H = d_out.shape
-    k, R_cap = inv_perm.shape[1], y_perm.shape[0]
+    if stream is not None:
+        return _on(stream, moe_combine_backward, d_out, y_perm, inv_perm, topk_w, d_y_perm, d_topk_w)
+    T, H = _matrix(d_out, "d_out")
+    dev, R_cap, k = d_out.get_device(), _matrix(y_perm, "y_perm")[0], _matrix(inv_perm, "inv_perm")[1]
     if d_y_perm is None:
         d_y_perm = torch.empty_like(y_perm)
     if d_topk_w is None:
-        d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        d_topk_w = torch.empty((T, k), dtype=torch.float32, device=d_out.device)
     f32 = torch.float32
-    _launch("moe_combine_backward", dev, _take(d_out, "d_out", f32, (T, H), dev),
+    _launch((_lib or lib()).moe_combine_backward, "moe_combine_backward", dev, _take(d_out, "d_out", f32, (T, H), dev),
             _take(y_perm, "y_perm", f32, (R_cap, H), dev), _take(inv_perm, "inv_perm", torch.int32, (T, k), dev),
             _take(topk_w, "topk_w", f32, (T, k), dev), T, k, H, R_cap, _take(d_y_perm, "d_y_perm", f32, (R_cap, H), dev),
             _take(d_topk_w, "d_topk_w", f32, (T, k), dev))
@@ -466,69 +463,71 @@ def _alloc_ws(nbytes: int, device) -> Optional[torch.Tensor]:
 
 
 def alloc_linear_workspace(M: int, N: int, K: int, act: str, device) -> Optional[torch.Tensor]:
-    """Workspace of moe_linear (None where this size needs none)."""
-    return _alloc_ws(linear_workspace_bytes(M, N, K, act), device)
+    """Workspace of moe_linear on that device (None where this size needs none)."""
+    with torch.cuda.device(device):
+        return _alloc_ws(linear_workspace_bytes(M, N, K, act), device)
 
 
 def alloc_linear_backward_workspace(M: int, N: int, K: int, act: str, device) -> Optional[torch.Tensor]:
-    return _alloc_ws(linear_backward_workspace_bytes(M, N, K, act), device)
+    """Workspace of moe_linear_backward on that device (None for no rows)."""
+    with torch.cuda.device(device):
+        return _alloc_ws(linear_backward_workspace_bytes(M, N, K, act), device)
 
 
-def _ws(ws: Optional[torch.Tensor], dev):
+def _ws(ws: Optional[torch.Tensor], dev: int):
     if ws is None:
         return None, 0
-    return _take(ws, "ws", torch.uint8, (ws.numel(),), dev), ws.numel()
+    n = ws.numel()
+    return _take(ws, "ws", torch.uint8, (n,), dev), n
 
 
-@_on_stream
 def moe_linear(x: torch.Tensor, w: torch.Tensor, w_up: Optional[torch.Tensor] = None,
                bias: Optional[torch.Tensor] = None, bias_up: Optional[torch.Tensor] = None, act: str = "none",
                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                out_dtype: torch.dtype = torch.bfloat16, z: Optional[torch.Tensor] = None,
-               z_up: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               z_up: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None,
                use_workspace: bool = True) -> torch.Tensor:
     """act(x . w^T + bias) (SwiGLU: silu(.) * (x . w_up^T + bias_up)) + residual; z, z_up: buffers for the
     pre-activations that moe_linear_backward needs.  out may be residual itself; its type wins over out_dtype."""
-    dev = _first(x, "x", 2)
-    _first(w, "w", 2)
-    (M, K), N = x.shape, w.shape[0]
-    bf, f32 = torch.bfloat16, torch.float32
+    if stream is not None:
+        return _on(stream, moe_linear, x, w, w_up, bias, bias_up, act, residual, out, out_dtype, z, z_up, ws,
+                   use_workspace=use_workspace)
+    (M, K), N = _matrix(x, "x"), _matrix(w, "w")[0]
+    dev, bf, f32 = x.get_device(), torch.bfloat16, torch.float32
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    od = _choice(OUT_DTYPES, out.dtype, "out's type")
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    odt = out.dtype
     a = _choice(LINEAR_ACTS, act, "act")
     if ws is None and use_workspace:
-        with torch.cuda.device(dev):
-            ws = alloc_linear_workspace(M, N, K, act, dev)
+        ws = alloc_linear_workspace(M, N, K, act, x.device)
     wsp, wsn = _ws(ws, dev)
-    _launch("moe_linear", dev, _take(x, "x", bf, (M, K), dev), _take(w, "w", bf, (N, K), dev),
+    mn = (M, N)
+    _launch((_lib or lib()).moe_linear, "moe_linear", dev, _take(x, "x", bf, (M, K), dev), _take(w, "w", bf, (N, K), dev),
             _take(w_up, "w_up", bf, (N, K), dev, True), _take(bias, "bias", f32, (N,), dev, True),
-            _take(bias_up, "bias_up", f32, (N,), dev, True), _take(residual, "residual", out.dtype, (M, N), dev, True),
-            M, N, K, a, od, _take(z, "z", bf, (M, N), dev, True), _take(z_up, "z_up", bf, (M, N), dev, True),
-            _take(out, "out", out.dtype, (M, N), dev), wsp, wsn)
+            _take(bias_up, "bias_up", f32, (N,), dev, True), _take(residual, "residual", odt, mn, dev, True), M, N, K, a,
+            _choice(OUT_DTYPES, odt, "out's type"), _take(z, "z", bf, mn, dev, True), _take(z_up, "z_up", bf, mn, dev, True),
+            _take(out, "out", odt, mn, dev), wsp, wsn)
     return out
 
 
-@_on_stream
 def moe_linear_backward(d_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor, w_up: Optional[torch.Tensor] = None,
                         act: str = "none", z: Optional[torch.Tensor] = None, z_up: Optional[torch.Tensor] = None,
                         d_x: Optional[torch.Tensor] = None, d_w: Optional[torch.Tensor] = None,
                         d_w_up: Optional[torch.Tensor] = None, d_bias: Optional[torch.Tensor] = None,
-                        d_bias_up: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> None:
+                        d_bias_up: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradients of moe_linear, written into those of d_x, d_w, d_w_up, d_bias, d_bias_up that are given."""
-    dev = _first(x, "x", 2)
-    _first(w, "w", 2)
-    (M, K), N = x.shape, w.shape[0]
-    bf, f32 = torch.bfloat16, torch.float32
-    od = _choice(OUT_DTYPES, d_out.dtype, "d_out's type")
+    if stream is not None:
+        return _on(stream, moe_linear_backward, d_out, x, w, w_up, act, z, z_up, d_x, d_w, d_w_up, d_bias, d_bias_up, ws)
+    (M, K), N = _matrix(x, "x"), _matrix(w, "w")[0]
+    dev, bf, f32 = x.get_device(), torch.bfloat16, torch.float32
     a = _choice(LINEAR_ACTS, act, "act")
     if ws is None:
-        with torch.cuda.device(dev):
-            ws = alloc_linear_backward_workspace(M, N, K, act, dev)
+        ws = alloc_linear_backward_workspace(M, N, K, act, x.device)
     wsp, wsn = _ws(ws, dev)
-    _launch("moe_linear_backward", dev, _take(d_out, "d_out", d_out.dtype, (M, N), dev),
-            _take(x, "x", bf, (M, K), dev), _take(w, "w", bf, (N, K), dev), _take(w_up, "w_up", bf, (N, K), dev, True),
-            _take(z, "z", bf, (M, N), dev, True), _take(z_up, "z_up", bf, (M, N), dev, True), M, N, K, a, od,
-            _take(d_x, "d_x", bf, (M, K), dev, True), _take(d_w, "d_w", bf, (N, K), dev, True),
-            _take(d_w_up, "d_w_up", bf, (N, K), dev, True), _take(d_bias, "d_bias", f32, (N,), dev, True),
-            _take(d_bias_up, "d_bias_up", f32, (N,), dev, True), wsp, wsn)
+    mn, mk, nk = (M, N), (M, K), (N, K)
+    _launch((_lib or lib()).moe_linear_backward, "moe_linear_backward", dev, _take(d_out, "d_out", d_out.dtype, mn, dev),
+            _take(x, "x", bf, mk, dev), _take(w, "w", bf, nk, dev), _take(w_up, "w_up", bf, nk, dev, True),
+            _take(z, "z", bf, mn, dev, True), _take(z_up, "z_up", bf, mn, dev, True), M, N, K, a,
+            _choice(OUT_DTYPES, d_out.dtype, "d_out's type"), _take(d_x, "d_x", bf, mk, dev, True),
+            _take(d_w, "d_w", bf, nk, dev, True), _take(d_w_up, "d_w_up", bf, nk, dev, True),
+            _take(d_bias, "d_bias", f32, (N,), dev, True), _take(d_bias_up, "d_bias_up", f32, (N,), dev, True), wsp, wsn)
