@@ -4,9 +4,10 @@
 //   d_topk_w[t, j]              = sum_h d_out[t, h] * y_perm[inv_perm[t, j], h]
 //
 // HBM-bound: d_out and the routed rows of y_perm are read once, the routed rows
-// of d_y_perm written once.  A block owns one token; each thread holds float4
-// columns of d_out and one partial dot product per slot, which the block sums
-// in a fixed order (no atomics).
+// of d_y_perm written once.  A block owns one token and holds V float4 columns
+// of d_out a thread; it takes the token's local slots one by one, the next
+// slot's row in flight while one is used, and adds the block's partial dot
+// products in a fixed order (no atomics).
 #include "operators.h"
 
 namespace moe {
@@ -14,44 +15,74 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// KS >= k slots (unrolled, guarded by k).
-template <int KS>
+// Sum over the wavefront, in every lane: quad swaps and mirrors inside a row of 16 lanes, then the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int x = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float of_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  return (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
+}
+
+// V: float4 columns per thread and span of a row (a block covers up to 4096 columns at once).
+template <int V>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
     const floatx4* __restrict__ d_out, const floatx4* __restrict__ y_perm, const int32_t* __restrict__ inv_perm,
     const float* __restrict__ topk_w, int k, int H4, int64_t R_cap, floatx4* __restrict__ d_y,
     float* __restrict__ d_w) {
-  __shared__ float s_part[kThreads / kWave][KS];
+  __shared__ float s_part[kThreads / kWave][32];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  int row[KS];
-  float w[KS], dot[KS];
+  // The token's next local slot after j (k: none) and its row; block-uniform.
+  auto next = [&](int& j, int64_t& row) {
+    for (++j; j < k; ++j) {
+      row = inv_perm[t * k + j];
+      if (row >= 0 && row < R_cap) break;
+    }
+  };
+  if (lane < 32) s_part[wv][lane] = 0.f;
+  for (int c0 = threadIdx.x; c0 - (int)threadIdx.x < H4; c0 += kThreads * V) {
+    floatx4 g[V], y[2][V];
+    auto load = [&](floatx4 (&x)[V], const floatx4* p) {
 #pragma unroll
-  for (int j = 0; j < KS; ++j) {
-    const int p = j < k ? inv_perm[t * k + j] : -1;
-    row[j] = (p >= 0 && p < R_cap) ? p : -1;
-    w[j] = j < k ? topk_w[t * k + j] : 0.f;
-    dot[j] = 0.f;
-  }
-  for (int c = threadIdx.x; c < H4; c += kThreads) {
-    const floatx4 g = __builtin_nontemporal_load(d_out + t * H4 + c);
-    floatx4 y[KS];
-#pragma unroll
-    for (int j = 0; j < KS; ++j)
-      if (row[j] >= 0) y[j] = __builtin_nontemporal_load(y_perm + (int64_t)row[j] * H4 + c);
-#pragma unroll
-    for (int j = 0; j < KS; ++j)
-      if (row[j] >= 0) {
-        __builtin_nontemporal_store(w[j] * g, d_y + (int64_t)row[j] * H4 + c);
-        const floatx4 p = g * y[j];
-        dot[j] += (p[0] + p[1]) + (p[2] + p[3]);
+      for (int v = 0; v < V; ++v) {
+        const int c = c0 + v * kThreads;
+        x[v] = c < H4 ? __builtin_nontemporal_load(p + c) : floatx4{0.f, 0.f, 0.f, 0.f};
       }
-  }
+    };
+    load(g, d_out + t * H4);
+    int j = -1, jn;
+    int64_t row = 0, rn = 0;
+    next(j, row);
+    if (j < k) load(y[0], y_perm + row * H4);
+    while (j < k) {
+      jn = j;
+      next(jn, rn);
+      if (jn < k) load(y[1], y_perm + rn * H4);
+      const float w = topk_w[t * k + j];
+      float dot = 0.f;
 #pragma unroll
-  for (int j = 0; j < KS; ++j) {
-    float v = dot[j];
+      for (int v = 0; v < V; ++v) {
+        const int c = c0 + v * kThreads;
+        if (c < H4) __builtin_nontemporal_store(w * g[v], d_y + row * H4 + c);
+        const floatx4 p = g[v] * y[0][v];
+        dot += (p[0] + p[1]) + (p[2] + p[3]);
+      }
+      dot = wave_sum(dot);
+      if (lane == 0) s_part[wv][j] += dot;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    if (lane == 0) s_part[wv][j] = v;
+      for (int v = 0; v < V; ++v) y[0][v] = y[1][v];
+      j = jn;
+      row = rn;
+    }
   }
   __syncthreads();
   if ((int)threadIdx.x < k)
@@ -68,15 +99,13 @@ hipError_t launch_combine_backward(const float* d_out, const float* y_perm, cons
   const floatx4* g = reinterpret_cast<const floatx4*>(d_out);
   const floatx4* y = reinterpret_cast<const floatx4*>(y_perm);
   floatx4* d_y = reinterpret_cast<floatx4*>(d_y_perm);
-#define MOE_COMBINE_BWD(KS_)                                                                                 \
-  hipLaunchKernelGGL(combine_backward_kernel<KS_>, dim3((unsigned)T), dim3(kThreads), 0, s, g, y, inv_perm, \
+#define MOE_COMBINE_BWD(V_)                                                                                \
+  hipLaunchKernelGGL(combine_backward_kernel<V_>, dim3((unsigned)T), dim3(kThreads), 0, s, g, y, inv_perm, \
                      topk_w, k, H4, R_cap, d_y, d_topk_w)
-  if (k <= 1) MOE_COMBINE_BWD(1);
-  else if (k <= 2) MOE_COMBINE_BWD(2);
-  else if (k <= 4) MOE_COMBINE_BWD(4);
-  else if (k <= 8) MOE_COMBINE_BWD(8);
-  else if (k <= 16) MOE_COMBINE_BWD(16);
-  else MOE_COMBINE_BWD(32);
+  // Columns per thread: a row in one span if it has 4096 columns or fewer.
+  if (H4 > 2 * kThreads) MOE_COMBINE_BWD(4);
+  else if (H4 > kThreads) MOE_COMBINE_BWD(2);
+  else MOE_COMBINE_BWD(1);
 #undef MOE_COMBINE_BWD
   return hipGetLastError();
 }

@@ -275,7 +275,7 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// One BM x BN output tile per workgroup (NMAT = 2: BN columns of both matrices), NW wavefronts in 2 x NW / 2.
+// One BM x BN output tile per workgroup (NMAT = 2: BN columns of both matrices), WM x WN wavefronts.
 //
 // Two LDS buffers and register-staged loads: while stage kt is computed from one buffer, stage kt + 1 goes from
 // registers into the other and the registers reload with stage kt + 2.  A stage is four phases, the two halves of
@@ -283,11 +283,12 @@ __device__ __forceinline__ void ring_barrier() {
 // and LDS writes and loads are spread over the MFMAs of the first three.  All of a stage's fragments have been read
 // when its last phase begins: there the workgroup synchronises, and the last phase reads the next stage's first
 // fragments.  Stages past the end load through a resource of no bytes, so every iteration is the same.
-template <int BM, int BN, bool A_COLS, bool B_COLS, int NMAT, int NW>
+template <int BM, int BN, bool A_COLS, bool B_COLS, int NMAT, int WM, int WN>
 struct Tile {
+  static constexpr int NW = WM * WN;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + NMAT * B_BYTES;
-  static constexpr int WT_M = BM / 2, WT_N = BN / (NW / 2);         // wave tile (per matrix)
+  static constexpr int WT_M = BM / WM, WT_N = BN / WN;              // wave tile (per matrix)
   static constexpr int TM = WT_M / 16, TN = WT_N / 16;
   static constexpr int HM = TM / 2, NB = NMAT * TN;                // fragments of half the rows; of the columns
   static constexpr int A_PIECES = BM / (8 * NW), B_PIECES = BN / (8 * NW);  // loads per wavefront and stage
@@ -295,7 +296,7 @@ struct Tile {
   static constexpr int NMFMA = HM * NB;                             // per phase
   static constexpr int PS = (LOADS + 2) / 3;                        // pieces per phase
   static constexpr int PITCH = NMAT * BN + 4;                       // floats per row of the staged result
-  static constexpr int SMEM = 2 * STAGE > 64 * PITCH * 4 ? 2 * STAGE : 64 * PITCH * 4;
+  static constexpr int SMEM = 2 * STAGE > WM * 32 * PITCH * 4 ? 2 * STAGE : WM * 32 * PITCH * 4;
   static_assert(HM >= 1 && TN >= 1 && A_PIECES >= 1 && B_PIECES >= 1, "tile too small for the wavefronts");
 
   // An operand's C rows (columns) from c0 on, as this lane loads them.  Stage kt is read through a resource based
@@ -349,7 +350,7 @@ struct Tile {
   static __device__ __forceinline__ void run(char* smem, const Gemm& g, int64_t m0, int n0, int k0, int k1,
                                              float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / (NW / 2), wn = wave % (NW / 2);
+    const int wm = wave / WN, wn = wave % WN;
     const Source<A_COLS, BM> src_a(g.a, m0, A_COLS ? g.seg : g.nk, k1, wave, lane);
     const Source<B_COLS, BN> src_b(g.b, n0, g.seg, k1, wave, lane);
     const Source<B_COLS, BN> src_u(NMAT == 2 ? g.b_up : g.b, n0, g.seg, k1, wave, lane);
@@ -477,7 +478,7 @@ struct Tile {
       order(integral_constant<int, RA + RB>{}, integral_constant<int, 0>{});
     }
 
-    // Epilogue: 32 rows of either half at a time through LDS, so that global memory is accessed along rows.  The
+    // Epilogue: 32 rows of each wavefront row at a time through LDS, so that global memory is accessed along rows.  The
     // columns' side feeds the MFMA's rows, so a lane holds, for row lane % 16 of a 16-row block, columns
     // 4 (lane / 16) + 0..3 of a 16-column block.
     float* sm = reinterpret_cast<float*>(smem);
@@ -503,10 +504,10 @@ struct Tile {
       }
       wait_lgkm0();
       ring_barrier();
-      // The 32 rows of the upper and of the lower half of the tile, NV rows of this thread's columns at a time.
+      // NV rows of this thread's columns at a time.
       auto rows = [&](auto f) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < WM; ++h)
 #pragma unroll 1
           for (int r0 = 0; r0 < 32; r0 += NV * STEP) {
             floatx4 v[NV], u[NV];
@@ -517,7 +518,7 @@ struct Tile {
               v[r] = *reinterpret_cast<const floatx4*>(p);
               u[r] = NMAT == 2 ? *reinterpret_cast<const floatx4*>(p + BN) : floatx4{0.f, 0.f, 0.f, 0.f};
             }
-            f(h * (BM / 2) + i * 32 + rt, v, u);
+            f(h * WT_M + i * 32 + rt, v, u);
           }
       };
       if (part) {
@@ -558,13 +559,14 @@ __device__ __forceinline__ void tile_of(int bid, int G, int mt, int nt, int tile
 
 // Tile kinds: rows, columns staged per stage (of one matrix, or half of each of two), wavefronts, workgroups per CU.
 struct Kind {
-  int bm, bn, nw, per_cu;
+  int bm, bn, wm, wn, per_cu;
+  constexpr int threads() const { return wm * wn * 64; }
 };
-constexpr Kind kKinds[] = {{256, 256, 8, 1}, {128, 128, 4, 2}, {64, 128, 4, 3}};
-constexpr int kNumKinds = 3;
+constexpr Kind kKinds[] = {{256, 256, 2, 4, 1}, {256, 128, 4, 2, 1}, {128, 128, 2, 2, 2}, {64, 128, 2, 2, 3}};
+constexpr int kNumKinds = 4;
 
 template <int KIND, bool A_COLS, bool B_COLS, int NMAT>
-using KindTile = Tile<kKinds[KIND].bm, kKinds[KIND].bn / NMAT, A_COLS, B_COLS, NMAT, kKinds[KIND].nw>;
+using KindTile = Tile<kKinds[KIND].bm, kKinds[KIND].bn / NMAT, A_COLS, B_COLS, NMAT, kKinds[KIND].wm, kKinds[KIND].wn>;
 
 // One product of a launch: its tiles times S slices of the reduction, slice q covering stages
 // [q nk / S, (q + 1) nk / S).  With S > 1 slice q of tile t leaves fp32 sums at part + (q tiles + t) (tile floats),
@@ -589,7 +591,7 @@ __device__ __forceinline__ void run_job(char* smem, const Job& j, int bid) {
 }
 
 template <int KIND, int NMAT>
-__global__ __launch_bounds__(kKinds[KIND].nw * 64, KIND == 2 ? 3 : 2) void forward_kernel(Job j) {
+__global__ __launch_bounds__(kKinds[KIND].threads(), KIND == 3 ? 3 : 2) void forward_kernel(Job j) {
   __shared__ __attribute__((aligned(1024))) char smem[KindTile<KIND, false, false, NMAT>::SMEM];
   run_job<KIND, false, false, NMAT>(smem, j, blockIdx.x);
 }
@@ -825,16 +827,16 @@ __device__ __forceinline__ void bias_sum(char* smem, const BiasSums& b, int bid)
 }
 
 // The backward pass's products in one launch, so that the tiles of one fill the CUs that another leaves idle: the
-// weight gradients (both operands columns; jobs 0 .. nw - 1), the input gradient (rows, columns; the last job) and
-// the bias gradients (from workgroup bias_first on).
+// input gradient (rows, columns; jobs 0 .. nx - 1, at most one; ahead of the others by 2-4 % at 8192 x 2816 x 2048),
+// the weight gradients (both operands columns) and the bias gradients (from workgroup bias_first on).
 struct BackwardJobs {
   Job j[3];
-  int n, nw, bias_first;
+  int n, nx, bias_first;
   BiasSums bias;
 };
 
 template <int KIND>
-__global__ __launch_bounds__(kKinds[KIND].nw * 64, KIND == 2 ? 3 : 2) void backward_kernel(BackwardJobs b) {
+__global__ __launch_bounds__(kKinds[KIND].threads(), KIND == 3 ? 3 : 2) void backward_kernel(BackwardJobs b) {
   using TW = KindTile<KIND, true, true, 1>;
   using TX = KindTile<KIND, false, true, 1>;
   __shared__ __attribute__((aligned(1024))) char smem[TW::SMEM > TX::SMEM ? TW::SMEM : TX::SMEM];
@@ -845,7 +847,7 @@ __global__ __launch_bounds__(kKinds[KIND].nw * 64, KIND == 2 ? 3 : 2) void backw
   int q = 0;
   while (q + 1 < b.n && (int)blockIdx.x >= b.j[q + 1].first) ++q;
   const int bid = blockIdx.x - b.j[q].first;
-  if (q < b.nw) run_job<KIND, true, true, 1>(smem, b.j[q], bid);
+  if (q >= b.nx) run_job<KIND, true, true, 1>(smem, b.j[q], bid);
   else run_job<KIND, false, true, 1>(smem, b.j[q], bid);
 }
 
@@ -897,6 +899,7 @@ struct Plan {
   int S[3];
   int64_t tiles[3];
   size_t part_bytes[3];  // fp32 sums of a split product
+  double time;           // estimated us
 };
 
 // CUs of the current device (256 if it cannot be asked), looked up once per device.
@@ -917,13 +920,13 @@ constexpr int kMaxSlices = 16;
 // per_cu of them at a time, a stage of r workgroups taking max(latency, r * rate), plus a fixed cost per workgroup;
 // a split adds the second launch and its traffic.
 Plan make_plan(const Size* z, int n, int nmat, bool split) {
-  constexpr double kRate[] = {1.5, 0.53, 0.32};      // us a stage and workgroup, CU full
-  constexpr double kLatency[] = {1.15, 0.58, 0.42};  // us a stage, at least
-  constexpr double kFixed[] = {9.0, 5.0, 3.5};       // us a workgroup: first stage's latency and epilogue
+  constexpr double kRate[] = {1.5, 0.93, 0.53, 0.32};      // us a stage and workgroup, CU full
+  constexpr double kLatency[] = {1.1, 0.73, 0.56, 0.42};   // us a stage, at least
+  constexpr double kFixed[] = {9.0, 6.0, 5.0, 3.5};        // us a workgroup: first stage's latency and epilogue
   constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
   const int cus = device_cus();
   Plan best{};
-  double best_t = 1e30;
+  best.time = 1e30;
   for (int kind = 0; kind < kNumKinds; ++kind) {
     const int bm = kKinds[kind].bm, bn = kKinds[kind].bn / nmat, occ = kKinds[kind].per_cu;
     for (int S = 1; S <= (split ? kMaxSlices : 1); ++S) {
@@ -957,10 +960,8 @@ Plan make_plan(const Size* z, int n, int nmat, bool split) {
         left -= r;
       }
       if (bytes > 0) t += kSecond + bytes / kBytes;
-      if (t < best_t) {
-        best_t = t;
-        best = p;
-      }
+      p.time = t;
+      if (t < best.time) best = p;
     }
   }
   return best;
@@ -981,38 +982,73 @@ unsigned reduce_blocks(const Job& j) { return (unsigned)((j.g.M * ((j.g.N + 3) /
 
 constexpr int kSkinnyRows = 16;  // up to here moe_linear streams the weights
 
+// How moe_linear runs: `rest` last rows stream the weights, the rows before them (if any) go through tiles.  A few
+// rows over a multiple of the tile would cost a whole row of tiles (4099 x 2048 x 2816: 66 us against 50 + 7).
+struct ForwardPlan {
+  int rest;
+  Plan tiles;
+};
+ForwardPlan forward_plan(int64_t M, int N, int K, int nmat, bool split) {
+  ForwardPlan f{};
+  if (M <= kSkinnyRows) {
+    f.rest = (int)M;
+    return f;
+  }
+  const Size all{M, N, stages(K)};
+  f.tiles = make_plan(&all, 1, nmat, split);
+  const int rest = (int)(M % 64);
+  if (rest == 0 || rest > kSkinnyRows || M < 64) return f;
+  const Size most{M - rest, N, all.nk};
+  const Plan p = make_plan(&most, 1, nmat, split);
+  // A launch, and the weights once more at the rate that they stream from the last-level cache.
+  if (p.time + 4.0 + (double)N * K * 2 * nmat / 4.0e6 < f.tiles.time) {
+    f.rest = rest;
+    f.tiles = p;
+  }
+  return f;
+}
+
 }  // namespace
 
 size_t linear_ws_bytes(int64_t M, int N, int K, int act) {
-  if (M <= kSkinnyRows) return 0;
-  const Size z{M, N, stages(K)};
-  return part_bytes(make_plan(&z, 1, act == ACT_SWIGLU ? 2 : 1, true), 1);
+  return part_bytes(forward_plan(M, N, K, act == ACT_SWIGLU ? 2 : 1, true).tiles, 1);
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
-  Job j{};
-  Gemm& g = j.g;
-  g.a = {a.x, nullptr, a.K, a.M, a.K};
-  g.b = {a.w, nullptr, a.K, a.N, a.K};
-  g.b_up = {a.w_up, nullptr, a.K, a.N, a.K};
-  g.M = a.M;
-  g.N = a.N;
-  g.nk = g.seg = stages(a.K);
-  g.e = {a.bias, a.bias_up, a.residual, a.out, a.z, a.z_up, a.act, a.out_f32};
   const bool dual = a.act == ACT_SWIGLU;
   const int nmat = dual ? 2 : 1;
-  if (a.M <= kSkinnyRows) {
+  const ForwardPlan f = forward_plan(a.M, a.N, a.K, nmat, a.ws != nullptr);
+  const int64_t main = a.M - f.rest;
+  // The product of rows [row, row + rows).
+  auto product = [&](int64_t row, int64_t rows) {
+    Gemm g{};
+    g.a = {a.x + row * a.K, nullptr, a.K, rows, a.K};
+    g.b = {a.w, nullptr, a.K, a.N, a.K};
+    g.b_up = {a.w_up, nullptr, a.K, a.N, a.K};
+    g.M = rows;
+    g.N = a.N;
+    g.nk = g.seg = stages(a.K);
+    const int64_t at = row * a.N, es = a.out_f32 ? 4 : 2;
+    g.e = {a.bias, a.bias_up, a.residual ? static_cast<const char*>(a.residual) + at * es : nullptr,
+           static_cast<char*>(a.out) + at * es, a.z ? a.z + at : nullptr, a.z_up ? a.z_up + at : nullptr, a.act, a.out_f32};
+    return g;
+  };
+  hipError_t e = hipSuccess;
+  if (f.rest > 0) {
+    const Gemm g = product(main, f.rest);
     if (dual) hipLaunchKernelGGL((skinny_kernel<true, 8, 2>), dim3((a.N + 7) / 8), dim3(512), 0, s, g);
     else hipLaunchKernelGGL((skinny_kernel<false, 8, 2>), dim3((a.N + 15) / 16), dim3(512), 0, s, g);
-    return hipGetLastError();
+    e = hipGetLastError();
   }
-  const Size z{a.M, a.N, g.nk};
-  const Plan p = make_plan(&z, 1, nmat, a.ws != nullptr);
+  if (main == 0 || e != hipSuccess) return e;
+  const Plan& p = f.tiles;
   if (p.tiles[0] < 1) return hipErrorInvalidValue;
-  set_tiles(g, p.kind, nmat);
+  Job j{};
+  j.g = product(0, main);
+  set_tiles(j.g, p.kind, nmat);
   j.S = p.S[0];
   j.part = static_cast<float*>(a.ws);
-  const dim3 grid((unsigned)(p.tiles[0] * j.S)), block(kKinds[p.kind].nw * 64);
+  const dim3 grid((unsigned)(p.tiles[0] * j.S)), block(kKinds[p.kind].threads());
 #define MOE_FORWARD(KIND_)                                                             \
   do {                                                                                 \
     if (dual) hipLaunchKernelGGL((forward_kernel<KIND_, 2>), grid, block, 0, s, j);    \
@@ -1020,9 +1056,10 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   } while (0)
   if (p.kind == 0) MOE_FORWARD(0);
   else if (p.kind == 1) MOE_FORWARD(1);
-  else MOE_FORWARD(2);
+  else if (p.kind == 2) MOE_FORWARD(2);
+  else MOE_FORWARD(3);
 #undef MOE_FORWARD
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e == hipSuccess && j.S > 1) {
     hipLaunchKernelGGL(reduce_kernel, dim3(reduce_blocks(j)), dim3(256), 0, s, j, kKinds[p.kind].bm,
                        kKinds[p.kind].bn / nmat, nmat);
@@ -1039,7 +1076,7 @@ struct BackwardLayout {
   Plan plan;
 };
 
-// Products in the order of the launch: the weight gradients, then the input gradient.
+// Products in the order of the plan: the weight gradients, then the input gradient.
 static BackwardLayout backward_layout(int64_t M, int N, int K, int act) {
   BackwardLayout l{};
   l.mats = act == ACT_SWIGLU ? 2 : 1;
@@ -1109,6 +1146,18 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
     j.part = reinterpret_cast<float*>(parts + off);
     blocks += l.plan.tiles[q] * j.S;
   };
+  if (a.d_x) {
+    Gemm g{};
+    g.a = {dz, nullptr, ld, a.M, ld};
+    g.b = {a.w, a.w_up, a.K, a.K, a.N};
+    g.M = a.M;
+    g.N = a.K;
+    g.seg = stages(a.N);
+    g.nk = mats * g.seg;
+    g.e.out = a.d_x;
+    add(g, mats);
+  }
+  jobs.nx = jobs.n;
   for (int m = 0; m < mats; ++m) {
     uint16_t* d_w = m ? a.d_w_up : a.d_w;
     if (!d_w) continue;
@@ -1121,28 +1170,17 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
     g.e.out = d_w;
     add(g, m);
   }
-  jobs.nw = jobs.n;
-  if (a.d_x) {
-    Gemm g{};
-    g.a = {dz, nullptr, ld, a.M, ld};
-    g.b = {a.w, a.w_up, a.K, a.K, a.N};
-    g.M = a.M;
-    g.N = a.K;
-    g.seg = stages(a.N);
-    g.nk = mats * g.seg;
-    g.e.out = a.d_x;
-    add(g, mats);
-  }
   jobs.bias_first = (int)blocks;
   jobs.bias = {sums, l.blocks, a.N, mats, a.d_bias, a.d_bias_up};
   if (bias) blocks += (mats * (int64_t)a.N + 63) / 64;
   if (blocks == 0) return hipSuccess;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const Kind& kind = kKinds[l.plan.kind];
-  const dim3 grid((unsigned)blocks), block(kind.nw * 64);
+  const dim3 grid((unsigned)blocks), block(kind.threads());
   if (l.plan.kind == 0) hipLaunchKernelGGL(backward_kernel<0>, grid, block, 0, s, jobs);
   else if (l.plan.kind == 1) hipLaunchKernelGGL(backward_kernel<1>, grid, block, 0, s, jobs);
-  else hipLaunchKernelGGL(backward_kernel<2>, grid, block, 0, s, jobs);
+  else if (l.plan.kind == 2) hipLaunchKernelGGL(backward_kernel<2>, grid, block, 0, s, jobs);
+  else hipLaunchKernelGGL(backward_kernel<3>, grid, block, 0, s, jobs);
   hipError_t e = hipGetLastError();
   unsigned most = 0;
   for (int q = 0; q < jobs.n; ++q)
