@@ -82,14 +82,9 @@ __device__ __forceinline__ float exp_of(float z) {
   const float t = z * 1.4426950408889634f;
   return __builtin_amdgcn_exp2f(t) * fmaf(fmaf(z, 1.4426950408889634f, -t), 0.69314718055994531f, 1.f);
 }
-__device__ __forceinline__ double exp_of(double z) { return exp(z); }
 __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
-__device__ __forceinline__ double inverse(double v) { return 1.0 / v; }
 // 1 / (1 + e^-z)
-template <typename K>
-__device__ __forceinline__ K sigmoid_of(K z) {
-  return inverse((K)1 + exp_of(-z));
-}
+__device__ __forceinline__ float sigmoid_of(float z) { return inverse(1.f + exp_of(-z)); }
 
 // Scaled score of a chosen logit for renormalised weights: both scores times a common factor that keeps the largest
 // of the row at least 1/2: softmax e^(l - top), sigmoid(l) = e^min(l, 0) / (1 + e^-|l|) with e^min(l, 0) scaled by
@@ -119,136 +114,201 @@ struct Place {
   bool vec4;  // rows and groups are whole 16-byte pieces
 };
 
-// Chooses the k experts of a token held by LT lanes into ids[0, k) (-1: none), given this lane's logits x (-inf: not
-// available), and returns whether keys of type K leave the choice in doubt.  m: the row's largest logit, or 0 for
-// sigmoid.  The best of a lane are sorted in registers, so a round of the selection is a maximum over the heads.
-//
-// K = float: keys are logits without a bias (exact), else score + bias, off by at most delta = 1.25e-6 + 2.4e-7
-// max |key| (score: exp2 and reciprocal 1 ulp each, the softmax's common denominator 5e-7 of it; bias: one
-// rounding).  Two keys in a row within 2 delta (equal ones, whose order is by id, among them), or the last kept and
-// the first dropped group within 5 delta, leave it in doubt.
-// K = double: nothing does; equal keys go by id.
-template <int LT, int PL, typename K>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const Place& pl, int l, int lane, int e0, const float (&x)[PL],
-                                       const float (&b)[PL], float m, int* ids, float& z) {
-  constexpr bool F32 = sizeof(K) == 4;
-  const K none = -INFINITY;
-  const int k = a.k;
-  K key[PL];
-  int id[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) id[i] = e0 + i;
-  K zz = 1;
-  if (!a.sigmoid && (a.bias || !a.renormalize)) {
-    K s = 0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s += x[i] > -INFINITY ? exp_of((K)x[i] - (K)m) : (K)0;
-    zz = sum_of<LT>(s);
-    z = (float)zz;
-  }
-  const K iz = inverse(zz);
-  auto score = [&](K v) { return a.sigmoid ? sigmoid_of(v) : exp_of(v - (K)m) * iz; };
-  float delta = 0.f;
-  if (a.bias) {
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const bool ok = x[i] > -INFINITY;
-      key[i] = ok ? score((K)x[i]) + (K)b[i] : none;
-      if (F32) big = fmaxf(big, ok ? fabsf((float)key[i]) : 0.f);
-    }
-    if (F32) delta = 1.25e-6f + 2.4e-7f * max_of<LT>(big);
+// Ranks a lane's group among the others: the number of lanes of better groups, `better(o, mine, h)` saying whether
+// group h of sum o comes ahead.
+template <int LT, typename K, typename F>
+__device__ __forceinline__ int lanes_ahead(const Place& pl, K sum, F better) {
+  int ahead = 0;
+  if constexpr (LT == 16) {
+#define MOE_ROR(N) ahead += better(dpp<0x120 + N>(sum), sum, -1) ? 1 : 0;
+    MOE_ROR(1) MOE_ROR(2) MOE_ROR(3) MOE_ROR(4) MOE_ROR(5) MOE_ROR(6) MOE_ROR(7) MOE_ROR(8)
+    MOE_ROR(9) MOE_ROR(10) MOE_ROR(11) MOE_ROR(12) MOE_ROR(13) MOE_ROR(14) MOE_ROR(15)
+#undef MOE_ROR
   } else {
+    for (int h = 0; h < pl.n_group; ++h)
+      ahead += (better(of_lane(sum, h << pl.lg_bits), sum, h) ? 1 : 0) << pl.lg_bits;
+  }
+  return ahead;
+}
+
+// The two largest keys of a group, from each lane's two largest.
+template <int LT, typename K>
+__device__ __forceinline__ void group_best(const Place& pl, K& g1, K& g2) {
+  auto merge = [&](K o1, K o2) {
+    g2 = max2(min2(g1, o1), max2(g2, o2));
+    g1 = max2(g1, o1);
+  };
+  if (pl.lg_bits >= 1) merge(dpp<0xB1>(g1), dpp<0xB1>(g2));
+  if (pl.lg_bits >= 2) merge(dpp<0x4E>(g1), dpp<0x4E>(g2));
+  if (pl.lg_bits >= 3) merge(dpp<0x141>(g1), dpp<0x141>(g2));
+  if (pl.lg_bits >= 4) merge(dpp<0x140>(g1), dpp<0x140>(g2));
+  if (LT == 64 && pl.lg_bits >= 5) merge(__shfl_xor(g1, 16), __shfl_xor(g2, 16));
+}
+
+// The lane of the token's LT lanes that takes a round: the first whose head is the largest key; false if none is left.
+template <int LT>
+__device__ __forceinline__ bool wins(bool head, int l, int lane) {
+  const unsigned long long at = __ballot(head);
+  if constexpr (LT == 64) return at != 0 && lane == __builtin_ctzll(at);
+  const uint32_t mine = (uint32_t)(at >> (lane & 48)) & 0xffffu;
+  return mine != 0 && l == __builtin_ctz(mine);
+}
+
+// Chooses the k experts of a token held by a wavefront into ids[0, k) (-1: none) by 64-bit keys, equal ones lowest id
+// first.  x: this lane's logits (-inf: not available), m: the row's largest (softmax).
+template <int PL>
+__device__ void choose_exact(const RouteArgs& a, const Place& pl, int lane, int e0, const float (&x)[PL],
+                             const float (&b)[PL], float m, int* ids) {
+  const double none = -INFINITY;
+  double key[PL];
+  int id[PL];
+  double iz = 1.0;
+  if (!a.sigmoid && a.bias) {
+    double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) key[i] = x[i];
+    for (int i = 0; i < PL; ++i) s += x[i] > -INFINITY ? exp((double)x[i] - (double)m) : 0.0;
+    iz = 1.0 / sum_of<64>(s);
+  }
+  auto score = [&](double v) { return a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)m) * iz; };
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    id[i] = e0 + i;
+    key[i] = !a.bias ? (double)x[i] : x[i] > -INFINITY ? score(x[i]) + (double)b[i] : none;
   }
   sort_network<PL>([&](int i, int j) {
-    const bool swap = key[j] > key[i] || (!F32 && key[j] == key[i] && id[j] < id[i]);
-    const K ki = key[i];
+    const bool swap = key[j] > key[i] || (key[j] == key[i] && id[j] < id[i]);
+    const double ki = key[i];
     const int ii = id[i];
     key[i] = swap ? key[j] : ki;
     key[j] = swap ? ki : key[j];
     id[i] = swap ? id[j] : ii;
     id[j] = swap ? ii : id[j];
   });
-
-  bool doubt = false;
   if (pl.n_group > 1) {
-    K g1 = key[0], g2 = PL > 1 ? key[PL > 1 ? 1 : 0] : none;
-    auto merge = [&](K o1, K o2) {
-      g2 = max2(min2(g1, o1), max2(g2, o2));
-      g1 = max2(g1, o1);
-    };
-    if (pl.lg_bits >= 1) merge(dpp<0xB1>(g1), dpp<0xB1>(g2));
-    if (pl.lg_bits >= 2) merge(dpp<0x4E>(g1), dpp<0x4E>(g2));
-    if (pl.lg_bits >= 3) merge(dpp<0x141>(g1), dpp<0x141>(g2));
-    if (pl.lg_bits >= 4) merge(dpp<0x140>(g1), dpp<0x140>(g2));
-    if (LT == 64 && pl.lg_bits >= 5) merge(__shfl_xor(g1, 16), __shfl_xor(g2, 16));
-    float gd = delta;
+    double g1 = key[0], g2 = PL > 1 ? key[PL > 1 ? 1 : 0] : none;
+    group_best<64>(pl, g1, g2);
     if (a.group_top == 2) {
       if (!a.bias) {
-        gd = 1.5e-6f;
         g1 = g1 > none ? score(g1) : g1;
         g2 = g2 > none ? score(g2) : g2;
       }
       if (g2 > none) g1 += g2;
     }
-    int ahead = 0;  // lanes of better groups
-    if constexpr (LT == 16) {
-#define MOE_ROR(N) ahead += dpp<0x120 + N>(g1) > g1 ? 1 : 0;
-      MOE_ROR(1) MOE_ROR(2) MOE_ROR(3) MOE_ROR(4) MOE_ROR(5) MOE_ROR(6) MOE_ROR(7) MOE_ROR(8)
-      MOE_ROR(9) MOE_ROR(10) MOE_ROR(11) MOE_ROR(12) MOE_ROR(13) MOE_ROR(14) MOE_ROR(15)
-#undef MOE_ROR
-    } else {
-      const int mine = l >> pl.lg_bits;
-      for (int h = 0; h < pl.n_group; ++h) {
-        const K o = of_lane(g1, h << pl.lg_bits);
-        ahead += (o > g1 || (!F32 && o == g1 && h < mine) ? 1 : 0) << pl.lg_bits;
-      }
-    }
-    const bool keep = ahead < (a.topk_group << pl.lg_bits);
-    if (F32) {
-      // Lanes of no group hold -inf and are ahead of nothing.  Equal groups can leave more than topk_group kept.
-      const bool in = keep && g1 > none;
-      const K low = -max_of<LT>(in ? -g1 : none), high = max_of<LT>(keep ? none : g1);
-      const K kept = sum_of<LT>(in ? (K)1 : (K)0);
-      doubt = low - high <= (K)(5.f * gd) || kept > (K)(a.topk_group << pl.lg_bits);
-    }
-    if (!keep)
+    const int mine = lane >> pl.lg_bits;
+    const int ahead = lanes_ahead<64>(pl, g1, [&](double o, double g, int h) { return o > g || (o == g && h < mine); });
+    if (ahead >= (a.topk_group << pl.lg_bits))
 #pragma unroll
       for (int i = 0; i < PL; ++i) key[i] = none;
+  }
+  if (lane < a.k) ids[lane] = -1;
+  wave_lds_order();
+  for (int j = 0; j < a.k; ++j) {
+    const double top = max_of<64>(key[0]);
+    if (wins<64>(key[0] == top && top > none, lane, lane)) {
+      ids[j] = id[0];
+#pragma unroll
+      for (int i = 0; i + 1 < PL; ++i) {
+        key[i] = key[i + 1];
+        id[i] = id[i + 1];
+      }
+      key[PL - 1] = none;
+    }
+  }
+  wave_lds_order();
+}
+
+// e^z and 1 / (1 + e^-z) by the hardware exp2 and reciprocal alone; z's rounding passes on at most 1.5e-8 of either
+// score, so both are within 5e-7.
+__device__ __forceinline__ float exp_fast(float z) { return __builtin_amdgcn_exp2f(z * 1.4426950408889634f); }
+__device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn_rcpf(1.f + exp_fast(-z)); }
+
+// The same for a token held by LT lanes, by fp32 keys; returns whether they leave the choice in doubt (then ids mean
+// nothing).  z: sum of e^(l - m), for the plain softmax's weights.
+//
+// A key's last log2(PL) bits hold its place on the lane, so the lane's keys are sorted by maxima and minima alone
+// (2 instructions an exchange; with the place beside it 5).  Keys (logits, or score + bias) are then off by at most
+// delta = PL 2^-23 max |key|, with a bias 1.25e-6 + 2.4e-7 max |key| more: scores within 5e-7, the softmax's
+// denominator 5e-7 of them, the sum's rounding.  Two keys in a row within 2 delta (equal ones, whose order is by id,
+// among them), or the last kept and the first dropped group within 5 delta, leave the choice in doubt, and so does an
+// available key next to the value that stands for none.
+template <int LT, int PL>
+__device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& pl, int l, int lane, int e0, const float (&x)[PL],
+                                            const float (&b)[PL], float m, int* ids, float& z) {
+  constexpr uint32_t kPlace = PL - 1;
+  constexpr float kNone = -3.402e38f, kLeast = -3.3e38f;  // no key; the least that is taken for one
+  const int k = a.k;
+  float key[PL];
+  bool doubt = false;
+  if (!a.sigmoid && (a.bias || !a.renormalize)) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s += exp_fast(x[i] - m);
+    z = sum_of<LT>(s);
+  }
+  const float iz = a.sigmoid ? 1.f : inverse(z);
+  auto score = [&](float v) { return a.sigmoid ? sigmoid_fast(v) : exp_fast(v - m) * iz; };
+  float big = 0.f, least = INFINITY;
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const bool ok = x[i] > -INFINITY;
+    const float v = !a.bias ? x[i] : score(x[i]) + b[i];
+    big = fmaxf(big, ok ? fabsf(v) : 0.f);
+    least = ok ? fminf(least, v) : least;
+    key[i] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, ok ? v : kNone) & ~kPlace) | (uint32_t)i);
+  }
+  doubt = least < kLeast;
+  const float delta = max_of<LT>(big) * (PL * 1.1920929e-7f + (a.bias ? 2.4e-7f : 0.f)) + (a.bias ? 1.25e-6f : 0.f);
+  sort_network<PL>([&](int i, int j) {
+    const float hi = fmaxf(key[i], key[j]), lo = fminf(key[i], key[j]);
+    key[i] = hi;
+    key[j] = lo;
+  });
+
+  if (pl.n_group > 1) {
+    float g1 = key[0], g2 = PL > 1 ? key[PL > 1 ? 1 : 0] : kNone;
+    group_best<LT>(pl, g1, g2);
+    float gd = delta;
+    if (a.group_top == 2) {
+      if (!a.bias) {
+        gd += 1.5e-6f;  // (a score changes by at most a quarter of its logit's change)
+        g1 = g1 > kLeast ? score(g1) : g1;
+        g2 = g2 > kLeast ? score(g2) : g2;
+      }
+      g1 = g2 > kLeast ? g1 + g2 : g1;
+    }
+    g1 = g1 > kLeast ? g1 : -INFINITY;
+    const int most = a.topk_group << pl.lg_bits;
+    const bool keep = lanes_ahead<LT>(pl, g1, [](float o, float g, int) { return o > g; }) < most;
+    // Lanes of no group are ahead of nothing.  Equal groups can leave more than topk_group kept.
+    const bool in = keep && g1 > -INFINITY;
+    const float low = -max_of<LT>(in ? -g1 : -INFINITY), high = max_of<LT>(keep ? -INFINITY : g1);
+    const float kept = sum_of<LT>(in ? 1.f : 0.f);
+    doubt = doubt || low - high <= 5.f * gd || kept > (float)most;
+    if (!keep)
+#pragma unroll
+      for (int i = 0; i < PL; ++i) key[i] = kNone;
   }
 
   if (l < k) ids[l] = -1;
   wave_lds_order();
-  K prev = INFINITY;
-  const K tol = 2.f * delta;
+  float prev = INFINITY;
+  const float tol = 2.f * delta + 1e-37f;
   for (int j = 0; j <= k; ++j) {  // a round more than slots: the first that misses has to miss clearly
-    const K top = max_of<LT>(key[0]);
-    if (F32) doubt = doubt || (top > none && prev - top <= tol);
+    const float top = max_of<LT>(key[0]);
+    doubt = doubt || (top > kLeast && prev - top <= tol);
     prev = top;
     if (j == k) break;
-    const unsigned long long at = __ballot(key[0] == top && top > none);
-    const uint32_t mine = LT == 64 ? 0 : (uint32_t)(at >> (lane & 48)) & 0xffffu;
-    const bool win = LT == 64 ? at != 0 && lane == __builtin_ctzll(at) : mine != 0 && l == __builtin_ctz(mine);
-    if (win) {
-      ids[j] = id[0];
-      // What lies deeper than k + 1 in a lane's list is not looked at.
-      constexpr int D = PL < 9 ? PL : 9;
+    if (wins<LT>(key[0] == top && top > kLeast, l, lane)) {
+      ids[j] = e0 + (int)(__builtin_bit_cast(uint32_t, top) & kPlace);
+      constexpr int D = PL < 9 ? PL : 9;  // what lies deeper than k + 1 in a lane's list is not looked at
 #pragma unroll
-      for (int i = 0; i + 1 < D; ++i) {
-        key[i] = key[i + 1];
-        id[i] = id[i + 1];
-      }
+      for (int i = 0; i + 1 < D; ++i) key[i] = key[i + 1];
       if (PL > D && k > 8) {
 #pragma unroll
-        for (int i = D - 1; i + 1 < PL; ++i) {
-          key[i] = key[i + 1];
-          id[i] = id[i + 1];
-        }
-        key[PL - 1] = none;
+        for (int i = D - 1; i + 1 < PL; ++i) key[i] = key[i + 1];
+        key[PL - 1] = kNone;
       } else {
-        key[D - 1] = none;
+        key[D - 1] = kNone;
       }
     }
   }
@@ -300,18 +360,21 @@ __device__ __forceinline__ int load_experts(const RouteArgs& a, const Place& pl,
   return e0;
 }
 
-// One token by a whole wavefront, with 64-bit keys; only the ids.
-template <int PL>
-__device__ void choose_exact(const RouteArgs& a, const Place& pl, int64_t t, int lane, int* ids) {
-  float x[PL], b[PL], m = 0.f, z = 1.f;
-  const int e0 = load_experts<PL>(a, pl, t, true, lane, x, b);
-  if (!a.sigmoid) {
-    m = -FLT_MAX;
+// This lane's share of the row's largest logit.
+template <int LT, int PL>
+__device__ __forceinline__ float row_max(const float (&x)[PL]) {
+  float m = -FLT_MAX;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
-    m = max_of<64>(m);
-  }
-  choose<64, PL, double>(a, pl, lane, lane, e0, x, b, m, ids, z);
+  for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
+  return max_of<LT>(m);
+}
+
+// One token by a whole wavefront, in 64 bits.
+template <int PL>
+__device__ void choose_token(const RouteArgs& a, const Place& pl, int64_t t, int lane, int* ids) {
+  float x[PL], b[PL];
+  const int e0 = load_experts<PL>(a, pl, t, true, lane, x, b);
+  choose_exact<PL>(a, pl, lane, e0, x, b, a.sigmoid ? 0.f : row_max<64>(x), ids);
 }
 
 // LT lanes per token, 64 / LT tokens per wavefront.  Tokens that fp32 keys leave in doubt are chosen again in 64 bits
@@ -325,19 +388,14 @@ __global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs
   const bool live = t < a.T;
   float x[PL], b[PL], m = 0.f, z = 1.f;
   const int e0 = load_experts<PL>(a, pl, t, live, l, x, b);
-  if (!a.sigmoid) {
-    m = -FLT_MAX;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) m = fmaxf(m, x[i]);
-    m = max_of<LT>(m);
-  }
+  if (!a.sigmoid) m = row_max<LT>(x);
   int* ids = s_id[wv][sub];
-  const bool doubt = choose<LT, PL, float>(a, pl, l, lane, e0, x, b, m, ids, z);
+  const bool doubt = choose_fast<LT, PL>(a, pl, l, lane, e0, x, b, m, ids, z);
   const unsigned long long again = __ballot(doubt && live);
   if (again != 0) {
     const Place px{pl.n_group, exact_bits, pl.vec4};
     for (int q = 0; q < TPW; ++q)
-      if (LT == 64 || ((again >> (16 * q)) & 0xffffu) != 0) choose_exact<PX>(a, px, t0 + q, lane, s_id[wv][q]);
+      if (LT == 64 || ((again >> (16 * q)) & 0xffffu) != 0) choose_token<PX>(a, px, t0 + q, lane, s_id[wv][q]);
   }
   // Slot j's id on lane j (k <= LT).
   const int sel = l < a.k ? ids[l] : -1;
