@@ -332,6 +332,7 @@ typedef enum {
  * a bias experts, and groups with group_top 1, are compared by their logits
  * (both scores grow with them); s_e + bias_e and sums of two are compared in
  * 64 bits.
+ * Outputs must not overlap the inputs or one another (checked).
  * Requires 1 <= k <= topk_group * E / n_group, n_group divides E,
  * 1 <= topk_group <= n_group, group_top in {1, 2} and at most E / n_group,
  * scale finite; E <= 1024, k <= 32, n_group <= 64.
@@ -355,6 +356,7 @@ moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, 
  *                 renormalised sigmoid   q_j (g_j - sum_i q_i g_i) (1 - s_j)
  *                 sigmoid                g_j s_j (1 - s_j)
  *                 softmax                g_e s_e [e chosen] - s_e sum_i s_i g_i, every e
+ * d_logits must not overlap the inputs (checked).
  * Requires k <= E, E <= 1024, k <= 32, scale finite.
  */
 moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
@@ -371,6 +373,7 @@ moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_i
  *               rows no slot names are left untouched.
  *   d_topk_w    [T, k] fp32 out: sum over h of d_out[t, h] * y_perm[inv_perm[t, j], h];
  *               0 for a slot that is not local.
+ * Outputs must not overlap the inputs or one another (checked).
  * Requires H % 4 == 0, k <= 32.
  */
 moe_status moe_combine_backward(const float* d_out, const float* y_perm, const int32_t* inv_perm,
@@ -410,7 +413,8 @@ size_t moe_linear_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
  *             even, for moe_linear_backward (z_up only for SwiGLU)
  *   out       [M, N] out_dtype (moe_dtype)
  * Accumulation, bias, activation and residual are fp32; each output is rounded
- * once.  Outputs must not overlap the inputs (residual == out excepted).
+ * once.  Outputs and ws must not overlap the inputs or one another (checked;
+ * residual == out excepted).
  * ws / ws_bytes: optional device scratch (NULL / 0 is allowed) of at least
  * moe_linear_workspace_bytes(); with it, small products split their reduction
  * over workgroups and sum the fp32 partials in a fixed order, so results are
@@ -439,7 +443,8 @@ size_t moe_linear_backward_workspace_bytes(int64_t M, int32_t N, int32_t K, int3
  * dz_up = d_out * silu(z)), computed in fp32; the products read it rounded to
  * bf16 (their other operands are bf16 too), the sums take it unrounded.
  * Accumulation is fp32, outputs are rounded once, and results are
- * deterministic.  Outputs must not overlap the inputs or one another.
+ * deterministic.  Outputs and ws must not overlap the inputs or one another
+ * (checked).
  * ws / ws_bytes: device scratch of at least
  * moe_linear_backward_workspace_bytes(); needed whenever M > 0.
  * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1.  M == 0: the weight and

@@ -1111,6 +1111,7 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
     return e;
   }
   const BackwardLayout l = backward_layout(a.M, a.N, a.K, a.act);
+  if (l.plan.tiles[0] < 1) return hipErrorInvalidValue;  // (no tiling has few enough workgroups)
   const int mats = l.mats, Np = l.Np, ld = l.ld;
   uint16_t* dz = static_cast<uint16_t*>(a.ws);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(a.ws) + l.sums);

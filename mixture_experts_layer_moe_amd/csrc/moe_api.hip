@@ -12,6 +12,27 @@ constexpr int32_t kAbiVersion = 5;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool tile_m_ok(int32_t tm) { return tm == 16 || tm == 32 || tm == 64 || tm == 128 || tm == 256; }
+// Bytes of an argument; absent ones overlap nothing.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+// Does one of the outputs overlap an input or another output?
+template <int NO, int NI>
+bool clash(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+    for (const Span& s : in)
+      if (overlap(out[i], s)) return true;
+  }
+  return false;
+}
+
 moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
@@ -301,6 +322,9 @@ moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, 
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w)) return MOE_ERR_INVALID_ARG;
+  const size_t e = (size_t)E * 4, te = (size_t)T * e, tk = (size_t)T * k * 4;
+  const Span outs[] = {{topk_idx, tk}, {topk_w, tk}}, ins[] = {{logits, te}, {bias, e}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
   const moe::RouteArgs a{logits,  bias,       T,         E,     k,        score == MOE_SCORE_SIGMOID, renormalize != 0,
                          n_group, topk_group, group_top, scale, topk_idx, topk_w};
   return launched(moe::launch_route_grouped(a, static_cast<hipStream_t>(stream)));
@@ -316,6 +340,9 @@ moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_i
   const void* ptrs[] = {logits, topk_idx, d_topk_w, d_logits};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const size_t te = (size_t)T * E * 4, tk = (size_t)T * k * 4;
+  const Span outs[] = {{d_logits, te}}, ins[] = {{logits, te}, {topk_idx, tk}, {d_topk_w, tk}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
   const moe::RouteBwdArgs a{logits, topk_idx, d_topk_w, T, E, k, score == MOE_SCORE_SIGMOID, renormalize != 0, scale,
                             d_logits};
   return launched(moe::launch_route_grouped_backward(a, static_cast<hipStream_t>(stream)));
@@ -330,6 +357,9 @@ moe_status moe_combine_backward(const float* d_out, const float* y_perm, const i
   const void* ptrs[] = {d_out, y_perm, inv_perm, topk_w, d_y_perm, d_topk_w};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const size_t th = (size_t)T * H * 4, rh = (size_t)R_cap * H * 4, tk = (size_t)T * k * 4;
+  const Span outs[] = {{d_y_perm, rh}, {d_topk_w, tk}}, ins[] = {{d_out, th}, {y_perm, rh}, {inv_perm, tk}, {topk_w, tk}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
   return launched(moe::launch_combine_backward(d_out, y_perm, inv_perm, topk_w, T, k, H, R_cap, d_y_perm, d_topk_w,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -372,6 +402,11 @@ moe_status moe_linear(const void* x, const void* w, const void* w_up, const floa
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
   if (ws && ws_bytes < moe::linear_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
+  const size_t mn = (size_t)M * N, nk = (size_t)N * K * 2, nb = (size_t)N * 4, es = out_dtype == MOE_F32 ? 4 : 2;
+  const Span outs[] = {{out, mn * es}, {z, mn * 2}, {z_up, mn * 2}, {ws, ws_bytes}};
+  const Span ins[] = {{x, (size_t)M * K * 2}, {w, nk}, {w_up, nk}, {bias, nb}, {bias_up, nb},
+                      {residual == out ? nullptr : residual, mn * es}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
   moe::LinearArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.w = static_cast<const uint16_t*>(w);
@@ -414,6 +449,10 @@ moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, 
     if (d_x && (!w || (dual && !w_up))) return MOE_ERR_INVALID_ARG;
     if ((d_w || d_w_up) && !x) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe::linear_backward_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
+    const size_t mn = (size_t)M * N, mk = (size_t)M * K * 2, nk = (size_t)N * K * 2, nb = (size_t)N * 4;
+    const Span outs[] = {{d_x, mk}, {d_w, nk}, {d_w_up, nk}, {d_bias, nb}, {d_bias_up, nb}, {ws, ws_bytes}};
+    const Span ins[] = {{d_out, mn * (out_dtype == MOE_F32 ? 4 : 2)}, {x, mk}, {w, nk}, {w_up, nk}, {z, mn * 2}, {z_up, mn * 2}};
+    if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
   }
   moe::LinearBwdArgs a{};
   a.d_out = d_out;

@@ -36,7 +36,10 @@ class Gating:
 
 @dataclass
 class SharedExpert:
-    """A dense FFN of the layer's activation that every token goes through (bf16, output-major)."""
+    """A dense FFN of the layer's activation that every token goes through (bf16, output-major).
+
+    Where several GPUs' outputs are summed (shares of the experts), one of them has it.
+    """
     w0: torch.Tensor               # [F_s, H]: W_gate^T (SwiGLU) or W1^T (GELU)
     w0_up: Optional[torch.Tensor]  # [F_s, H]: W_up^T (SwiGLU only)
     w1: torch.Tensor               # [H, F_s]
@@ -48,6 +51,14 @@ class MoELayer:
                  w1: torch.Tensor, tile_m: Optional[int] = None, renormalize: bool = True,
                  fused_gather: bool = False, signalled: bool = False,
                  gating: Optional[Gating] = None, shared: Optional[SharedExpert] = None):
+        if shared is not None:
+            Fs = shared.w0.shape[0]
+            if (shared.w0_up is not None) != (cfg.act == "swiglu"):
+                raise ValueError("shared.w0_up belongs to a SwiGLU layer, and only to one")
+            for n, t, shape in (("w0", shared.w0, (Fs, cfg.H)), ("w0_up", shared.w0_up, (Fs, cfg.H)),
+                                ("w1", shared.w1, (cfg.H, Fs))):
+                if t is not None and t.shape != shape:
+                    raise ValueError(f"shared.{n} must have shape {shape}, got {tuple(t.shape)}")
         self.cfg = cfg
         self.gating, self.shared = gating, shared
         self.fused_gather = fused_gather
@@ -70,7 +81,6 @@ class MoELayer:
         self.out = torch.empty((T, H), dtype=torch.float32, device=dev)
         self.fused_ws = ffi.alloc_fused_workspace(self.perm.tiles_cap, H, dev) if signalled else None
         if shared is not None:
-            Fs = shared.w0.shape[0]
             self.shared_h = torch.empty((T, Fs), dtype=torch.bfloat16, device=dev)
             self.shared_ws = [ffi.alloc_linear_workspace(T, Fs, H, cfg.act, dev),
                               ffi.alloc_linear_workspace(T, H, Fs, "none", dev)]

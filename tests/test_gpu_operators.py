@@ -248,6 +248,43 @@ def test_linear_whole_numbers(M, N, K, ws, odt):
     assert torch.equal(plain.cpu(), (x.double() @ w.double().T).float().to(odt))
 
 
+# Sizes at which the launches choose each tile, split over the reduction or not, with a ragged edge in every direction.
+@pytest.mark.parametrize("M,N,K", [(3001, 4100, 72), (1500, 4100, 520), (1500, 4100, 72), (4099, 130, 4104), (3600, 1029, 2056),
+                                   (1795, 1029, 2056), (130, 513, 20488), (400, 770, 12296)])
+def test_linear_tiles(M, N, K):
+    g = gen(M + N + K)
+    d = dev()
+    x, w, res = whole((M, K), g).to(d), whole((N, K), g).to(d), whole((M, N), g).to(d).float()
+    out, c1 = guarded((M, N), F32)
+    out.copy_(res)
+    z, c2 = guarded((M, N), BF)
+    ffi.moe_linear(x, w, residual=out, out=out, z=z)
+    c1(), c2()
+    zr = torch.mm(x.double(), w.double().T)
+    assert torch.equal(out, (zr + res).float())
+    assert torch.equal(z, zr.float().to(BF))
+
+
+@pytest.mark.parametrize("M,N,K", [(1500, 4100, 72), (1795, 4100, 520), (1500, 2050, 520), (1500, 2050, 72), (4099, 70, 4104),
+                                   (4099, 1001, 520), (33, 33, 2056), (1300, 257, 72)])
+def test_linear_tiles_of_two_matrices(M, N, K):
+    """The gate's bias lifts z to where its sigmoid is 1 in 32 bits, so that z u is whole too (below 2^24)."""
+    g = gen(M + N + K)
+    d = dev()
+    x, w, wu, res = (whole(s, g).to(d) for s in ((M, K), (N, K), (N, K), (M, N)))
+    bias, bu = torch.full((N,), 2048.0, device=d), whole((N,), g).float().to(d)
+    out, c1 = guarded((M, N), F32)
+    out.copy_(res)
+    z, c2 = guarded((M, N), BF)
+    zu, c3 = guarded((M, N), BF)
+    ffi.moe_linear(x, w, w_up=wu, bias=bias, bias_up=bu, act="swiglu", residual=out, out=out, z=z, z_up=zu)
+    c1(), c2(), c3()
+    zr, ur = torch.mm(x.double(), w.double().T) + 2048.0, torch.mm(x.double(), wu.double().T) + bu
+    assert float(zr.min()) > 64 and float((zr * ur).abs().max()) < 2 ** 24 - 64
+    assert torch.equal(out, (zr * ur + res).float())
+    assert torch.equal(z, zr.float().to(BF)) and torch.equal(zu, ur.float().to(BF))
+
+
 def act_bound(act, zb, z, u=None, ub=None):
     """Bound of the activation's error from z's (and u's)."""
     f = np.abs(Q.act(act, z))
@@ -373,6 +410,34 @@ def test_linear_backward(M, N, K, act, odt):
     assert (np.abs(n64(outs["d_x"][0]) - ref["d_x"]) <= xb * 1.01 + BF_HALF * np.abs(ref["d_x"])).all()
 
 
+# Sizes at which the launch chooses each tile, with each of its products split or not.
+@pytest.mark.parametrize("M,N,K,act", [
+    (1500, 1001, 4104, "none"), (2500, 130, 4104, "none"), (515, 1001, 4104, "none"), (4352, 700, 520, "none"),
+    (257, 1300, 2056, "none"), (70, 1300, 4104, "none"), (4352, 70, 1032, "none"), (515, 3600, 520, "none"),
+    (33, 1300, 72, "none"), (515, 1300, 72, "none"),
+    (1300, 520, 4104, "swiglu"), (4352, 130, 2056, "swiglu"), (1300, 4100, 136, "swiglu"), (2500, 257, 2056, "swiglu"),
+    (1500, 3600, 136, "swiglu"), (1300, 70, 2056, "swiglu"), (33, 2600, 1032, "swiglu"), (1500, 3100, 72, "swiglu"),
+    (1300, 257, 72, "swiglu"), (33, 33, 72, "swiglu")])
+def test_linear_backward_tiles(M, N, K, act):
+    """Whole numbers throughout: with z of 32 or 64, silu(z) is z and silu'(z) is 1 in 32 bits."""
+    g = gen(M + N + K)
+    d = dev()
+    G, x, w, wu, zu = (whole(s, g).to(d) for s in ((M, N), (M, K), (N, K), (N, K), (M, N)))
+    z = (32 << torch.randint(0, 2, (M, N), generator=g)).to(BF).to(d)
+    dual = act == "swiglu"
+    dz, dzu = (G.double() * zu.double(), G.double() * z.double()) if dual else (G.double(), None)
+    want = {"d_x": torch.mm(dz, w.double()) + (torch.mm(dzu, wu.double()) if dual else 0)}
+    for s, v in (("", dz), ("_up", dzu))[:2 if dual else 1]:
+        want |= {"d_w" + s: torch.mm(v.T.contiguous(), x.double()), "d_bias" + s: v.sum(0)}
+    outs = {n: guarded(tuple(v.shape), F32 if "bias" in n else BF) for n, v in want.items()}
+    up = dict(w_up=wu, z=z, z_up=zu) if dual else {}
+    ffi.moe_linear_backward(G, x, w, act=act, **up, **{n: t for n, (t, _) in outs.items()})
+    for n, (t, check) in outs.items():
+        check()
+        assert float(want[n].abs().max()) < 2 ** 24
+        assert torch.equal(t, want[n].float().to(t.dtype)), n
+
+
 def test_linear_backward_parts_and_empty_batch():
     """Gradients asked for one by one equal those asked for together; no rows: zero weight and bias gradients."""
     g = gen(8)
@@ -453,6 +518,14 @@ def test_layer_with_gating_and_shared_expert():
     assert torch.equal(*outs)
 
 
+def test_signalled_layer_with_gating_and_shared_expert():
+    """The one-launch path adds the shared expert as the four calls do."""
+    cfg, d, gating, shared = layer_inputs()
+    cfg = cfg.with_(tile_m=256)
+    layer = MoELayer.from_inputs(cfg, d, gating=gating, shared=shared, signalled=True)
+    P.assert_output_close(n64(layer.run()), layer_reference(cfg, d, gating, shared), "signalled layer with shared expert")
+
+
 def test_layer_replayed_from_a_graph_and_on_another_stream():
     cfg, d, gating, shared = layer_inputs()
     layer = MoELayer.from_inputs(cfg, d, gating=gating, shared=shared)
@@ -510,6 +583,105 @@ def test_gradients_replayed_from_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (out, *outs.values()))), i
+
+
+def test_router_gradients_replayed_from_a_graph():
+    g = gen(14)
+    d = dev()
+    T, E, k, H = 67, 64, 6, 256
+    logits, y, d_out = (torch.randn(*s, generator=g).to(d) for s in ((T, E), (T * k + 64 * 16, H), (T, H)))
+    idx, w = torch.empty(T, k, dtype=torch.int32, device=d), torch.empty(T, k, device=d)
+    inv = torch.randperm(y.shape[0], generator=g)[:T * k].view(T, k).to(torch.int32)
+    inv[3, 2] = inv[5] = -1
+    inv = inv.to(d)
+    d_y, d_w, d_l = torch.zeros_like(y), torch.empty_like(w), torch.empty_like(logits)
+
+    def step():
+        ffi.moe_route_grouped(logits, k, score="sigmoid", n_group=8, topk_group=4, group_top=2, topk_idx=idx, topk_w=w)
+        ffi.moe_combine_backward(d_out, y, inv, w, d_y, d_w)
+        ffi.moe_route_grouped_backward(logits, idx, d_w, score="sigmoid", d_logits=d_l)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        logits.mul_(-1.25)
+        step()
+        want = [v.clone() for v in (idx, w, d_y, d_w, d_l)]
+        for v in (w, d_y, d_w, d_l):
+            v.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (idx, w, d_y, d_w, d_l))), i
+
+
+# ---------------------------------------------------------------------------
+# Offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+def test_route_offsets_past_32_bits():
+    """More than 2^31 logits: tokens at both ends and around the limit equal the same tokens alone."""
+    d = dev()
+    E, k = 1024, 4
+    T = (1 << 21) + 300
+    logits = torch.zeros(T, E, device=d)
+    some = torch.cat([torch.arange(0, 64), torch.arange((1 << 20) - 64, (1 << 20) + 64), torch.arange(T - 364, T)]).to(d)
+    part = torch.randn(len(some), E, generator=gen(15)).to(d)
+    logits[some] = part
+    kw = dict(score="sigmoid", n_group=8, topk_group=3, group_top=2)
+    idx, w = ffi.moe_route_grouped(logits, k, **kw)
+    pidx, pw = ffi.moe_route_grouped(part, k, **kw)
+    assert torch.equal(idx[some], pidx) and torch.equal(w[some], pw)
+    d_w = torch.zeros(T, k, device=d)
+    pd = torch.randn(len(some), k, generator=gen(16)).to(d)
+    d_w[some] = pd
+    d_l = ffi.moe_route_grouped_backward(logits, idx, d_w, score="sigmoid")
+    assert torch.equal(d_l[some], ffi.moe_route_grouped_backward(part, pidx, pd, score="sigmoid"))
+    d_l[some] = 0
+    assert not bool(d_l.any())
+
+
+def test_combine_backward_offsets_past_32_bits():
+    d = dev()
+    H, R = 2048, (1 << 20) + 600
+    rows = torch.tensor([0, 1, (1 << 19) - 1, 1 << 19, 1 << 20, (1 << 20) + 1, R - 2, R - 1])
+    g = gen(17)
+    y = torch.zeros(R, H, device=d)
+    part = whole((len(rows), H), g).float().to(d)
+    y[rows.to(d)] = part
+    inv = rows.view(4, 2).to(torch.int32).to(d)
+    d_out, w = whole((4, H), g).float().to(d), whole((4, 2), g).float().to(d)
+    d_y, d_w = ffi.moe_combine_backward(d_out, y, inv, w, torch.full((R, H), 9.0, device=d))
+    pos = torch.arange(8, dtype=torch.int32, device=d).view(4, 2)
+    p_y, p_w = ffi.moe_combine_backward(d_out, part, pos, w)
+    assert torch.equal(d_y[rows.to(d)], p_y) and torch.equal(d_w, p_w)
+    d_y[rows.to(d)] = 9.0
+    assert bool((d_y == 9.0).all())
+
+
+@pytest.mark.parametrize("M,N,K", [((1 << 21) + 70, 8, 1032), ((1 << 21) + 70, 1032, 8), (2050, (1 << 20) - 1, 8)])
+def test_linear_offsets_past_32_bits(M, N, K):
+    """More than 2^31 elements of x, of out and its gradient; whole numbers, so every sum is exact."""
+    d = dev()
+    g = torch.Generator(device=d).manual_seed(18)
+    big = lambda *s: torch.randint(-2, 3, s, generator=g, device=d, dtype=torch.int8).to(BF)  # noqa: E731
+    x, w = big(M, K), big(N, K)
+    out = ffi.moe_linear(x, w)
+    rows = torch.tensor([0, 1, M // 2, M - 200, M - 2, M - 1], device=d)
+    assert torch.equal(out[rows], torch.mm(x[rows].double(), w.double().T).float().to(BF))
+    d_out = out.clamp_(-2, 2)
+    d_x, d_w, d_b = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=d)
+    ffi.moe_linear_backward(d_out, x, w, d_x=d_x, d_w=d_w, d_bias=d_b)
+    assert torch.equal(d_x[rows], torch.mm(d_out[rows].double(), w.double()).float().to(BF))
+    cols = torch.tensor([0, N // 2, N - 1], device=d)
+    gc = d_out[:, cols].double()
+    assert torch.equal(d_b[cols], gc.sum(0).float())
+    want = torch.zeros(3, K, dtype=torch.float64, device=d)
+    for i in range(0, M, 1 << 18):
+        want += torch.mm(gc[i:i + (1 << 18)].T.contiguous(), x[i:i + (1 << 18)].double())
+    assert torch.equal(d_w[cols], want.float().to(BF))
 
 
 def test_router_training_step_against_differences():

@@ -102,6 +102,47 @@ def test_linear_workspace_refusal(L):
     assert L.moe_linear_workspace_bytes(10, 64, 64, 9) == 0
 
 
+def at(kib):
+    return ctypes.c_void_p(kib << 10)
+
+
+def test_overlaps_are_refused(L):
+    """An output that shares bytes with an input or another output; addresses are told apart by KiB, none is read."""
+    # [10, 64] logits take 2.5 KiB, [10, 4] choices 160 bytes
+    r = dict(l=at(16), b=at(32), i=at(48), w=at(64))
+    for o in (dict(i=at(18)), dict(w=at(16)), dict(w=at(48)), dict(i=at(32))):
+        assert route(L, **{**r, **o}) == INVALID
+    r = dict(l=at(16), i=at(32), g=at(48), d=at(64))
+    for o in (dict(d=at(16)), dict(d=at(18)), dict(d=at(14)), dict(d=at(31)), dict(d=at(47))):
+        assert route_bwd(L, **{**r, **o}) == INVALID
+    # [10, 64] gradients 2.5 KiB, [40, 64] rows 10 KiB
+    r = dict(g=at(16), y=at(32), i=at(64), w=at(80), dy=at(96), dw=at(128))
+    for o in (dict(dy=at(32)), dict(dy=at(41)), dict(dy=at(18)), dict(dw=at(96)), dict(dw=at(80)), dict(dw=at(64))):
+        assert combine_bwd(L, **{**r, **o}) == INVALID
+    # x [10, 64] and outputs 1.25 KiB, weights [64, 64] 8 KiB
+    r = dict(act=1, x=at(16), w=at(32), wu=at(64), b=at(96), bu=at(100), r=at(128), z=at(144), zu=at(160), out=at(176))
+    for o in (dict(out=at(16)), dict(out=at(39)), dict(out=at(71)), dict(out=at(95)), dict(out=at(100)), dict(out=at(129)),
+              dict(z=at(176)), dict(z=at(160)), dict(z=at(128)), dict(zu=at(177)), dict(zu=at(17)),
+              dict(ws=at(176), n=1 << 20), dict(ws=at(8), n=1 << 14)):
+        assert linear(L, **{**r, **o}) == INVALID
+    r = dict(act=1, g=at(16), x=at(32), w=at(48), wu=at(64), z=at(80), zu=at(96), dx=at(112), dw=at(128), dwu=at(144),
+             db=at(160), dbu=at(164), ws=at(1 << 12))
+    for o in (dict(dx=at(16)), dict(dx=at(33)), dict(dx=at(128)), dict(dw=at(48)), dict(dw=at(137)), dict(dwu=at(71)),
+              dict(db=at(80)), dict(dbu=at(160)), dict(dx=at(96)), dict(ws=at(150)), dict(ws=at(0x1000), dx=at(0x1001))):
+        assert linear_bwd(L, **{**r, **o}) == INVALID
+
+
+def test_layer_checks_its_shared_expert():
+    from mixture_experts_layer_moe_amd import workloads as W
+    from mixture_experts_layer_moe_amd.layer import MoELayer, SharedExpert
+    cfg = W.CONFIGS["fine_grained"].with_(T=4, H=16, F=16, E=4, k=2, tile_m=16)
+    e = lambda *s: torch.empty(s, dtype=torch.bfloat16)  # noqa: E731
+    for sh in (SharedExpert(e(8, 16), None, e(16, 8)), SharedExpert(e(8, 16), e(8, 24), e(16, 8)),
+               SharedExpert(e(8, 24), e(8, 24), e(16, 8)), SharedExpert(e(8, 16), e(8, 16), e(8, 16))):
+        with pytest.raises(ValueError, match="shared"):
+            MoELayer(cfg, e(4, 16), torch.empty(4, 4), None, e(4, 16, 16), e(4, 16, 16), e(4, 16, 16), shared=sh)
+
+
 def linear_bwd(L, **over):
     a = dict(g=FAKE, x=FAKE, w=FAKE, wu=NULL, z=NULL, zu=NULL, M=10, N=64, K=64, act=2, od=0, dx=FAKE, dw=FAKE, dwu=NULL,
              db=NULL, dbu=NULL, ws=FAKE, n=1 << 30)
