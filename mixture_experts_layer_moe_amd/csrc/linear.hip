@@ -347,6 +347,62 @@ struct Tile {
     uint32_t oa, ob;
   };
 
+  // The epilogue straight from the accumulators: a lane holds, for row r + 16 i, the columns n + 16 j + 0..3.
+  template <int ES>
+  static __device__ __forceinline__ void direct(const Sink& k, const Gemm& g, int r, int n, floatx4 (&acc)[NB][TM]) {
+    constexpr int AHEAD = TM * NB <= 16 ? 1 : 0;                    // residual rows are loaded ahead while registers last,
+    constexpr int TOGETHER = (AHEAD ? 8 : 4) / TN;                 // this many together
+    constexpr int C = TM < TOGETHER ? TM : TOGETHER, CH = TM / C;
+    asm volatile("" : "+v"(r), "+v"(n));  // nothing of this ahead of the branch to it
+    uint32_t at[TN];
+    floatx4 b[NB];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      at[j] = n + 16 * j < k.N ? (uint32_t)((r * k.N + n + 16 * j) * ES) : kOut;
+      b[j] = load_bias(g.e.bias, n + 16 * j, k.N);
+      if (NMAT == 2) b[NB - TN + j] = load_bias(g.e.bias_up, n + 16 * j, k.N);
+    }
+    const uint32_t step = (uint32_t)(16 * k.N * ES);
+    floatx4 res[AHEAD + 1][C][TN];
+    auto load = [&](int c, uint32_t from) {  // chunk c, `from` rows' bytes past at[]
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) res[c & AHEAD][i][j] = get4<true, ES>(k.res, at[j] + from + i * step, 1);
+    };
+    auto all = [&](auto has_res) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(b[j]));
+      if constexpr (has_res && AHEAD) load(0, 0);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if constexpr (has_res)
+          if (c + AHEAD < CH) load(c + AHEAD, AHEAD * C * step);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            floatx4 v = acc[j][c * C + i] + b[j];
+            if constexpr (NMAT == 2) {
+              const floatx4 u = acc[NB - TN + j][c * C + i] + b[NB - TN + j];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = activate(ACT_SWIGLU, v[q]) * u[q];
+            }
+            if constexpr (has_res) v += res[c & AHEAD][i][j];
+            put4<true, ES>(k.out, at[j] + i * step, 1, v);
+          }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          at[j] += C * step;
+          asm volatile("" : "+v"(at[j]));  // (all chunks' addresses at once would not fit)
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if (k.has_res) all(std::true_type{});
+    else all(std::false_type{});
+  }
+
   static __device__ __forceinline__ void run(char* smem, const Gemm& g, int64_t m0, int n0, int k0, int k1,
                                              float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -478,13 +534,20 @@ struct Tile {
       order(integral_constant<int, RA + RB>{}, integral_constant<int, 0>{});
     }
 
+    const Sink sink(g.e, m0, BM, g.M, g.N);
+    if (!part && sink.vec && !sink.has_z && !sink.has_zu && (NMAT == 2 || sink.act == ACT_NONE)) {
+      const int r = wm * WT_M + (lane & 15), n = n0 + wn * WT_N + (lane >> 4) * 4;
+      if (sink.f32) direct<4>(sink, g, r, n, acc);
+      else direct<2>(sink, g, r, n, acc);
+      return;
+    }
+
     // Epilogue: 32 rows of each wavefront row at a time through LDS, so that global memory is accessed along rows.  The
     // columns' side feeds the MFMA's rows, so a lane holds, for row lane % 16 of a 16-row block, columns
     // 4 (lane / 16) + 0..3 of a 16-column block.
     float* sm = reinterpret_cast<float*>(smem);
     constexpr int C4 = BN / 4, STEP = NW * 64 / C4, NV = 32 / STEP < 4 ? 32 / STEP : 4;  // a thread keeps its columns
     const int n = (threadIdx.x % C4) * 4;
-    const Sink sink(g.e, m0, BM, g.M, g.N);
     const floatx4 bias = load_bias(g.e.bias, n0 + n, g.N), bias_up = load_bias(g.e.bias_up, n0 + n, g.N);
 #pragma unroll 1
     for (int i = 0; i < TM / 2; ++i) {
