@@ -742,7 +742,7 @@ __global__ __launch_bounds__(NK * 64) void skinny_kernel(Gemm g) {
 // ---------------------------------------------------------------------------
 // dz, and the bias gradients
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 32;  // rows per block of dz_kernel
+constexpr int kDzRows = 8;  // rows per block of dz_kernel
 
 // VEC consecutive values of row-major [., N] data as floats (VEC = 8: 16-byte aligned).
 template <int VEC>
@@ -782,64 +782,61 @@ __device__ __forceinline__ void store_values(uint16_t* o, const float (&v)[VEC])
 // dz (SwiGLU: dz and dz_up, dz_up at column offset Np) rounded to bf16, [M, ld] with zeros in columns [N, Np) of
 // each, and the block's column sums of the unrounded values, part[block row][mats][N].  HBM-bound: reads d_out, z
 // (and z_up), writes dz once.  64 threads side by side of VEC columns (8 where rows are 16-byte aligned, N % 8 ==
-// 0), four rows apart; each thread has the loads of U rows in flight (two of eight columns: more would
-// halve the occupancy that hides them).
+// 0), four rows apart; each thread has the loads of its two rows in flight and ends.  Blocks of 32 rows, two at a
+// time, took 10 us against 4 at 197 x 1000 and 43 against 33 at 8192 x 2816 (SwiGLU).
 template <int VEC>
 __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ d_out, bool f32,
                                                  const uint16_t* __restrict__ z, const uint16_t* __restrict__ z_up,
                                                  int act, int64_t M, int N, int Np, int ld, uint16_t* __restrict__ dz,
                                                  float* __restrict__ part) {
-  constexpr int U = VEC == 8 ? 2 : 8;
+  constexpr int U = kDzRows / 4;
   const int n = (blockIdx.x * 64 + (threadIdx.x & 63)) * VEC, rg = threadIdx.x >> 6;
-  const int64_t r0 = (int64_t)blockIdx.y * kDzRows;
+  const int64_t r0 = (int64_t)blockIdx.y * kDzRows + rg;
   const bool dual = act == ACT_SWIGLU, in = n < N;
+  float g[U][VEC], a[U][VEC], b[U][VEC];
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    const int64_t r = r0 + q * 4;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[q][e] = a[q][e] = b[q][e] = 0.f;
+    if (in && r < M) {
+      load_values<VEC>(g[q], d_out, f32, r * N + n);
+      if (act != ACT_NONE) load_values<VEC>(a[q], z, false, r * N + n);
+      if (dual) load_values<VEC>(b[q], z_up, false, r * N + n);
+    }
+  }
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f(g[q][e], a[q][e], b[q][e]);
+  };
+  // g becomes dz and b becomes dz_up.
+  switch (act) {
+    case ACT_NONE: break;
+    case ACT_GELU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_GELU, zz); }); break;
+    case ACT_SILU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_SILU, zz); }); break;
+    default:
+      each([](float& d, float& zz, float& u) {
+        const float go = d;
+        d = go * activate_grad(ACT_SWIGLU, zz) * u;
+        u = go * activate(ACT_SWIGLU, zz);
+      });
+  }
   float s0[VEC], s1[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) s0[e] = s1[e] = 0.f;
-#pragma unroll 1
-  for (int q0 = 0; q0 < kDzRows / 4; q0 += U) {
-    float g[U][VEC], a[U][VEC], b[U][VEC];
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int64_t r = r0 + (q0 + q) * 4 + rg;
+  for (int q = 0; q < U; ++q) {
+    const int64_t r = r0 + q * 4;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) g[q][e] = a[q][e] = b[q][e] = 0.f;
-      if (in && r < M) {
-        load_values<VEC>(g[q], d_out, f32, r * N + n);
-        if (act != ACT_NONE) load_values<VEC>(a[q], z, false, r * N + n);
-        if (dual) load_values<VEC>(b[q], z_up, false, r * N + n);
-      }
+    for (int e = 0; e < VEC; ++e) {
+      s0[e] += g[q][e];
+      s1[e] += b[q][e];
     }
-    auto each = [&](auto f) {
-#pragma unroll
-      for (int q = 0; q < U; ++q)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f(g[q][e], a[q][e], b[q][e]);
-    };
-    // g becomes dz and b becomes dz_up.
-    switch (act) {
-      case ACT_NONE: break;
-      case ACT_GELU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_GELU, zz); }); break;
-      case ACT_SILU: each([](float& d, float& zz, float&) { d *= activate_grad(ACT_SILU, zz); }); break;
-      default:
-        each([](float& d, float& zz, float& u) {
-          const float go = d;
-          d = go * activate_grad(ACT_SWIGLU, zz) * u;
-          u = go * activate(ACT_SWIGLU, zz);
-        });
-    }
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int64_t r = r0 + (q0 + q) * 4 + rg;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        s0[e] += g[q][e];
-        s1[e] += b[q][e];
-      }
-      if (n < Np && r < M) {
-        store_values<VEC>(dz + r * ld + n, g[q]);
-        if (dual) store_values<VEC>(dz + r * ld + Np + n, b[q]);
-      }
+    if (n < Np && r < M) {
+      store_values<VEC>(dz + r * ld + n, g[q]);
+      if (dual) store_values<VEC>(dz + r * ld + Np + n, b[q]);
     }
   }
   if (!part) return;
@@ -859,8 +856,8 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ d_out,
   }
 }
 
-// Column sums of dz_kernel's blocks: 64 columns a workgroup (of 256 threads or more), a quarter of the row blocks
-// each, added in order.
+// Column sums of dz_kernel's blocks: 64 columns a workgroup, an equal share of the row blocks for each of its
+// wavefronts, 16 of them in flight, added in order.
 struct BiasSums {
   const float* part;
   int64_t rows;  // row blocks
@@ -869,23 +866,28 @@ struct BiasSums {
 };
 __device__ __forceinline__ void bias_sum(char* smem, const BiasSums& b, int bid) {
   float* sm = reinterpret_cast<float*>(smem);
-  const int c = bid * 64 + (threadIdx.x & 63), qr = threadIdx.x >> 6;
-  if (qr < 4) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    const int64_t r0 = qr * b.rows / 4, r1 = (qr + 1) * b.rows / 4;
-    if (c < b.mats * b.N) {
-      int64_t r = r0;
-      for (; r + 4 <= r1; r += 4)
+  const int c = bid * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6, waves = blockDim.x >> 6, width = b.mats * b.N;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < width) {
+    int64_t r = q * b.rows / waves;
+    const int64_t end = (q + 1) * b.rows / waves;
+    const float* p = b.part + c;
+    for (; r + 16 <= end; r += 16) {
+      float v[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += b.part[(r + e) * b.mats * b.N + c];
-      for (; r < r1; ++r) s[0] += b.part[r * b.mats * b.N + c];
+      for (int e = 0; e < 16; ++e) v[e] = p[(r + e) * width];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e & 3] += v[e];
     }
-    sm[qr * 64 + (threadIdx.x & 63)] = (s[0] + s[1]) + (s[2] + s[3]);
+    for (; r < end; ++r) s[0] += p[r * width];
   }
+  sm[threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (qr == 0 && c < b.mats * b.N) {
+  if (q == 0 && c < width) {
+    float v = sm[threadIdx.x];
+    for (int w = 1; w < waves; ++w) v += sm[64 * w + threadIdx.x];
     float* o = c < b.N ? b.d_bias : b.d_bias_up;
-    if (o) o[c < b.N ? c : c - b.N] = (sm[threadIdx.x] + sm[64 + threadIdx.x]) + (sm[128 + threadIdx.x] + sm[192 + threadIdx.x]);
+    if (o) o[c < b.N ? c : c - b.N] = v;
   }
 }
 
