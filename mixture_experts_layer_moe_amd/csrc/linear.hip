@@ -69,6 +69,10 @@ __device__ __forceinline__ float activate_grad(int act, float z) {
 // rows at four chunks; the 16 lanes served together are rows 0-3 and 12-15 at one chunk and rows 4-11 at the next
 // one (or the other way round), which this spreads over all 64 banks, as it does 16 rows at one chunk.
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+// Paired rows operand (the forward product's weights): a fragment's rows are 8 (lane / 4 % 4) + lane % 4 of a block of
+// 32, plus 4 for its partner, so that a lane's results of both are eight columns side by side: outputs are written 16
+// bytes at a time.  The 16 lanes served together are again at two neighbouring chunks.
+__device__ __forceinline__ int swz_p(int row) { return ((row >> 1) & 1) | ((row >> 3) & 3) << 1; }
 // Columns operand of C columns: LDS row of 2 C bytes per reduction index; half a wavefront of a transposing read
 // takes 32 bytes of each of the rows r..r + 3 and r + 8..r + 11, so the 64-byte unit is XORed with the row and the
 // 32-byte half of it with row / 8 to spread those over all 64 banks.
@@ -79,6 +83,12 @@ __device__ __forceinline__ int swz_t(int r) {
 
 // MFMA fragment (16 operand rows from row c0, 32 reduction indices from 32 ks) of a staged operand: lane holds
 // row c0 + lane % 16, reduction indices 32 ks + 8 (lane / 16) + 0..7.
+// (paired: the block of 32 rows from c0 on, its fragment `half`).
+template <int C>
+__device__ __forceinline__ bf16x8 paired_fragment(const char* tile, int c0, int half, int ks, int lane) {
+  const int row = c0 + ((lane >> 2) & 3) * 8 + half * 4 + (lane & 3), chunk = ks * 4 + (lane >> 4);
+  return *reinterpret_cast<const bf16x8*>(tile + row * 128 + ((chunk ^ swz_p(row)) << 4));
+}
 template <bool COLS, int C>
 __device__ __forceinline__ bf16x8 fragment(const char* tile, int c0, int ks, int lane) {
   const int l16 = lane & 15, g = lane >> 4;
@@ -297,11 +307,14 @@ struct Tile {
   static constexpr int PS = (LOADS + 2) / 3;                        // pieces per phase
   static constexpr int PITCH = NMAT * BN + 4;                       // floats per row of the staged result
   static constexpr int SMEM = 2 * STAGE > WM * 32 * PITCH * 4 ? 2 * STAGE : WM * 32 * PITCH * 4;
+  static constexpr bool PAIRS = !B_COLS;
+  static constexpr int VW = PAIRS ? 2 : 1;                          // groups of four columns side by side in a lane
+  static_assert(TN % VW == 0, "pairs of fragments");
   static_assert(HM >= 1 && TN >= 1 && A_PIECES >= 1 && B_PIECES >= 1, "tile too small for the wavefronts");
 
   // An operand's C rows (columns) from c0 on, as this lane loads them.  Stage kt is read through a resource based
   // at its first element; rows and reduction indices past the operand's end lie outside of it.
-  template <bool COLS, int C>
+  template <bool COLS, int C, bool PAIRED = false>
   struct Source {
     const char *base, *base2;  // stage 0 of the two segments (base2 less the first segment's stages)
     int64_t adv;               // bytes between stages
@@ -318,9 +331,9 @@ struct Tile {
       if (!COLS) {
         const int left = (int)(o.extent - c0 < C ? o.extent - c0 : C);
         full = tail = (int)(((left - 1) * o.ld + BK) * 2);
-        const int row = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ swz(row);
+        const int row = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ (PAIRED ? swz_p(row) : swz(row));
         off = (uint32_t)((row * o.ld + chunk * 8) * 2);
-        step = (uint32_t)(8 * NW * o.ld * 2);
+        step = (uint32_t)(8 * NW * o.ld * 2);  // (8 NW rows on, the swizzle is the same)
         klim = (int)((o.R - chunk * 8 + BK - 1) / BK);
       } else {
         constexpr int LPR = C / 8;  // lanes per LDS row
@@ -347,30 +360,61 @@ struct Tile {
     uint32_t oa, ob;
   };
 
-  // The epilogue straight from the accumulators: a lane holds, for row r + 16 i, the columns n + 16 j + 0..3.
+  // VW groups of four values side by side, at byte offset `at` (kOut and above: none).
+  template <int ES>
+  static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t at, const floatx4 (&v)[VW]) {
+    if constexpr (ES == 2 && VW == 2) {
+      const u32x2 a = pack4(v[0]), b = pack4(v[1]);
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{a[0], a[1], b[0], b[1]}, r, at, 0, 0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < VW; ++q) put4<true, ES>(r, at + q * 4 * ES, 1, v[q]);
+    }
+  }
+  template <int ES>
+  static __device__ __forceinline__ void get(__amdgpu_buffer_rsrc_t r, uint32_t at, floatx4 (&v)[VW]) {
+    if constexpr (ES == 2 && VW == 2) {
+      const u32x4 h = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q >> 1][(q & 1) * 2] = bf2f((uint16_t)h[q]);
+        v[q >> 1][(q & 1) * 2 + 1] = bf2f((uint16_t)(h[q] >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < VW; ++q) v[q] = get4<true, ES>(r, at + q * 4 * ES, 1);
+    }
+  }
+
+  // The epilogue straight from the accumulators: a lane holds, for row r + 16 i, the 4 VW columns from n + 16 VW j on.
   template <int ES>
   static __device__ __forceinline__ void direct(const Sink& k, const Gemm& g, int r, int n, floatx4 (&acc)[NB][TM]) {
-    constexpr int AHEAD = TM * NB <= 16 ? 1 : 0;                    // residual rows are loaded ahead while registers last,
-    constexpr int TOGETHER = (AHEAD ? 8 : 4) / TN;                 // this many together
+    asm volatile("" : "+v"(r), "+v"(n));                       // nothing of this ahead of the branch to it
+    constexpr int P = TN / VW;                                 // pieces of a row
+    constexpr int AHEAD = TM * NB <= 16 ? 1 : 0;               // residual rows are loaded ahead while registers last,
+    constexpr int TOGETHER = (AHEAD ? 8 : 4) / TN;             // this many together
     constexpr int C = TM < TOGETHER ? TM : TOGETHER, CH = TM / C;
-    asm volatile("" : "+v"(r), "+v"(n));  // nothing of this ahead of the branch to it
-    uint32_t at[TN];
+    uint32_t at[P];
     floatx4 b[NB];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      at[j] = n + 16 * j < k.N ? (uint32_t)((r * k.N + n + 16 * j) * ES) : kOut;
-      b[j] = load_bias(g.e.bias, n + 16 * j, k.N);
-      if (NMAT == 2) b[NB - TN + j] = load_bias(g.e.bias_up, n + 16 * j, k.N);
+    for (int p = 0; p < P; ++p) {
+      const int col = n + 16 * VW * p;
+      at[p] = col < k.N ? (uint32_t)((r * k.N + col) * ES) : kOut;
+#pragma unroll
+      for (int q = 0; q < VW; ++q) {
+        b[p * VW + q] = load_bias(g.e.bias, col + 4 * q, k.N);
+        if (NMAT == 2) b[NB - TN + p * VW + q] = load_bias(g.e.bias_up, col + 4 * q, k.N);
+      }
     }
     const uint32_t step = (uint32_t)(16 * k.N * ES);
-    floatx4 res[AHEAD + 1][C][TN];
-    auto load = [&](int c, uint32_t from) {  // chunk c, `from` rows' bytes past at[]
+    floatx4 res[AHEAD + 1][C][P][VW];
+    auto load = [&](int c, uint32_t from) {  // chunk c, `from` bytes past at[]
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) res[c & AHEAD][i][j] = get4<true, ES>(k.res, at[j] + from + i * step, 1);
+        for (int p = 0; p < P; ++p) get<ES>(k.res, at[p] + from + i * step, res[c & AHEAD][i][p]);
     };
-    auto all = [&](auto has_res) {
+    auto all = [&](auto has_res, auto has_z) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(b[j]));
       if constexpr (has_res && AHEAD) load(0, 0);
@@ -381,26 +425,44 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            floatx4 v = acc[j][c * C + i] + b[j];
-            if constexpr (NMAT == 2) {
-              const floatx4 u = acc[NB - TN + j][c * C + i] + b[NB - TN + j];
+          for (int p = 0; p < P; ++p) {
+            const uint32_t here = at[p] + i * step, z_at = here / (ES / 2);  // (past every resource where at[] is)
+            floatx4 v[VW], u[VW];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = activate(ACT_SWIGLU, v[q]) * u[q];
+            for (int q = 0; q < VW; ++q) {
+              v[q] = acc[p * VW + q][c * C + i] + b[p * VW + q];
+              u[q] = NMAT == 2 ? acc[NB - TN + p * VW + q][c * C + i] + b[NB - TN + p * VW + q] : v[q];
             }
-            if constexpr (has_res) v += res[c & AHEAD][i][j];
-            put4<true, ES>(k.out, at[j] + i * step, 1, v);
+            if constexpr (has_z) {
+              put<2>(k.z, z_at, v);
+              if (NMAT == 2) put<2>(k.z_up, z_at, u);
+            }
+#pragma unroll
+            for (int q = 0; q < VW; ++q) {
+              if constexpr (NMAT == 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[q][e] = activate(ACT_SWIGLU, v[q][e]) * u[q][e];
+              if constexpr (has_res) v[q] += res[c & AHEAD][i][p][q];
+            }
+            put<ES>(k.out, here, v);
           }
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          at[j] += C * step;
-          asm volatile("" : "+v"(at[j]));  // (all chunks' addresses at once would not fit)
+        for (int p = 0; p < P; ++p) {
+          at[p] += C * step;
+          asm volatile("" : "+v"(at[p]));  // (all chunks' addresses at once would not fit)
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    if (k.has_res) all(std::true_type{});
-    else all(std::false_type{});
+    using std::false_type;
+    using std::true_type;
+    if (k.has_z || k.has_zu) {  // (stores of the one that is absent go nowhere)
+      if (k.has_res) all(true_type{}, true_type{});
+      else all(false_type{}, true_type{});
+    } else {
+      if (k.has_res) all(true_type{}, false_type{});
+      else all(false_type{}, false_type{});
+    }
   }
 
   static __device__ __forceinline__ void run(char* smem, const Gemm& g, int64_t m0, int n0, int k0, int k1,
@@ -408,8 +470,8 @@ struct Tile {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const Source<A_COLS, BM> src_a(g.a, m0, A_COLS ? g.seg : g.nk, k1, wave, lane);
-    const Source<B_COLS, BN> src_b(g.b, n0, g.seg, k1, wave, lane);
-    const Source<B_COLS, BN> src_u(NMAT == 2 ? g.b_up : g.b, n0, g.seg, k1, wave, lane);
+    const Source<B_COLS, BN, PAIRS> src_b(g.b, n0, g.seg, k1, wave, lane);
+    const Source<B_COLS, BN, PAIRS> src_u(NMAT == 2 ? g.b_up : g.b, n0, g.seg, k1, wave, lane);
     floatx4 acc[NB][TM];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
@@ -448,7 +510,10 @@ struct Tile {
     auto read_b = [&](int buf, int ks) {
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        fb[ks][j] = fragment<B_COLS, BN>(smem + buf * STAGE + A_BYTES + (j / TN) * B_BYTES, wn * WT_N + (j % TN) * 16, ks, lane);
+        if constexpr (PAIRS)
+          fb[ks][j] = paired_fragment<BN>(smem + buf * STAGE + A_BYTES + (j / TN) * B_BYTES, wn * WT_N + (j % TN) / 2 * 32, j & 1, ks, lane);
+        else
+          fb[ks][j] = fragment<B_COLS, BN>(smem + buf * STAGE + A_BYTES + (j / TN) * B_BYTES, wn * WT_N + (j % TN) * 16, ks, lane);
     };
     // The MFMAs of one phase.  They have no side effects: the use of the accumulators keeps them ahead of the next
     // phase's.
@@ -535,8 +600,8 @@ struct Tile {
     }
 
     const Sink sink(g.e, m0, BM, g.M, g.N);
-    if (!part && sink.vec && !sink.has_z && !sink.has_zu && (NMAT == 2 || sink.act == ACT_NONE)) {
-      const int r = wm * WT_M + (lane & 15), n = n0 + wn * WT_N + (lane >> 4) * 4;
+    if (!part && (g.N & (4 * VW - 1)) == 0 && (NMAT == 2 || sink.act == ACT_NONE)) {
+      const int r = wm * WT_M + (lane & 15), n = n0 + wn * WT_N + (lane >> 4) * 4 * VW;
       if (sink.f32) direct<4>(sink, g, r, n, acc);
       else direct<2>(sink, g, r, n, acc);
       return;
@@ -561,7 +626,7 @@ struct Tile {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            const int c = (j / TN) * BN + wn * WT_N + (j % TN) * 16 + (lane >> 4) * 4;
+            const int c = (j / TN) * BN + wn * WT_N + (j % TN) / VW * 16 * VW + (lane >> 4) * 4 * VW + j % VW * 4;
             *reinterpret_cast<floatx4*>(sm + (wm * 32 + h * 16 + (lane & 15)) * PITCH + c) = acc[j][2 * ii + h];
           }
       }
