@@ -293,6 +293,12 @@ __device__ __forceinline__ void ring_barrier() {
 // and LDS writes and loads are spread over the MFMAs of the first three.  All of a stage's fragments have been read
 // when its last phase begins: there the workgroup synchronises, and the last phase reads the next stage's first
 // fragments.  Stages past the end load through a resource of no bytes, so every iteration is the same.
+//
+// MFMA-bound, under the card's power limit: the SwiGLU product 4096 x 14336 x 4096 (962 GFLOP) takes 0.74-0.8 ms, its
+// matrix cores busy 69 % of the cycles at 1.66 GHz; a plain 8192 x 8192 x 8192 product 0.79-0.82 ms, the library's
+// 0.76-0.81.  The 16x16x32 MFMA on eight wavefronts keeps every accumulator in VGPRs: four wavefronts with
+// 32x32x16 moved them to AGPRs and back (825 us for that SwiGLU product when this took 750-770), eight with 32x32x16
+// took 788, and 256x128 tiles on four wavefronts 86 us against 49 at 4096 x 2048 x 2816.
 template <int BM, int BN, bool A_COLS, bool B_COLS, int NMAT, int WM, int WN>
 struct Tile {
   static constexpr int NW = WM * WN;
@@ -387,6 +393,9 @@ struct Tile {
   }
 
   // The epilogue straight from the accumulators: a lane holds, for row r + 16 i, the 4 VW columns from n + 16 VW j on.
+  // For products without an activation and SwiGLU, where rows are whole pieces: 12.5 us against the LDS epilogue's 17
+  // at 4096 x 4096 x 64, 62 against 84 at 4096 x 14336 x 64 (SwiGLU), 93 against 104 there with z and z_up saved (with
+  // single groups of four bf16 values 126, which is why the forward product pairs its fragments).
   template <int ES>
   static __device__ __forceinline__ void direct(const Sink& k, const Gemm& g, int r, int n, floatx4 (&acc)[NB][TM]) {
     asm volatile("" : "+v"(r), "+v"(n));                       // nothing of this ahead of the branch to it
@@ -607,7 +616,8 @@ struct Tile {
       return;
     }
 
-    // Epilogue: 32 rows of each wavefront row at a time through LDS, so that global memory is accessed along rows.  The
+    // The other epilogues (GELU and SiLU, whose code would be long unrolled; split sums; rows of odd lengths, whose
+    // values go one by one): 32 rows of each wavefront row at a time through LDS, so that global memory is accessed along rows.  The
     // columns' side feeds the MFMA's rows, so a lane holds, for row lane % 16 of a 16-row block, columns
     // 4 (lane / 16) + 0..3 of a 16-column block.
     float* sm = reinterpret_cast<float*>(smem);
@@ -686,6 +696,10 @@ __device__ __forceinline__ void tile_of(int bid, int G, int mt, int nt, int tile
 }
 
 // Tile kinds: rows, columns staged per stage (of one matrix, or half of each of two), wavefronts, workgroups per CU.
+// A stage reads (BM + BN) x 128 bytes for BM BN x 64 products, so large tiles run at a higher rate (the us per stage in
+// make_plan: 1.43, 1.15, 1.01 and 0.84 PFLOP/s) and small ones fill the chip when there are few: 1024 x 2048 x 512
+// takes 8.5 us with 64-row tiles, 4096 x 2048 x 2816 49 us with 256x128 (one round of 256) where 256x256 tiles keep
+// half of the CUs idle.
 struct Kind {
   int bm, bn, wm, wn, per_cu;
   constexpr int threads() const { return wm * wn * 64; }
@@ -732,7 +746,7 @@ __global__ __launch_bounds__(kKinds[KIND].threads(), KIND == 3 ? 3 : 2) void for
 // bytes of each of 8 rows: with 64 bytes of 16 rows, the MFMA's own layout, whole lines are asked for twice and a CU
 // draws 20 GB/s instead of 28 (1 x 28672 x 8192: 92 against 67 us).  So a wavefront passes its operands through LDS
 // of its own, which needs no barrier (its LDS accesses complete in order).  U steps of 64 reduction indices are in
-// flight.  The wavefronts' sums meet in LDS and are added in order.
+// flight.  Bound by the weights' bytes: 58.7 MB at 1 x 2048 x 7168 (SwiGLU) in 10.1 us, 5.8 TB/s.  The wavefronts' sums meet in LDS and are added in order.
 template <bool DUAL, int NK, int U>
 __global__ __launch_bounds__(NK * 64) void skinny_kernel(Gemm g) {
   constexpr int COLS = DUAL ? 8 : 16;  // output columns
@@ -956,7 +970,9 @@ __device__ __forceinline__ void bias_sum(char* smem, const BiasSums& b, int bid)
   }
 }
 
-// The backward pass's products in one launch, so that the tiles of one fill the CUs that another leaves idle: the
+// The backward pass's products in one launch (8192 x 2816 x 2048 SwiGLU, 378 GFLOP: 330-350 us, MFMA 55 % busy at 2.0
+// GHz, because 432 tiles of 88 and 128 stages leave 80 CUs without a second one; splitting the weight gradients to
+// even that out would write and read 100-180 MB of partial tiles), so that the tiles of one fill the CUs that another leaves idle: the
 // input gradient (rows, columns; jobs 0 .. nx - 1, at most one; ahead of the others by 2-4 % at 8192 x 2816 x 2048),
 // the weight gradients (both operands columns) and the bias gradients (from workgroup bias_first on).
 struct BackwardJobs {
@@ -981,7 +997,8 @@ __global__ __launch_bounds__(kKinds[KIND].threads(), KIND == 3 ? 3 : 2) void bac
   else run_job<KIND, false, true, 1>(smem, b.j[q], bid);
 }
 
-// Adds the slices of a job's tiles in order and applies its epilogue; one group of four outputs per thread.
+// Adds the slices of a job's tiles in order and applies its epilogue; one group of four outputs per thread.  The
+// partial tiles come from the last-level cache (64 x 4096 x 1024, backward: 5 us, with launch).
 __device__ __forceinline__ void reduce_job(const Job& j, int bm, int bn, int nmat) {
   const int n4 = (j.g.N + 3) / 4;
   const int64_t o = blockIdx.x * 256ll + threadIdx.x;
@@ -1046,7 +1063,8 @@ int device_cus() {
 
 constexpr int kMaxSlices = 16;
 
-// Picks the tile kind and slices with the least estimated time: a CU runs its share of the launch's workgroups,
+// Picks the tile kind and slices with the least estimated time, from measured figures of each kind (products of one
+// to seven rounds, K 64 to 4096): a CU runs its share of the launch's workgroups,
 // per_cu of them at a time, a stage of r workgroups taking max(latency, r * rate), plus a fixed cost per workgroup;
 // a split adds the second launch and its traffic.
 Plan make_plan(const Size* z, int n, int nmat, bool split) {

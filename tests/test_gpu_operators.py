@@ -285,6 +285,32 @@ def test_linear_tiles_of_two_matrices(M, N, K):
     assert torch.equal(z, zr.float().to(BF)) and torch.equal(zu, ur.float().to(BF))
 
 
+@pytest.mark.parametrize("M,N,K", [(3001, 4104, 72), (1500, 4104, 520), (1500, 2056, 520), (1500, 4104, 72), (1500, 2056, 72),
+                                   (203, 264, 136), (300, 268, 72)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("odt", [BF, F32])
+def test_linear_rows_of_whole_pieces(M, N, K, act, odt):
+    """Rows of 16-byte pieces on every tile, with and without a residual and the pre-activations, one or both."""
+    g = gen(M + N + K)
+    d = dev()
+    dual = act == "swiglu"
+    x, w, wu, r = (whole(s, g).to(d) for s in ((M, K), (N, K), (N, K), (M, N)))
+    b = torch.full((N,), 2048.0, device=d) if dual else whole((N,), g).float().to(d)
+    zr, ur = torch.mm(x.double(), w.double().T) + b, torch.mm(x.double(), wu.double().T)
+    assert float((zr * ur).abs().max()) < 2 ** 24 - 64 and (not dual or float(zr.min()) > 64)
+    for res, save in [(False, ""), (True, ""), (False, "z"), (True, "zu"), (True, "u"), (False, "zu")]:
+        out, c1 = guarded((M, N), odt)
+        z, c2 = guarded((M, N), BF)
+        u, c3 = guarded((M, N), BF)
+        ffi.moe_linear(x, w, w_up=wu if dual else None, bias=b, act=act, residual=r.to(odt) if res else None, out=out,
+                       z=z if "z" in save else None, z_up=u if dual and "u" in save else None)
+        c1(), c2(), c3()
+        ref = (zr * ur if dual else zr) + (r.double() if res else 0)
+        assert torch.equal(out, ref.float().to(odt)), (res, save)
+        assert torch.equal(z, zr.float().to(BF) if "z" in save else torch.full_like(z, -7.0)), (res, save)
+        assert torch.equal(u, ur.float().to(BF) if dual and "u" in save else torch.full_like(u, -7.0)), (res, save)
+
+
 def act_bound(act, zb, z, u=None, ub=None):
     """Bound of the activation's error from z's (and u's)."""
     f = np.abs(Q.act(act, z))
