@@ -1064,14 +1064,17 @@ int device_cus() {
 constexpr int kMaxSlices = 16;
 
 // Picks the tile kind and slices with the least estimated time, from measured figures of each kind (products of one
-// to seven rounds, K 64 to 4096): a CU runs its share of the launch's workgroups,
-// per_cu of them at a time, a stage of r workgroups taking max(latency, r * rate), plus a fixed cost per workgroup;
-// a split adds the second launch and its traffic.
+// to seven rounds, K 64 to 4096): a CU runs its share of the launch's workgroups, per_cu of them at a time, a stage of r
+// workgroups taking max(latency, r * rate), plus a fixed cost per workgroup; a split adds the second launch and its
+// traffic.  For a single product the rate is that of the CUs in use, since the others' idling raises their clock (3000 x
+// 3000 x 1000: 144 tiles of 256x256 take 28 us, the 64x128 tiles chosen without this 39); in the backward pass's launch
+// other products fill them.
 Plan make_plan(const Size* z, int n, int nmat, bool split) {
   constexpr double kRate[] = {1.5, 0.93, 0.53, 0.32};      // us a stage and workgroup, CU full
   constexpr double kLatency[] = {1.1, 0.73, 0.56, 0.42};   // us a stage, at least
   constexpr double kFixed[] = {9.0, 6.0, 5.0, 3.5};        // us a workgroup: first stage's latency and epilogue
   constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
+  constexpr double kUneven = 2.6;  // two workgroups a CU on average, where three fit: many CUs get three
   const int cus = device_cus();
   Plan best{};
   best.time = 1e30;
@@ -1100,12 +1103,15 @@ Plan make_plan(const Size* z, int n, int nmat, bool split) {
       if (!any || blocks > 2.0e9) continue;
       const double per_block = work / blocks;          // stages of an average workgroup
       int64_t left = (int64_t)((blocks + cus - 1) / cus);  // workgroups of the fullest CU
-      double t = 0;
+      double t = 0, rest = blocks;
       while (left > 0) {
         const int r = left < occ ? (int)left : occ;
-        const double stage = kLatency[kind] > r * kRate[kind] ? kLatency[kind] : r * kRate[kind];
+        double at_once = r;
+        if (n == 1) at_once = r == 1 && rest < cus ? rest / cus : r == 2 && occ == 3 ? kUneven : r;
+        const double stage = kLatency[kind] > at_once * kRate[kind] ? kLatency[kind] : at_once * kRate[kind];
         t += (t == 0 ? longest : per_block) * stage + kFixed[kind];
         left -= r;
+        rest -= (double)r * cus;
       }
       if (bytes > 0) t += kSecond + bytes / kBytes;
       p.time = t;

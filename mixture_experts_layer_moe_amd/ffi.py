@@ -367,7 +367,7 @@ def _matrix(t: torch.Tensor, name: str):
 
 
 def _launch(fn, name: str, dev: int, *args):
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:

@@ -250,7 +250,7 @@ def test_linear_whole_numbers(M, N, K, ws, odt):
 
 # Sizes at which the launches choose each tile, split over the reduction or not, with a ragged edge in every direction.
 @pytest.mark.parametrize("M,N,K", [(3001, 4100, 72), (1500, 4100, 520), (1500, 4100, 72), (4099, 130, 4104), (3600, 1029, 2056),
-                                   (1795, 1029, 2056), (130, 513, 20488), (400, 770, 12296)])
+                                   (1795, 1029, 2056), (130, 513, 20488), (400, 770, 12296), (1500, 1300, 4104)])
 def test_linear_tiles(M, N, K):
     g = gen(M + N + K)
     d = dev()
@@ -266,7 +266,7 @@ def test_linear_tiles(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1500, 4100, 72), (1795, 4100, 520), (1500, 2050, 520), (1500, 2050, 72), (4099, 70, 4104),
-                                   (4099, 1001, 520), (33, 33, 2056), (1300, 257, 72)])
+                                   (4099, 1001, 520), (33, 33, 2056), (1300, 257, 72), (1500, 700, 4104)])
 def test_linear_tiles_of_two_matrices(M, N, K):
     """The gate's bias lifts z to where its sigmoid is 1 in 32 bits, so that z u is whole too (below 2^24)."""
     g = gen(M + N + K)
@@ -646,6 +646,23 @@ def test_router_gradients_replayed_from_a_graph():
 # ---------------------------------------------------------------------------
 # Offsets past 32 bits
 # ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_linear_longest_rows(M):
+    """The longest reduction, and the widest weights of the input gradient; sums below 2^24."""
+    N, K = 24, 1 << 20
+    d = dev()
+    g = torch.Generator(device=d).manual_seed(19)
+    few = lambda *s: torch.randint(-2, 3, s, generator=g, device=d, dtype=torch.int8).to(BF)  # noqa: E731
+    x, w, d_out = few(M, K), few(N, K), few(M, N)
+    want = torch.mm(x.double(), w.double().T).float()
+    for ws in (True, False):
+        assert torch.equal(ffi.moe_linear(x, w, out_dtype=F32, use_workspace=ws), want)
+    d_x, d_w = torch.empty_like(x), torch.empty_like(w)
+    ffi.moe_linear_backward(d_out, x, w, d_x=d_x, d_w=d_w)
+    assert torch.equal(d_x, torch.mm(d_out.double(), w.double()).float().to(BF))
+    assert torch.equal(d_w, torch.mm(d_out.double().T.contiguous(), x.double()).float().to(BF))
+
 
 def test_route_offsets_past_32_bits():
     """More than 2^31 logits: tokens at both ends and around the limit equal the same tokens alone."""
