@@ -617,9 +617,9 @@ struct Tile {
     }
 
     // The other epilogues (GELU and SiLU, whose code would be long unrolled; split sums; rows of odd lengths, whose
-    // values go one by one): 32 rows of each wavefront row at a time through LDS, so that global memory is accessed along rows.  The
-    // columns' side feeds the MFMA's rows, so a lane holds, for row lane % 16 of a 16-row block, columns
-    // 4 (lane / 16) + 0..3 of a 16-column block.
+    // values go one by one): 32 rows of each wavefront row at a time through LDS, so that global memory is accessed
+    // along rows.  The columns' side feeds the MFMA's rows, so a lane holds, for row lane % 16 of a 16-row block,
+    // columns 4 (lane / 16) + 0..3 of a 16-column block (paired: 8 (lane / 16) + 0..3 or 4..7 of 32 columns).
     float* sm = reinterpret_cast<float*>(smem);
     constexpr int C4 = BN / 4, STEP = NW * 64 / C4, NV = 32 / STEP < 4 ? 32 / STEP : 4;  // a thread keeps its columns
     const int n = (threadIdx.x % C4) * 4;
@@ -683,7 +683,8 @@ constexpr int kXcds = 8;
 constexpr int kGroupM = 8;  // row tiles per rasterisation group
 
 // Workgroup -> slice and tile: workgroups go round-robin to the XCDs, and each XCD's run is contiguous in an order of
-// slices, and in a slice of groups of kGroupM row tiles, column by column, so that tiles that run together share operand panels in its L2.
+// slices, and in a slice of groups of kGroupM row tiles, column by column, so that tiles that run together share
+// operand panels in its L2.
 __device__ __forceinline__ void tile_of(int bid, int G, int mt, int nt, int tiles, int& slice, int& ti, int& tj) {
   const int each = G / kXcds, more = G % kXcds, x = bid % kXcds;
   int vid = x * each + (x < more ? x : more) + bid / kXcds;
@@ -746,7 +747,8 @@ __global__ __launch_bounds__(kKinds[KIND].threads(), KIND == 3 ? 3 : 2) void for
 // bytes of each of 8 rows: with 64 bytes of 16 rows, the MFMA's own layout, whole lines are asked for twice and a CU
 // draws 20 GB/s instead of 28 (1 x 28672 x 8192: 92 against 67 us).  So a wavefront passes its operands through LDS
 // of its own, which needs no barrier (its LDS accesses complete in order).  U steps of 64 reduction indices are in
-// flight.  Bound by the weights' bytes: 58.7 MB at 1 x 2048 x 7168 (SwiGLU) in 10.1 us, 5.8 TB/s.  The wavefronts' sums meet in LDS and are added in order.
+// flight.  Bound by the weights' bytes: 58.7 MB at 1 x 2048 x 7168 (SwiGLU) in 10.1 us, 5.8 TB/s.  The wavefronts'
+// sums meet in LDS and are added in order.
 template <bool DUAL, int NK, int U>
 __global__ __launch_bounds__(NK * 64) void skinny_kernel(Gemm g) {
   constexpr int COLS = DUAL ? 8 : 16;  // output columns
@@ -972,8 +974,8 @@ __device__ __forceinline__ void bias_sum(char* smem, const BiasSums& b, int bid)
 
 // The backward pass's products in one launch (8192 x 2816 x 2048 SwiGLU, 378 GFLOP: 330-350 us, MFMA 55 % busy at 2.0
 // GHz, because 432 tiles of 88 and 128 stages leave 80 CUs without a second one; splitting the weight gradients to
-// even that out would write and read 100-180 MB of partial tiles), so that the tiles of one fill the CUs that another leaves idle: the
-// input gradient (rows, columns; jobs 0 .. nx - 1, at most one; ahead of the others by 2-4 % at 8192 x 2816 x 2048),
+// even that out would write and read 100-180 MB of partial tiles), so that the tiles of one fill the CUs that another
+// leaves idle: the input gradient (rows, columns; jobs 0 .. nx - 1, at most one; ahead of the others by 2-4 % at 8192 x 2816 x 2048),
 // the weight gradients (both operands columns) and the bias gradients (from workgroup bias_first on).
 struct BackwardJobs {
   Job j[3];
