@@ -13,6 +13,7 @@
 // BM or BN columns, and read with the transposing LDS read (ds_read_b64_tr_b16:
 // the 16 lanes of a group, reading 4 rows of 16 columns, each get one column),
 // so no operand is transposed in memory.
+#include "linear_layout.h"
 #include "operators.h"
 
 #include <atomic>
@@ -20,8 +21,6 @@
 
 namespace moe {
 namespace {
-
-constexpr int BK = 64;  // reduction indices per stage
 
 typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
@@ -33,7 +32,6 @@ __device__ __forceinline__ float bf2f(uint16_t h) { return __builtin_bit_cast(fl
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
-constexpr uint32_t kOut = 0x80000000u;  // a byte offset past every resource
 
 // 1 / (1 + e^-z) with the hardware exp2 and reciprocal (about 1 ulp each).
 __device__ __forceinline__ float sigmoid_f(float z) {
@@ -65,22 +63,6 @@ __device__ __forceinline__ float activate_grad(int act, float z) {
 // ---------------------------------------------------------------------------
 // Operand staging
 // ---------------------------------------------------------------------------
-// Rows operand: LDS row of 128 B per operand row, 16-byte chunk index XORed with row / 2.  A fragment read takes 16
-// rows at four chunks; the 16 lanes served together are rows 0-3 and 12-15 at one chunk and rows 4-11 at the next
-// one (or the other way round), which this spreads over all 64 banks, as it does 16 rows at one chunk.
-__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
-// Paired rows operand (the forward product's weights): a fragment's rows are 8 (lane / 4 % 4) + lane % 4 of a block of
-// 32, plus 4 for its partner, so that a lane's results of both are eight columns side by side: outputs are written 16
-// bytes at a time.  The 16 lanes served together are again at two neighbouring chunks.
-__device__ __forceinline__ int swz_p(int row) { return ((row >> 1) & 1) | ((row >> 3) & 3) << 1; }
-// Columns operand of C columns: LDS row of 2 C bytes per reduction index; half a wavefront of a transposing read
-// takes 32 bytes of each of the rows r..r + 3 and r + 8..r + 11, so the 64-byte unit is XORed with the row and the
-// 32-byte half of it with row / 8 to spread those over all 64 banks.
-template <int C>
-__device__ __forceinline__ int swz_t(int r) {
-  return (C >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | ((r >> 3) & 1) << 1;
-}
-
 // MFMA fragment (16 operand rows from row c0, 32 reduction indices from 32 ks) of a staged operand: lane holds
 // row c0 + lane % 16, reduction indices 32 ks + 8 (lane / 16) + 0..7.
 // (paired: the block of 32 rows from c0 on, its fragment `half`).
@@ -318,47 +300,23 @@ struct Tile {
   static_assert(TN % VW == 0, "pairs of fragments");
   static_assert(HM >= 1 && TN >= 1 && A_PIECES >= 1 && B_PIECES >= 1, "tile too small for the wavefronts");
 
-  // An operand's C rows (columns) from c0 on, as this lane loads them.  Stage kt is read through a resource based
-  // at its first element; rows and reduction indices past the operand's end lie outside of it.
+  // An operand's C rows (columns) from c0 on, as this lane loads them: stage kt through a resource at its first element.
   template <bool COLS, int C, bool PAIRED = false>
   struct Source {
     const char *base, *base2;  // stage 0 of the two segments (base2 less the first segment's stages)
-    int64_t adv;               // bytes between stages
-    int full, tail;            // resource bytes of a stage, and of a segment's last stage
-    int seg, k1;
-    uint32_t off, step;        // this lane's byte offset of piece 0, and between pieces
-    int klim;                  // rows operand: stages whose chunk of this lane lies before the reduction's end
+    SourceMap<COLS, C, NW, PAIRED> map;
+    uint32_t off, step;
 
-    __device__ __forceinline__ Source(const Operand& o, int64_t c0, int seg_, int k1_, int wave, int lane)
-        : seg(seg_), k1(k1_) {
-      adv = COLS ? BK * o.ld * 2 : BK * 2;
+    __device__ __forceinline__ Source(const Operand& o, int64_t c0, int seg, int k1, int wave, int lane)
+        : map(o.ld, o.extent, o.R, c0, seg, k1, wave, lane), off(map.off), step(map.step) {
       base = reinterpret_cast<const char*>(o.p + (COLS ? c0 : c0 * o.ld));
-      base2 = o.p2 ? reinterpret_cast<const char*>(o.p2 + (COLS ? c0 : c0 * o.ld)) - seg * adv : nullptr;
-      if (!COLS) {
-        const int left = (int)(o.extent - c0 < C ? o.extent - c0 : C);
-        full = tail = (int)(((left - 1) * o.ld + BK) * 2);
-        const int row = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ (PAIRED ? swz_p(row) : swz(row));
-        off = (uint32_t)((row * o.ld + chunk * 8) * 2);
-        step = (uint32_t)(8 * NW * o.ld * 2);  // (8 NW rows on, the swizzle is the same)
-        klim = (int)((o.R - chunk * 8 + BK - 1) / BK);
-      } else {
-        constexpr int LPR = C / 8;  // lanes per LDS row
-        const int last = (int)(o.R - (int64_t)(seg - 1) * BK);  // reduction indices in a segment's last stage
-        full = (int)(((BK - 1) * o.ld + (o.extent - c0)) * 2);
-        tail = (int)(((last - 1) * o.ld + (o.extent - c0)) * 2);
-        const int r = wave * (64 / LPR) + lane / LPR, chunk = (lane % LPR) ^ swz_t<C>(r);
-        off = c0 + chunk * 8 < o.extent ? (uint32_t)((r * o.ld + chunk * 8) * 2) : kOut;
-        step = (uint32_t)(NW * (64 / LPR) * o.ld * 2);
-        klim = 0;
-      }
+      base2 = o.p2 ? reinterpret_cast<const char*>(o.p2 + (COLS ? c0 : c0 * o.ld)) - seg * map.adv : nullptr;
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int kt) const {
-      const bool second = base2 && kt >= seg;
-      const bool short_stage = COLS && (kt == seg - 1 || kt == 2 * seg - 1);
-      const int bytes = kt >= k1 ? 0 : short_stage ? tail : full;
-      return make_rsrc((second ? base2 : base) + kt * adv, bytes);
+      const bool second = base2 && kt >= map.seg;
+      return make_rsrc((second ? base2 : base) + kt * map.adv, map.bytes(kt));
     }
-    __device__ __forceinline__ uint32_t offset(int kt) const { return COLS || kt < klim ? off : kOut; }
+    __device__ __forceinline__ uint32_t offset(int kt) const { return map.offset(kt); }
   };
 
   struct Stage {  // where a stage's loads come from
