@@ -27,8 +27,9 @@
  *                               for balance, expert groups and a scale
  *   moe_linear                  dense product with bias, activation and
  *                               residual (shared expert, projections)
- *   moe_route_grouped_backward, moe_combine_backward, moe_linear_backward
- *                               gradients of the three
+ *   moe_route_grouped_backward, moe_route_grouped_bias_backward,
+ *   moe_combine_backward, moe_linear_backward
+ *                               gradients of the two and of moe_combine
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer unless stated otherwise, and
@@ -343,10 +344,14 @@ moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, 
                              void* stream);
 
 /*
- * moe_route_grouped_backward -- gradient of topk_w with respect to logits for
- * a fixed choice topk_idx (the choice itself, and so the bias and the groups,
- * has no gradient).
+ * moe_route_grouped_bias_backward -- gradient of topk_w with respect to logits
+ * for a fixed choice topk_idx (the choice itself, and so the groups and the
+ * bias's values, has no gradient).
  *
+ *   bias        [E] fp32, moe_route_grouped's, or NULL.  Its finite values
+ *               count for nothing here; an expert that it bars (-inf or NaN)
+ *               has score 0, takes no part in the softmax's sum and gets no
+ *               gradient.
  *   topk_idx    [T, k] int32 as moe_route_grouped writes it; slots outside
  *               [0, E) take no part.
  *   d_topk_w    [T, k] fp32: gradient of topk_w.
@@ -359,6 +364,12 @@ moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, 
  * d_logits must not overlap the inputs (checked).
  * Requires k <= E, E <= 1024, k <= 32, scale finite.
  */
+moe_status moe_route_grouped_bias_backward(const float* logits, const float* bias, const int32_t* topk_idx,
+                                           const float* d_topk_w, int64_t T, int32_t E, int32_t k, int32_t score,
+                                           int32_t renormalize, float scale, float* d_logits, void* stream);
+
+/* moe_route_grouped_backward -- the same with bias NULL: the gradient of a
+ * forward call without a bias, or with one that bars no expert. */
 moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
                                       int64_t T, int32_t E, int32_t k, int32_t score, int32_t renormalize,
                                       float scale, float* d_logits, void* stream);

@@ -330,9 +330,9 @@ moe_status moe_route_grouped(const float* logits, const float* bias, int64_t T, 
   return launched(moe::launch_route_grouped(a, static_cast<hipStream_t>(stream)));
 }
 
-moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, int64_t T,
-                                      int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
-                                      float* d_logits, void* stream) {
+moe_status moe_route_grouped_bias_backward(const float* logits, const float* bias, const int32_t* topk_idx,
+                                           const float* d_topk_w, int64_t T, int32_t E, int32_t k, int32_t score,
+                                           int32_t renormalize, float scale, float* d_logits, void* stream) {
   if (T < 0 || E < 1 || k < 1 || k > E || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || k > 32 || T > (int64_t)INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
@@ -340,12 +340,20 @@ moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_i
   const void* ptrs[] = {logits, topk_idx, d_topk_w, d_logits};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(bias)) return MOE_ERR_INVALID_ARG;
   const size_t te = (size_t)T * E * 4, tk = (size_t)T * k * 4;
-  const Span outs[] = {{d_logits, te}}, ins[] = {{logits, te}, {topk_idx, tk}, {d_topk_w, tk}};
+  const Span outs[] = {{d_logits, te}}, ins[] = {{logits, te}, {bias, (size_t)E * 4}, {topk_idx, tk}, {d_topk_w, tk}};
   if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
-  const moe::RouteBwdArgs a{logits, topk_idx, d_topk_w, T, E, k, score == MOE_SCORE_SIGMOID, renormalize != 0, scale,
-                            d_logits};
+  const moe::RouteBwdArgs a{logits, bias, topk_idx, d_topk_w, T, E, k, score == MOE_SCORE_SIGMOID, renormalize != 0,
+                            scale, d_logits};
   return launched(moe::launch_route_grouped_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, int64_t T,
+                                      int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
+                                      float* d_logits, void* stream) {
+  return moe_route_grouped_bias_backward(logits, nullptr, topk_idx, d_topk_w, T, E, k, score, renormalize, scale,
+                                         d_logits, stream);
 }
 
 moe_status moe_combine_backward(const float* d_out, const float* y_perm, const int32_t* inv_perm, const float* topk_w,

@@ -22,6 +22,7 @@ hipError_t launch_route_grouped(const RouteArgs& a, hipStream_t s);
 
 struct RouteBwdArgs {
   const float* logits;
+  const float* bias;  // may be null
   const int32_t* idx;
   const float* d_w;
   int64_t T;

@@ -437,7 +437,7 @@ __device__ __forceinline__ Slot load_slot(const RouteBwdArgs& a, int64_t t, bool
     if (s.id >= 0) {
       const float v = a.logits[t * a.E + s.id];
       s.lg = fminf(v, FLT_MAX);
-      if (!(v > -INFINITY)) s.id = -1;  // an expert that is not available has score 0
+      if (!(v > -INFINITY) || (a.bias && !(a.bias[s.id] > -INFINITY))) s.id = -1;  // not available: score 0
     }
   }
   return s;
@@ -460,9 +460,9 @@ __device__ __forceinline__ float slot_term(const RouteBwdArgs& a, const Slot& s,
   return a.sigmoid ? s.g * sigmoid_of(s.lg) * sigmoid_of(-s.lg) : s.g * (exp_of(s.lg - m) * iz);
 }
 
-// V consecutive logits from e, -inf where there are none.
+// V consecutive logits from e, -inf where there are none or the expert is not available.
 template <int V>
-__device__ __forceinline__ void load_row(float (&x)[V], const float* row, int e, bool in) {
+__device__ __forceinline__ void load_row(float (&x)[V], const float* row, const float* bias, int e, bool in) {
 #pragma unroll
   for (int q = 0; q < V; ++q) x[q] = -INFINITY;
   if (in) {
@@ -476,6 +476,11 @@ __device__ __forceinline__ void load_row(float (&x)[V], const float* row, int e,
   }
 #pragma unroll
   for (int q = 0; q < V; ++q) x[q] = x[q] > -INFINITY ? fminf(x[q], FLT_MAX) : -INFINITY;
+  if (bias && in) {
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+      if (!(bias[e + q] > -INFINITY)) x[q] = -INFINITY;
+  }
 }
 template <int V>
 __device__ __forceinline__ void store_row(float* row, int e, const float (&o)[V]) {
@@ -508,7 +513,7 @@ __global__ __launch_bounds__(kTokens* kWave) void route_rows_backward_kernel(Rou
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
         const int e = V * (lane + 64 * i);
-        load_row<V>(o[w][i], a.logits + (t0 + w) * E, e, t0 + w < a.T && e < E);
+        load_row<V>(o[w][i], a.logits + (t0 + w) * E, a.bias, e, t0 + w < a.T && e < E);
       }
   const Slot s = load_slot(a, t0 + sub, t0 + sub < a.T, lane & (LT - 1));
   float m = 0.f, iz = 0.f;
@@ -579,7 +584,7 @@ __global__ __launch_bounds__(kTokens* kWave) void route_small_backward_kernel(Ro
   const bool live = t < a.T, in = live && e < a.E;
   const bool dense = !a.sigmoid && !a.renormalize;
   float o[4];
-  load_row<4>(o, a.logits + t * a.E, e, in && dense);
+  load_row<4>(o, a.logits + t * a.E, a.bias, e, in && dense);
   const Slot s = load_slot(a, t, live, l);
   float m = 0.f, iz = 0.f;
   if (dense) {

@@ -57,6 +57,7 @@ _SIGNATURES = {
     "moe_combine": (ctypes.c_int, [_p, _p, _p, _i64, _i32, _i32, _i64, _p, _p]),
     "moe_route_grouped": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _p, _p, _p]),
     "moe_route_grouped_backward": (ctypes.c_int, [_p, _p, _p, _i64, _i32, _i32, _i32, _i32, _f32, _p, _p]),
+    "moe_route_grouped_bias_backward": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _f32, _p, _p]),
     "moe_combine_backward": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i64, _p, _p, _p]),
     "moe_linear_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "moe_linear": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _sz, _p]),
@@ -415,17 +416,20 @@ def moe_route_grouped(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor]
 
 def moe_route_grouped_backward(logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor,
                                score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
-                               d_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Gradient of moe_route_grouped's topk_w with respect to logits, for its choice topk_idx."""
+                               d_logits: Optional[torch.Tensor] = None, stream=None,
+                               bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of moe_route_grouped's topk_w with respect to logits, for its choice topk_idx; bias: the forward call's,
+    which matters where it bars experts (-inf or NaN)."""
     if stream is not None:
-        return _on(stream, moe_route_grouped_backward, logits, topk_idx, d_topk_w, score, renormalize, scale, d_logits)
+        return _on(stream, moe_route_grouped_backward, logits, topk_idx, d_topk_w, score, renormalize, scale, d_logits,
+                   bias=bias)
     T, E = _matrix(logits, "logits")
     dev, k = logits.get_device(), _matrix(topk_idx, "topk_idx")[1]
     if d_logits is None:
         d_logits = torch.empty_like(logits)
     f32 = torch.float32
-    _launch((_lib or lib()).moe_route_grouped_backward, "moe_route_grouped_backward", dev,
-            _take(logits, "logits", f32, (T, E), dev), _take(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+    _launch((_lib or lib()).moe_route_grouped_bias_backward, "moe_route_grouped_backward", dev,
+            _take(logits, "logits", f32, (T, E), dev), _take(bias, "bias", f32, (E,), dev, True), _take(topk_idx, "topk_idx", torch.int32, (T, k), dev),
             _take(d_topk_w, "d_topk_w", f32, (T, k), dev), T, E, k, _choice(SCORES, score, "score"),
             1 if renormalize else 0, scale, _take(d_logits, "d_logits", f32, (T, E), dev))
     return d_logits

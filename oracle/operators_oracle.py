@@ -71,24 +71,26 @@ def route_grouped(logits, k, bias=None, score="softmax", n_group=1, topk_group=1
     return idx, w
 
 
-def gate_weights(logits, idx, score, renormalize, scale):
-    """topk_w for a fixed choice (slots outside [0, E) are empty)."""
+def gate_weights(logits, idx, score, renormalize, scale, bias=None):
+    """topk_w for a fixed choice (slots outside [0, E) are empty); the bias matters where it bars experts."""
     logits = np.asarray(logits, np.float64)
+    b = None if bias is None else np.asarray(bias, np.float64)
     w = np.zeros(idx.shape)
     for t in range(len(idx)):
-        s, x, ok = _row_scores(logits[t], None, score)
+        s, x, ok = _row_scores(logits[t], b, score)
         has = [j for j, e in enumerate(idx[t]) if 0 <= e < logits.shape[1] and ok[e]]
         w[t, has] = _weights(s, x, idx[t][has].astype(int), score, renormalize, scale)
     return w
 
 
-def route_grouped_backward(logits, idx, d_w, score, renormalize, scale):
+def route_grouped_backward(logits, idx, d_w, score, renormalize, scale, bias=None):
     """(d_logits, magnitude): the gradient and, for tolerances, the sum of the absolute terms it is made of."""
     logits = np.asarray(logits, np.float64)
+    b = None if bias is None else np.asarray(bias, np.float64)
     T, E = logits.shape
     out, mag = np.zeros((T, E)), np.zeros((T, E))
     for t in range(T):
-        s, x, ok = _row_scores(logits[t], None, score)
+        s, x, ok = _row_scores(logits[t], b, score)
         has = [j for j, e in enumerate(idx[t]) if 0 <= e < E and ok[e]]
         ids, g = idx[t][has].astype(int), scale * np.asarray(d_w[t], np.float64)[has]
         if not len(ids):

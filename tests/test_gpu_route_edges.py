@@ -1,0 +1,113 @@
+"""Routing on the GPU where bias, masks and magnitudes are at their edges, against the float64 oracle.
+
+Indices are compared exactly.  Tolerances (u = 2^-24, half an fp32 step): a gate weight is a quotient of an fp32
+exponential and a sum of at most k of them, within 2e-6 of its value; a gradient is a sum of products of such weights,
+within 4e-6 of the sum of its absolute terms (exponential 2 u, division 1 u, each addition 1 u of positive terms, the
+argument's rounding at most 2 u of |l| <= 16).
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_moe_amd import ffi
+from oracle import operators_oracle as Q
+
+import parity_helpers as P
+
+pytestmark = pytest.mark.gpu
+
+F32 = torch.float32
+INF, NAN, FMAX = float("inf"), float("nan"), float(torch.finfo(torch.float32).max)
+
+
+def dev():
+    return P.require_gpu()
+
+
+def gen(seed):
+    return torch.Generator(device="cpu").manual_seed(seed)
+
+
+def n64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ---------------------------------------------------------------------------
+# Gradient under a bias that bars experts
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (33, 64, 6), (257, 160, 6), (3, 1024, 32), (17, 37, 11), (2051, 256, 8),
+                                   (2050, 130, 5), (9, 512, 17)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("bar", [-INF, NAN])
+def test_gradient_with_barred_experts(T, E, k, score, renorm, bar):
+    g = gen(T + E)
+    l = torch.randn(T, E, generator=g) * 2
+    b = torch.randn(E, generator=g) * 0.1
+    barred = torch.randperm(E, generator=g)[:max(1, E // 8)]
+    b[barred] = bar
+    l[:, barred] += 3.0  # they would be much of the sum
+    b[(barred[0] + 1) % E] = INF  # bars nothing, not even one of those above
+    barred = torch.nonzero(~(b > -INF)).flatten()
+    d_w = torch.randn(T, k, generator=g)
+    d = dev()
+    kw = dict(score=score, renormalize=renorm, scale=1.5)
+    idx, w = ffi.moe_route_grouped(l.to(d), k, bias=b.to(d), **kw)
+    got = ffi.moe_route_grouped_backward(l.to(d), idx, d_w.to(d), bias=b.to(d), **kw)
+    I = idx.cpu().numpy()
+    np.testing.assert_allclose(n64(w), Q.gate_weights(l.numpy(), I, score, renorm, 1.5, b.numpy()), rtol=2e-6)
+    ref, mag = Q.route_grouped_backward(l.numpy(), I, d_w.numpy(), score, renorm, 1.5, b.numpy())
+    assert (np.abs(n64(got) - ref) <= 4e-6 * mag + 1e-37).all()
+    assert not bool(got[:, barred.to(d)].any())
+    # a slot that names a barred expert has score 0 and takes no part
+    I[0, 0] = int(barred[0])
+    got = ffi.moe_route_grouped_backward(l.to(d), torch.from_numpy(I).to(d), d_w.to(d), bias=b.to(d), **kw)
+    ref, mag = Q.route_grouped_backward(l.numpy(), I, d_w.numpy(), score, renorm, 1.5, b.numpy())
+    assert (np.abs(n64(got) - ref) <= 4e-6 * mag + 1e-37).all()
+
+
+def test_gradient_with_barred_experts_against_differences_of_the_forward():
+    """The forward call's own weights, moved: fp32 weights, steps of 2^-6, second differences of at most step^2."""
+    T, E, k, h = 4, 12, 3, 2.0 ** -6
+    g = gen(3)
+    l, b = torch.randn(T, E, generator=g), torch.randn(E, generator=g) * 0.1
+    b[4], b[9] = -INF, NAN
+    l[:, 4] = 3.0
+    d_w = torch.randn(T, k, generator=g)
+    d = dev()
+    kw = dict(score="softmax", renormalize=False)
+    idx, _ = ffi.moe_route_grouped(l.to(d), k, bias=b.to(d), **kw)
+    got = n64(ffi.moe_route_grouped_backward(l.to(d), idx, d_w.to(d), bias=b.to(d), **kw))
+    order = idx.long()
+
+    def weights(x):  # of the chosen experts, in the first choice's order
+        i, w = ffi.moe_route_grouped(x.to(d), E, bias=b.to(d), **kw)
+        full = torch.zeros(T, E, device=d).scatter_(1, i.clamp(min=0).long(), torch.where(i >= 0, w, torch.zeros_like(w)))
+        return n64(full.gather(1, order))
+    for e in range(E):
+        hi, lo = l.clone(), l.clone()
+        hi[:, e] += h
+        lo[:, e] -= h
+        num = ((weights(hi) - weights(lo)) * d_w.numpy()).sum(1) / (2 * h)
+        # softmax: third derivatives at most 1, so h^2 / 6 of each term; weights within 2e-6, over 2 h
+        tol = (h * h / 6 + 2e-6 / h) * np.abs(d_w.numpy()).sum(1)
+        assert (np.abs(got[:, e] - num) <= tol).all(), e
+
+
+def test_gradient_without_a_barring_bias_does_not_depend_on_it():
+    g = gen(4)
+    d = dev()
+    l, b, d_w = torch.randn(70, 64, generator=g).to(d), torch.randn(64, generator=g).to(d), torch.randn(70, 6, generator=g).to(d)
+    for score in ("softmax", "sigmoid"):
+        idx, _ = ffi.moe_route_grouped(l, 6, bias=b, score=score, renormalize=False)
+        a = ffi.moe_route_grouped_backward(l, idx, d_w, score=score, renormalize=False)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        c = ffi.moe_route_grouped_backward(l, idx, d_w, score=score, renormalize=False, bias=b, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(a, c)
+    with pytest.raises(ValueError, match="bias"):
+        ffi.moe_route_grouped_backward(l, idx, d_w, bias=b[:32].contiguous())
+    with pytest.raises(TypeError, match="bias"):
+        ffi.moe_route_grouped_backward(l, idx, d_w, bias=b.double())
