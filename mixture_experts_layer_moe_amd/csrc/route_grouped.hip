@@ -234,12 +234,12 @@ __device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn
 // delta = PL 2^-23 max |key|, with a bias 1.25e-6 + 2.4e-7 max |key| more: scores within 5e-7, the softmax's
 // denominator 5e-7 of them, the sum's rounding.  Two keys in a row within 2 delta (equal ones, whose order is by id,
 // among them), or the last kept and the first dropped group within 5 delta, leave the choice in doubt, and so does an
-// available key next to the value that stands for none.
+// available key next to the value that stands for none, or whose sum with another could be.
 template <int LT, int PL>
 __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& pl, int l, int lane, int e0, const float (&x)[PL],
                                             const float (&b)[PL], float m, int* ids, float& z) {
   constexpr uint32_t kPlace = PL - 1;
-  constexpr float kNone = -3.402e38f, kLeast = -3.3e38f;  // no key; the least that is taken for one
+  constexpr float kNone = -3.402e38f, kLeast = -3.3e38f;  // no key; the least that is taken for one, or for a sum
   const int k = a.k;
   float key[PL];
   bool doubt = false;
@@ -260,7 +260,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& pl,
     least = ok ? fminf(least, v) : least;
     key[i] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, ok ? v : kNone) & ~kPlace) | (uint32_t)i);
   }
-  doubt = least < kLeast;
+  doubt = least < (a.bias && a.group_top == 2 ? -1.6e38f : kLeast);  // (sums of two from -1.6e38 stay above kLeast)
   const float delta = max_of<LT>(big) * (PL * 1.1920929e-7f + (a.bias ? 2.4e-7f : 0.f)) + (a.bias ? 1.25e-6f : 0.f);
   sort_network<PL>([&](int i, int j) {
     const float hi = fmaxf(key[i], key[j]), lo = fminf(key[i], key[j]);

@@ -111,3 +111,29 @@ def test_gradient_without_a_barring_bias_does_not_depend_on_it():
         ffi.moe_route_grouped_backward(l, idx, d_w, bias=b[:32].contiguous())
     with pytest.raises(TypeError, match="bias"):
         ffi.moe_route_grouped_backward(l, idx, d_w, bias=b.double())
+
+
+# ---------------------------------------------------------------------------
+# The choice
+# ---------------------------------------------------------------------------
+
+def check_choice(l, k, b=None, **kw):
+    """Indices and weights of the routing against the oracle's, exactly and within 2e-6."""
+    d = dev()
+    idx, w = ffi.moe_route_grouped(l.to(d), k, bias=None if b is None else b.to(d), **kw)
+    ridx, rw = Q.route_grouped(l.numpy(), k, None if b is None else b.numpy(), **kw)
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    np.testing.assert_allclose(n64(w), rw, rtol=2e-6, atol=1e-37)
+
+
+@pytest.mark.parametrize("T", [5, 2051])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_sums_pass_the_lowest_fp32(T, score):
+    """Pairs of finite biases whose sum is below every fp32: such a group is still one, and still ranked."""
+    b = torch.tensor([1e38, 5e37, -1.8e38, -2.2e38, -1.9e38, -2.0e38, -2.4e38, -2.6e38])
+    l = torch.randn(T, 8, generator=gen(T))
+    check_choice(l, 3, b, score=score, n_group=4, topk_group=2, group_top=2)
+    g = gen(T + 1)
+    for E, G, tg, k in [(64, 8, 3, 6), (256, 8, 4, 8), (96, 3, 2, 9)]:
+        b = -1.6e38 - 1.6e38 * torch.rand(E, generator=g)
+        check_choice(torch.randn(T, E, generator=g), k, b, score=score, n_group=G, topk_group=tg, group_top=2)
