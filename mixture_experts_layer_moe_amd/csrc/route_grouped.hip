@@ -274,9 +274,12 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& pl,
     float gd = delta;
     if (a.group_top == 2) {
       if (!a.bias) {
-        gd += 1.5e-6f;  // (a score changes by at most a quarter of its logit's change)
-        g1 = g1 > kLeast ? score(g1) : g1;
-        g2 = g2 > kLeast ? score(g2) : g2;
+        // A score changes by no more than its logit does (softmax: below the row's largest; a place in a key's last
+        // bits can lift it above, by whole units where logits are in the millions).
+        gd += 1.5e-6f;
+        auto group_score = [&](float v) { return score(a.sigmoid ? v : fminf(v, m)); };
+        g1 = g1 > kLeast ? group_score(g1) : g1;
+        g2 = g2 > kLeast ? group_score(g2) : g2;
       }
       g1 = g2 > kLeast ? g1 + g2 : g1;
     }

@@ -137,3 +137,23 @@ def test_groups_whose_sums_pass_the_lowest_fp32(T, score):
     for E, G, tg, k in [(64, 8, 3, 6), (256, 8, 4, 8), (96, 3, 2, 9)]:
         b = -1.6e38 - 1.6e38 * torch.rand(E, generator=g)
         check_choice(torch.randn(T, E, generator=g), k, b, score=score, n_group=G, topk_group=tg, group_top=2)
+
+
+@pytest.mark.parametrize("T", [67, 2051])
+@pytest.mark.parametrize("E,G", [(256, 8), (1024, 2), (240, 16), (64, 4)])
+@pytest.mark.parametrize("top,step", [(2.5e6, 0.25), (1e9, 64.0), (-2.5e6, 0.25), (4e5, 2.0 ** -5)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_groups_of_large_logits(T, E, G, top, step, renorm):
+    """Sums of two softmax scores with neighbouring fp32 logits at any two places of two groups, far from the others."""
+    g = gen(E + T)
+    Eg = E // G
+    l = torch.full((T, E), top) - 0.01 * abs(top)
+    for t in range(T):
+        ga, gb = torch.randperm(G, generator=g)[:2].tolist()
+        pa, pb = torch.randint(0, Eg, (2,), generator=g).tolist()
+        if t % 2:  # first and last place of a group
+            pa, pb = 0, Eg - 1
+        l[t, ga * Eg + pa] = top + step * int(torch.randint(1, 8, (1,), generator=g))
+        l[t, gb * Eg + pb] = top
+    for k in (1, 3):
+        check_choice(l, k, score="softmax", n_group=G, topk_group=1, group_top=2, renormalize=renorm)
