@@ -290,7 +290,8 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const Place& pl,
     const bool in = keep && g1 > -INFINITY;
     const float low = -max_of<LT>(in ? -g1 : -INFINITY), high = max_of<LT>(keep ? -INFINITY : g1);
     const float kept = sum_of<LT>(in ? 1.f : 0.f);
-    doubt = doubt || low - high <= 5.f * gd || kept > (float)most;
+    // (the last term: places alone, where keys are zeros or below the normal range)
+    doubt = doubt || low - high <= 5.f * gd + 1e-37f || kept > (float)most;
     if (!keep)
 #pragma unroll
       for (int i = 0; i < PL; ++i) key[i] = kNone;

@@ -157,3 +157,15 @@ def test_softmax_groups_of_large_logits(T, E, G, top, step, renorm):
         l[t, gb * Eg + pb] = top
     for k in (1, 3):
         check_choice(l, k, score="softmax", n_group=G, topk_group=1, group_top=2, renormalize=renorm)
+
+
+@pytest.mark.parametrize("T", [67, 2051])
+@pytest.mark.parametrize("E,G,tg", [(32, 2, 1), (256, 8, 1), (100, 5, 1), (1024, 16, 2), (21, 3, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_equal_or_tiny_logits_with_masks(T, E, G, tg, score):
+    """Logits of zero, as at initialisation, or below the normal fp32 range, few of them available: the lowest group wins."""
+    g = gen(E * 3 + T)
+    l = torch.where(torch.rand(T, E, generator=g) < 1.5 / (E // G), 0.0, -INF)
+    l[::3] = torch.where(l[::3] > -INF, torch.randint(-9, 10, l[::3].shape, generator=g) * 1.4e-45, l[::3])
+    check_choice(l, 1, score=score, n_group=G, topk_group=tg, group_top=1)
+    check_choice(l, min(5, tg * (E // G)), score=score, n_group=G, topk_group=tg, group_top=1)
