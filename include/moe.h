@@ -385,7 +385,7 @@ moe_status moe_route_grouped_backward(const float* logits, const int32_t* topk_i
  *   d_topk_w    [T, k] fp32 out: sum over h of d_out[t, h] * y_perm[inv_perm[t, j], h];
  *               0 for a slot that is not local.
  * Outputs must not overlap the inputs or one another (checked).
- * Requires H % 4 == 0, k <= 32.
+ * Requires H % 4 == 0, k <= 32, T <= 2^31 - 1.
  */
 moe_status moe_combine_backward(const float* d_out, const float* y_perm, const int32_t* inv_perm,
                                 const float* topk_w, int64_t T, int32_t k, int32_t H, int64_t R_cap,

@@ -101,15 +101,21 @@ hipError_t launch_combine_backward(const float* d_out, const float* y_perm, cons
   const floatx4* g = reinterpret_cast<const floatx4*>(d_out);
   const floatx4* y = reinterpret_cast<const floatx4*>(y_perm);
   floatx4* d_y = reinterpret_cast<floatx4*>(d_y_perm);
-#define MOE_COMBINE_BWD(V_)                                                                                \
-  hipLaunchKernelGGL(combine_backward_kernel<V_>, dim3((unsigned)T), dim3(kThreads), 0, s, g, y, inv_perm, \
-                     topk_w, k, H4, R_cap, d_y, d_topk_w)
-  // Columns per thread: a row in one span if it has 4096 columns or fewer.
-  if (H4 > 2 * kThreads) MOE_COMBINE_BWD(4);
-  else if (H4 > kThreads) MOE_COMBINE_BWD(2);
-  else MOE_COMBINE_BWD(1);
+  constexpr int64_t kMaxTokens = 1 << 23;  // per launch (a grid holds fewer than 2^32 threads)
+#define MOE_COMBINE_BWD(V_)                                                                                       \
+  hipLaunchKernelGGL(combine_backward_kernel<V_>, dim3(n), dim3(kThreads), 0, s, g + t * H4, y, inv_perm + t * k, \
+                     topk_w + t * k, k, H4, R_cap, d_y, d_topk_w + t * k)
+  for (int64_t t = 0; t < T; t += kMaxTokens) {
+    const unsigned n = (unsigned)(T - t < kMaxTokens ? T - t : kMaxTokens);
+    // Columns per thread: a row in one span if it has 4096 columns or fewer.
+    if (H4 > 2 * kThreads) MOE_COMBINE_BWD(4);
+    else if (H4 > kThreads) MOE_COMBINE_BWD(2);
+    else MOE_COMBINE_BWD(1);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
 #undef MOE_COMBINE_BWD
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace moe

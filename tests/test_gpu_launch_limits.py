@@ -1,0 +1,30 @@
+"""Sizes whose work-items would pass 2^32 in one launch: split over launches, or run in larger tiles."""
+import pytest
+import torch
+
+from mixture_experts_layer_moe_amd import ffi
+
+import parity_helpers as P
+
+pytestmark = pytest.mark.gpu
+
+
+def test_combine_backward_of_more_tokens_than_one_launch_takes():
+    d = P.require_gpu()
+    T, H, k, R = (1 << 24) + 70, 4, 1, 64
+    g = torch.Generator(device=d).manual_seed(1)
+    d_out = torch.randint(-3, 4, (T, H), generator=g, device=d, dtype=torch.int32).float()
+    y = torch.randint(-3, 4, (R, H), generator=g, device=d, dtype=torch.int32).float()
+    w = torch.randint(1, 4, (T, k), generator=g, device=d, dtype=torch.int32).float()
+    half = 1 << 23
+    tokens = torch.tensor([0, 1, half - 2, half - 1, half, half + 1, 2 * half - 1, 2 * half, T - 2, T - 1], device=d)
+    inv = torch.full((T, k), -1, dtype=torch.int32, device=d)
+    inv[tokens, 0] = torch.arange(len(tokens), dtype=torch.int32, device=d) * 5 + 2
+    d_y, d_w = ffi.moe_combine_backward(d_out, y, inv, w, torch.full((R, H), 9.0, device=d), torch.full((T, k), 9.0, device=d))
+    rows = inv[tokens, 0].long()
+    want = torch.full((R, H), 9.0, device=d)
+    want[rows] = d_out[tokens] * w[tokens]
+    assert torch.equal(d_y, want)
+    assert torch.equal(d_w[tokens, 0], (d_out[tokens] * y[rows]).sum(1))
+    d_w[tokens] = 0
+    assert not bool(d_w.any())
