@@ -86,9 +86,10 @@ hipError_t launch_combine(const float* y_perm, const int32_t* inv_perm, const fl
   // Float4 columns per thread: enough that one block covers the row (up to 4),
   // so a token's index and weight loads are paid once.
   const int vec = H4 >= 4 * kThreads ? 4 : H4 >= 2 * kThreads ? 2 : 1;
+  constexpr int64_t kMaxTokens = 1 << 23;  // per launch (a grid holds fewer than 2^32 threads)
 #define MOE_COMBINE_LAUNCH(KV, V)                                                                              \
-  hipLaunchKernelGGL((combine_kernel<KV, V>), dim3((unsigned)T, (unsigned)((H4 + kThreads * V - 1) / (kThreads * V))), \
-                     dim3(kThreads), 0, s, y, inv_perm, topk_w, k, H4, R_cap, o)
+  hipLaunchKernelGGL((combine_kernel<KV, V>), dim3(n, (unsigned)((H4 + kThreads * V - 1) / (kThreads * V))),   \
+                     dim3(kThreads), 0, s, y, inv_perm + t * k, topk_w + t * k, k, H4, R_cap, o + t * H4)
 #define MOE_COMBINE_V(V)                                  \
   switch (k) {                                            \
     case 1: MOE_COMBINE_LAUNCH(1, V); break;              \
@@ -98,16 +99,21 @@ hipError_t launch_combine(const float* y_perm, const int32_t* inv_perm, const fl
     case 8: MOE_COMBINE_LAUNCH(8, V); break;              \
     default: MOE_COMBINE_LAUNCH(0, V); break;             \
   }
-  if (vec == 4) {
-    MOE_COMBINE_V(4)
-  } else if (vec == 2) {
-    MOE_COMBINE_V(2)
-  } else {
-    MOE_COMBINE_V(1)
+  for (int64_t t = 0; t < T; t += kMaxTokens) {
+    const unsigned n = (unsigned)(T - t < kMaxTokens ? T - t : kMaxTokens);
+    if (vec == 4) {
+      MOE_COMBINE_V(4)
+    } else if (vec == 2) {
+      MOE_COMBINE_V(2)
+    } else {
+      MOE_COMBINE_V(1)
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
 #undef MOE_COMBINE_V
 #undef MOE_COMBINE_LAUNCH
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace moe

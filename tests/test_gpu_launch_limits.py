@@ -28,3 +28,15 @@ def test_combine_backward_of_more_tokens_than_one_launch_takes():
     assert torch.equal(d_w[tokens, 0], (d_out[tokens] * y[rows]).sum(1))
     d_w[tokens] = 0
     assert not bool(d_w.any())
+
+
+def test_combine_of_more_tokens_than_one_launch_takes():
+    d = P.require_gpu()
+    T, H, k, R = (1 << 24) + 70, 4, 2, 64
+    g = torch.Generator(device=d).manual_seed(2)
+    y = torch.randint(-3, 4, (R, H), generator=g, device=d, dtype=torch.int32).float()
+    w = torch.randint(1, 4, (T, k), generator=g, device=d, dtype=torch.int32).float()
+    inv = torch.randint(-1, R, (T, k), generator=g, device=d, dtype=torch.int32)
+    out = ffi.moe_combine(y, inv, w, torch.full((T, H), 9.0, device=d))
+    rows = torch.where((inv >= 0)[:, :, None], y[inv.clamp(min=0).long()], torch.zeros((), device=d))
+    assert torch.equal(out, (rows * w[:, :, None]).sum(1))
