@@ -142,7 +142,7 @@ moe_status moe_route_topk(const float* logits, int64_t T, int32_t E, int32_t k,
  * moe_grouped_ffn_gather, which reads the token rows from x itself.
  * ws / ws_bytes: device scratch of at least moe_permute_workspace_bytes().
  * Requires H % 8 == 0, tile_m in {16, 32, 64, 128, 256},
- * E_loc * num_ranks <= 4096, num_ranks <= 64, k <= 32.
+ * E_loc * num_ranks <= 4096, num_ranks <= 64, k <= 32, T <= 2^26 - 16.
  */
 moe_status moe_permute(const void* x, const int32_t* topk_idx, const int32_t* src_rank,
                        int64_t T, int32_t H, int32_t k, int32_t E, int32_t expert_begin,

@@ -98,6 +98,7 @@ moe_status permute_impl(const void* x, const int32_t* topk_idx, const int32_t* s
     return MOE_ERR_UNSUPPORTED;
   const int64_t R_cap = moe_rows_capacity(T, k, E_loc, tile_m);
   if (T * (int64_t)k > INT32_MAX || R_cap > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (T > (1 << 26) - 16) return MOE_ERR_UNSUPPORTED;  // a wavefront a token: a grid holds fewer than 2^32 threads
   if (T == 0) return MOE_OK;
   // x and x_perm both null: indices only (the rows are gathered later by moe_grouped_ffn_gather).
   if ((x == nullptr) != (x_perm == nullptr)) return MOE_ERR_INVALID_ARG;
