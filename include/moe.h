@@ -431,7 +431,9 @@ size_t moe_linear_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
  * over workgroups and sum the fp32 partials in a fixed order, so results are
  * deterministic, and differ from those without ws by fp32 summation order.  A
  * non-NULL ws that is too small returns MOE_ERR_WORKSPACE.
- * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1.  M == 0: nothing to do.
+ * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1, and at most 8 million
+ * tiles of 256 rows and 256 columns (SwiGLU: 128), which are 10^12 bytes of out
+ * where N > 128; more may return MOE_ERR_UNSUPPORTED.  M == 0: nothing to do.
  */
 moe_status moe_linear(const void* x, const void* w, const void* w_up, const float* bias, const float* bias_up,
                       const void* residual, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,
@@ -458,8 +460,10 @@ size_t moe_linear_backward_workspace_bytes(int64_t M, int32_t N, int32_t K, int3
  * (checked).
  * ws / ws_bytes: device scratch of at least
  * moe_linear_backward_workspace_bytes(); needed whenever M > 0.
- * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1.  M == 0: the weight and
- * bias gradients are set to zero.
+ * Requires K % 8 == 0; N, K <= 1048576; M <= 2^31 - 1, and at most 8 million
+ * tiles of 256 x 256 of d_x, d_w and d_w_up together (asked for or not); more
+ * may return MOE_ERR_UNSUPPORTED.  M == 0: the weight and bias gradients are
+ * set to zero.
  */
 moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, const void* w_up, const void* z,
                                const void* z_up, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,

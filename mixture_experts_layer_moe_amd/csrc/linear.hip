@@ -1035,6 +1035,7 @@ Plan make_plan(const Size* z, int n, int nmat, bool split) {
   constexpr double kFixed[] = {9.0, 6.0, 5.0, 3.5};        // us a workgroup: first stage's latency and epilogue
   constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
   constexpr double kUneven = 2.6;  // two workgroups a CU on average, where three fit: many CUs get three
+  constexpr double kMaxThreads = 4294967295.0 - (1 << 25);  // of a grid, less the bias sums' (N <= 2^20)
   const int cus = device_cus();
   Plan best{};
   best.time = 1e30;
@@ -1060,7 +1061,7 @@ Plan make_plan(const Size* z, int n, int nmat, bool split) {
           bytes += 2.0 * p.part_bytes[q];
         }
       }
-      if (!any || blocks > 2.0e9) continue;
+      if (!any || blocks * kKinds[kind].threads() > kMaxThreads) continue;
       const double per_block = work / blocks;          // stages of an average workgroup
       int64_t left = (int64_t)((blocks + cus - 1) / cus);  // workgroups of the fullest CU
       double t = 0, rest = blocks;
@@ -1133,6 +1134,7 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   const int nmat = dual ? 2 : 1;
   const ForwardPlan f = forward_plan(a.M, a.N, a.K, nmat, a.ws != nullptr);
   const int64_t main = a.M - f.rest;
+  if (main > 0 && f.tiles.tiles[0] < 1) return hipErrorNotSupported;  // (no tiling has few enough workgroups)
   // The product of rows [row, row + rows).
   auto product = [&](int64_t row, int64_t rows) {
     Gemm g{};
@@ -1156,7 +1158,6 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   }
   if (main == 0 || e != hipSuccess) return e;
   const Plan& p = f.tiles;
-  if (p.tiles[0] < 1) return hipErrorInvalidValue;
   Job j{};
   j.g = product(0, main);
   set_tiles(j.g, p.kind, nmat);
@@ -1225,7 +1226,7 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
     return e;
   }
   const BackwardLayout l = backward_layout(a.M, a.N, a.K, a.act);
-  if (l.plan.tiles[0] < 1) return hipErrorInvalidValue;  // (no tiling has few enough workgroups)
+  if (l.plan.tiles[0] < 1) return hipErrorNotSupported;  // (no tiling has few enough workgroups)
   const int mats = l.mats, Np = l.Np, ld = l.ld;
   uint16_t* dz = static_cast<uint16_t*>(a.ws);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(a.ws) + l.sums);
@@ -1289,7 +1290,6 @@ hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s) {
   jobs.bias = {sums, l.blocks, a.N, mats, a.d_bias, a.d_bias_up};
   if (bias) blocks += (mats * (int64_t)a.N + 63) / 64;
   if (blocks == 0) return hipSuccess;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const Kind& kind = kKinds[l.plan.kind];
   const dim3 grid((unsigned)blocks), block(kind.threads());
   if (l.plan.kind == 0) hipLaunchKernelGGL(backward_kernel<0>, grid, block, 0, s, jobs);

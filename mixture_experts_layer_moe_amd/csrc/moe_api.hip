@@ -388,6 +388,9 @@ moe_status linear_sizes(int64_t M, int32_t N, int32_t K, int32_t act) {
   return MOE_OK;
 }
 
+// hipErrorNotSupported: a product of more tiles than a launch takes, found before anything is enqueued.
+moe_status linear_launched(hipError_t e) { return e == hipErrorNotSupported ? MOE_ERR_UNSUPPORTED : launched(e); }
+
 }  // namespace
 
 extern "C" {
@@ -432,7 +435,7 @@ moe_status moe_linear(const void* x, const void* w, const void* w_up, const floa
   a.z_up = static_cast<uint16_t*>(z_up);
   a.out = out;
   a.ws = ws;
-  return launched(moe::launch_linear(a, static_cast<hipStream_t>(stream)));
+  return linear_launched(moe::launch_linear(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_linear_backward_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act) {
@@ -481,7 +484,7 @@ moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, 
   a.d_bias = d_bias;
   a.d_bias_up = d_bias_up;
   a.ws = ws;
-  return launched(moe::launch_linear_backward(a, static_cast<hipStream_t>(stream)));
+  return linear_launched(moe::launch_linear_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -40,3 +40,18 @@ def test_combine_of_more_tokens_than_one_launch_takes():
     out = ffi.moe_combine(y, inv, w, torch.full((T, H), 9.0, device=d))
     rows = torch.where((inv >= 0)[:, :, None], y[inv.clamp(min=0).long()], torch.zeros((), device=d))
     assert torch.equal(out, (rows * w[:, :, None]).sum(1))
+
+
+def test_linear_of_more_small_tiles_than_one_launch_takes():
+    """2^24 tiles of 64 rows and more, which small products would take: larger ones run instead."""
+    d = P.require_gpu()
+    M, N, K = (1 << 30) + 70, 1, 8
+    g = torch.Generator(device=d).manual_seed(3)
+    x = torch.randint(-2, 3, (M, K), generator=g, device=d, dtype=torch.int8).to(torch.bfloat16)
+    w = torch.randint(-2, 3, (N, K), generator=g, device=d, dtype=torch.int8).to(torch.bfloat16)
+    out = ffi.moe_linear(x, w, out=torch.full((M, N), 99.0, dtype=torch.bfloat16, device=d))
+    for i in range(0, M, 1 << 27):
+        want = torch.zeros(min(M - i, 1 << 27), device=d)
+        for q in range(K):
+            want += x[i:i + (1 << 27), q].float() * w[0, q].float()
+        assert torch.equal(out[i:i + (1 << 27), 0].float(), want), i
