@@ -1,7 +1,8 @@
-// Where the loads of the dense projection's tiles lie: integer arithmetic alone, so that a host test can walk every
-// lane of every stage through it.
+// How the dense projection divides its products into tiles and launches, and where the tiles' loads lie: arithmetic
+// alone, so that a host test can ask for a size's tiles and walk every lane of every stage.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 
 namespace moe {
@@ -65,5 +66,129 @@ struct SourceMap {
   }
   constexpr uint32_t offset(int kt) const { return COLS || kt < klim ? off : kOut; }
 };
+
+// ---------------------------------------------------------------------------
+// Tiles and slices
+// ---------------------------------------------------------------------------
+// Tile kinds: rows, columns staged per stage (of one matrix, or half of each of two), wavefronts, workgroups per CU.
+// A stage reads (BM + BN) x 128 bytes for BM BN x 64 products, so large tiles run at a higher rate (the us per stage in
+// make_plan: 1.43, 1.15, 1.01 and 0.84 PFLOP/s) and small ones fill the chip when there are few: 1024 x 2048 x 512
+// takes 8.5 us with 64-row tiles, 4096 x 2048 x 2816 49 us with 256x128 (one round of 256) where 256x256 tiles keep
+// half of the CUs idle.
+struct Kind {
+  int bm, bn, wm, wn, per_cu;
+  constexpr int threads() const { return wm * wn * 64; }
+};
+constexpr Kind kKinds[] = {{256, 256, 2, 4, 1}, {256, 128, 4, 2, 1}, {128, 128, 2, 2, 2}, {64, 128, 2, 2, 3}};
+constexpr int kNumKinds = 4;
+
+inline int stages(int64_t R) { return (int)((R + BK - 1) / BK); }
+
+// How a launch runs: its tile kind and, per product, the slices of the reduction.
+struct Size {
+  int64_t M;
+  int N, nk;
+};
+struct Plan {
+  int kind;
+  int S[3];
+  int64_t tiles[3];
+  size_t part_bytes[3];  // fp32 sums of a split product
+  double time;           // estimated us
+};
+
+constexpr int kMaxSlices = 16;
+
+// Picks the tile kind and slices with the least estimated time, from measured figures of each kind (products of one
+// to seven rounds, K 64 to 4096): a CU runs its share of the launch's workgroups, per_cu of them at a time, a stage of r
+// workgroups taking max(latency, r * rate), plus a fixed cost per workgroup; a split adds the second launch and its
+// traffic.  For a single product the rate is that of the CUs in use, since the others' idling raises their clock (3000 x
+// 3000 x 1000: 144 tiles of 256x256 take 28 us, the 64x128 tiles chosen without this 39); in the backward pass's launch
+// other products fill them.
+inline Plan make_plan(const Size* z, int n, int nmat, bool split, int cus) {
+  constexpr double kRate[] = {1.5, 0.93, 0.53, 0.32};      // us a stage and workgroup, CU full
+  constexpr double kLatency[] = {1.1, 0.73, 0.56, 0.42};   // us a stage, at least
+  constexpr double kFixed[] = {9.0, 6.0, 5.0, 3.5};        // us a workgroup: first stage's latency and epilogue
+  constexpr double kSecond = 5.0, kBytes = 4.0e6;    // us of the second launch; bytes per us of its traffic
+  constexpr double kUneven = 2.6;  // two workgroups a CU on average, where three fit: many CUs get three
+  constexpr double kMaxThreads = 4294967295.0 - (1 << 25);  // of a grid, less the bias sums' (N <= 2^20)
+  Plan best{};
+  best.time = 1e30;
+  for (int kind = 0; kind < kNumKinds; ++kind) {
+    const int bm = kKinds[kind].bm, bn = kKinds[kind].bn / nmat, occ = kKinds[kind].per_cu;
+    for (int S = 1; S <= (split ? kMaxSlices : 1); ++S) {
+      Plan p{};
+      p.kind = kind;
+      double blocks = 0, work = 0, bytes = 0;
+      int longest = 0;
+      bool any = false;
+      for (int q = 0; q < n; ++q) {
+        p.tiles[q] = ((z[q].M + bm - 1) / bm) * ((z[q].N + bn - 1) / bn);
+        const int most = z[q].nk / 4 < 1 ? 1 : z[q].nk / 4;  // at least four stages a slice
+        p.S[q] = S < most ? S : most;
+        any |= p.S[q] == S;
+        const int per = (z[q].nk + p.S[q] - 1) / p.S[q];
+        blocks += (double)p.tiles[q] * p.S[q];
+        work += (double)p.tiles[q] * p.S[q] * per;
+        longest = per > longest ? per : longest;
+        if (p.S[q] > 1) {
+          p.part_bytes[q] = (size_t)p.tiles[q] * p.S[q] * bm * nmat * bn * 4;
+          bytes += 2.0 * p.part_bytes[q];
+        }
+      }
+      if (!any || blocks * kKinds[kind].threads() > kMaxThreads) continue;
+      const double per_block = work / blocks;          // stages of an average workgroup
+      int64_t left = (int64_t)((blocks + cus - 1) / cus);  // workgroups of the fullest CU
+      double t = 0, rest = blocks;
+      while (left > 0) {
+        const int r = left < occ ? (int)left : occ;
+        double at_once = r;
+        if (n == 1) at_once = r == 1 && rest < cus ? rest / cus : r == 2 && occ == 3 ? kUneven : r;
+        const double stage = kLatency[kind] > at_once * kRate[kind] ? kLatency[kind] : at_once * kRate[kind];
+        t += (t == 0 ? longest : per_block) * stage + kFixed[kind];
+        left -= r;
+        rest -= (double)r * cus;
+      }
+      if (bytes > 0) t += kSecond + bytes / kBytes;
+      p.time = t;
+      if (t < best.time) best = p;
+    }
+  }
+  return best;
+}
+
+inline size_t part_bytes(const Plan& p, int n) {
+  size_t b = 0;
+  for (int q = 0; q < n; ++q) b += p.part_bytes[q];
+  return b;
+}
+
+constexpr int kSkinnyRows = 16;  // up to here moe_linear streams the weights
+
+// How moe_linear runs: `rest` last rows stream the weights, the rows before them (if any) go through tiles.  A few
+// rows over a multiple of the tile would cost a whole row of tiles (4099 x 2048 x 2816: 66 us against 50 + 7).
+struct ForwardPlan {
+  int rest;
+  Plan tiles;
+};
+inline ForwardPlan forward_plan(int64_t M, int N, int K, int nmat, bool split, int cus) {
+  ForwardPlan f{};
+  if (M <= kSkinnyRows) {
+    f.rest = (int)M;
+    return f;
+  }
+  const Size all{M, N, stages(K)};
+  f.tiles = make_plan(&all, 1, nmat, split, cus);
+  const int rest = (int)(M % 64);
+  if (rest == 0 || rest > kSkinnyRows || M < 64) return f;
+  const Size most{M - rest, N, all.nk};
+  const Plan p = make_plan(&most, 1, nmat, split, cus);
+  // A launch, and the weights once more at the rate that they stream from the last-level cache.
+  if (p.time + 4.0 + (double)N * K * 2 * nmat / 4.0e6 < f.tiles.time) {
+    f.rest = rest;
+    f.tiles = p;
+  }
+  return f;
+}
 
 }  // namespace moe

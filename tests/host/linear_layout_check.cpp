@@ -64,4 +64,12 @@ int64_t backward_wrong(int64_t M, int64_t N, int64_t K, int mats) {
   return wrong;
 }
 
+// Tile kind, slices and streamed rows of moe_linear with a workspace on a device of 256 CUs.
+void forward_tiles(int64_t M, int N, int K, int dual, int* out) {
+  const moe::ForwardPlan f = moe::forward_plan(M, N, K, dual ? 2 : 1, true, 256);
+  out[0] = f.tiles.kind;
+  out[1] = f.tiles.S[0];
+  out[2] = f.rest;
+}
+
 }  // extern "C"
