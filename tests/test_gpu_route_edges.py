@@ -169,3 +169,24 @@ def test_groups_of_equal_or_tiny_logits_with_masks(T, E, G, tg, score):
     l[::3] = torch.where(l[::3] > -INF, torch.randint(-9, 10, l[::3].shape, generator=g) * 1.4e-45, l[::3])
     check_choice(l, 1, score=score, n_group=G, topk_group=tg, group_top=1)
     check_choice(l, min(5, tg * (E // G)), score=score, n_group=G, topk_group=tg, group_top=1)
+
+
+@pytest.mark.parametrize("T", [130, 2051])
+@pytest.mark.parametrize("E,G,tg,gt,k", [(256, 8, 4, 2, 8), (160, 8, 3, 1, 6), (64, 1, 1, 1, 6)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", ["bf16", "bf16, zero bias", "-1e9", "lowest", "barred by a bias of -1e9", "few values"])
+def test_inputs_that_leave_the_fp32_choice_in_doubt(T, E, G, tg, gt, k, score, kind):
+    """Equal logits and finite masks: most tokens are chosen in 64 bits, in both of the kernel's forms."""
+    g = gen(E + T)
+    l, b = torch.randn(T, E, generator=g) * 1.5, None
+    if kind.startswith("bf16"):
+        l = l.bfloat16().float()
+        b = torch.zeros(E) if "bias" in kind else None
+    elif kind == "few values":
+        l = l.round() / 2
+    elif kind.startswith("barred"):
+        b = torch.randn(E, generator=g) * 0.1
+        b[torch.randperm(E, generator=g)[:2]] = -1e9
+    else:
+        l = torch.where(torch.rand(T, E, generator=g) < 0.05, -1e9 if kind == "-1e9" else -FMAX, l)
+    check_choice(l, k, b, score=score, n_group=G, topk_group=tg, group_top=gt, renormalize=False)
