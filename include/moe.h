@@ -135,8 +135,9 @@ moe_status moe_route_topk(const float* logits, int64_t T, int32_t E, int32_t k,
  *                   row tile, ordered by (priority, expert, tile index) where
  *                   a tile's priority is the largest source rank among its rows.
  *   num_tiles       [1] int32: number of valid entries in tiles.
- * Inputs: x [T, H] bf16; topk_idx [T, k] int32 (from moe_route_topk, or any
- * ids in [0, E) with no repeat within a row); src_rank [T] int32 with values
+ * Inputs: x [T, H] bf16; topk_idx [T, k] int32 (from moe_route_topk or
+ * moe_route_grouped, or any ids with no repeat within a row; those outside the
+ * local range, -1 among them, are not local); src_rank [T] int32 with values
  * in [0, num_ranks), or NULL = every token is local (rank 0).
  * x and x_perm may both be NULL: then only the index outputs are written, for
  * moe_grouped_ffn_gather, which reads the token rows from x itself.
@@ -313,18 +314,20 @@ typedef enum {
  * token to the best groups of experts.
  *
  *   logits      [T, E] fp32, row-major.  An expert whose logit is -inf or NaN,
- *               or whose bias is -inf or NaN, is not available to that token;
+ *               or whose bias is -inf or NaN, is not available to that token:
+ *               it cannot be chosen and takes no part in the softmax's sum.
  *               +inf counts as the largest finite fp32.
  *   bias        [E] fp32 added to the scores for the choice only, or NULL.
  *   n_group     the E experts form n_group groups of E / n_group consecutive
  *               ids.  A group's score is the sum of the group_top (1 or 2)
  *               largest s_e + bias_e of its available experts; the topk_group
  *               best groups are kept (a group with no available expert ranks
- *               last), the others' experts are not available.
- *   topk_idx    [T, k] int32 out: the k best available experts in descending
- *               s_e + bias_e; slots left over (fewer than k available experts,
- *               a padding token whose logits are all -inf) hold -1, which
- *               moe_permute treats as not local.
+ *               last).  The others' experts cannot be chosen, but stay in the
+ *               softmax's sum.
+ *   topk_idx    [T, k] int32 out: the k best available experts of the kept
+ *               groups in descending s_e + bias_e; slots left over (fewer than
+ *               k such experts, a padding token whose logits are all -inf)
+ *               hold -1, which moe_permute treats as not local.
  *   topk_w      [T, k] fp32 out: scale * s_e, divided by the sum of the row's
  *               chosen s_e when renormalize != 0; 0 in the slots that hold -1.
  *               The division is carried out on scaled scores, so it stays

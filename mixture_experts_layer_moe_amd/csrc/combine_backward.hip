@@ -9,7 +9,8 @@
 // slot's row in flight while one is used, and adds the block's partial dot
 // products in a fixed order (no atomics).  4096 tokens of 4096 columns, two local slots each: 336 MB in 63 us (5.3
 // TB/s; a copy of 1 GiB reaches 5.1); 5003 tokens, 8 slots of which about one is local: 247 MB in 47 us (all slots'
-// rows at once, the absent ones masked, took 58).
+// rows at once, the absent ones masked, took 58).  Rows under 1024 columns leave threads without work: 16384 tokens of
+// 256 columns 84 MB in 31 us.
 #include "operators.h"
 
 namespace moe {

@@ -352,8 +352,9 @@ struct Tile {
 
   // The epilogue straight from the accumulators: a lane holds, for row r + 16 i, the 4 VW columns from n + 16 VW j on.
   // For products without an activation and SwiGLU, where rows are whole pieces: 12.5 us against the LDS epilogue's 17
-  // at 4096 x 4096 x 64, 62 against 84 at 4096 x 14336 x 64 (SwiGLU), 93 against 104 there with z and z_up saved (with
-  // single groups of four bf16 values 126, which is why the forward product pairs its fragments).
+  // at 4096 x 4096 x 64 (22 there with GELU, 19 with SiLU), 62 against 84 at 4096 x 14336 x 64 (SwiGLU), 93 against 104
+  // there with z and z_up saved (with single groups of four bf16 values 126, which is why the forward product pairs its
+  // fragments).
   template <int ES>
   static __device__ __forceinline__ void direct(const Sink& k, const Gemm& g, int r, int n, floatx4 (&acc)[NB][TM]) {
     asm volatile("" : "+v"(r), "+v"(n));                       // nothing of this ahead of the branch to it
@@ -807,7 +808,10 @@ __device__ __forceinline__ void store_values(uint16_t* o, const float (&v)[VEC])
 }
 
 // dz (SwiGLU: dz and dz_up, dz_up at column offset Np) rounded to bf16, [M, ld] with zeros in columns [N, Np) of
-// each, and the block's column sums of the unrounded values, part[block row][mats][N].  HBM-bound: reads d_out, z
+// each, and the block's column sums of the unrounded values, part[block row][mats][N].  bf16 because the matrix
+// instructions take it, like the products' other operands: the gradients' relative error against 64 bits is then
+// 2.3e-3, of which their own rounding is 1.7e-3 (two independent roundings of that size: sqrt 2 of it); dz in two bf16
+// parts would leave 1.7e-3 and double the products.  HBM-bound: reads d_out, z
 // (and z_up), writes dz once.  64 threads side by side of VEC columns (8 where rows are 16-byte aligned, N % 8 ==
 // 0), four rows apart; each thread has the loads of its two rows in flight and ends.  Blocks of 32 rows, two at a
 // time, took 10 us against 4 at 197 x 1000 and 43 against 33 at 8192 x 2816 (SwiGLU).

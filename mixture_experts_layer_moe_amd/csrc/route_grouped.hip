@@ -8,13 +8,21 @@
 // The choice has to be the one that exact arithmetic makes.  Both scores grow
 // strictly with the logit, so without a bias experts (and groups ranked by
 // their best expert) are compared by their logits, exactly.  Keys with a bias
-// and sums of two scores are 64-bit: two of them that differ by less than an
-// fp32 rounding are met every few thousand tokens.
+// and sums of two scores are 64-bit: with logits of full fp32 precision two of
+// them that differ by less than an fp32 rounding are met every few thousand
+// tokens.
 //
-// Bound by the chain of dependent steps in a token's choice (sort, groups, k
-// rounds), not by its bytes: 16384 x 256, 8 of 4 of 8 groups: 17 us, of which
-// 3-4 us are the few tokens that are chosen again in 64 bits; the logits alone
-// would take 3.5 us.  One token: 4.7 us, of which a launch is 2.3.
+// Bound by instruction issue once the tokens fill the chip: 16384 x 256, 8 of 4
+// of 8 groups, takes 16-17 us (the logits alone would take 3.5).  1300 VALU
+// instructions a wavefront, four wavefronts a SIMD: its VALU is busy for 97 % of
+// an average wavefront's life and 68 % of the launch, whose last 3-4 us are the
+// few tokens that are chosen again in 64 bits.  With a wavefront a SIMD or less
+// bound by the chain of dependent steps (sort, groups, k rounds): 4099 x 160 6-8
+// us (VALU 34 %), one token 4.7-5.5 (25 %), of which a launch is 2.3.
+// Where ties are common most tokens are chosen again: 16384 x 256 with bf16
+// logits 26 us without a bias and 34 with one of zeros, with two experts pushed
+// out by a bias of -1e9 37 (the doubt test's tolerance goes by the row's largest
+// key); 4099 x 160 with bf16 logits or masks of -1e4 and below 15-16.
 #include "operators.h"
 
 #include <float.h>
@@ -386,7 +394,7 @@ __device__ void choose_token(const RouteArgs& a, const Place& pl, int64_t t, int
 }
 
 // LT lanes per token, 64 / LT tokens per wavefront.  Tokens that fp32 keys leave in doubt are chosen again in 64 bits
-// (PX experts a lane): at 16384 x 256 a few in a thousand; 64-bit keys for all took 45 us there.
+// (PX experts a lane): at 16384 x 256 with normal fp32 logits a few in a thousand; 64-bit keys for all took 45 us there.
 template <int LT, int PL, int PX>
 __global__ __launch_bounds__(kTokens* kWave) void route_grouped_kernel(RouteArgs a, Place pl, int exact_bits) {
   __shared__ int s_id[kTokens][64 / LT][32];
