@@ -1,0 +1,449 @@
+"""Measured cases of the 4-bit (MXFP4) operators and of the layer for a few tokens.
+
+Calls of the MoE layer's library, as a user of the layer makes them:
+
+  quant    moe_mxfp4_quantize, moe_mxfp4_dequantize   weights or tokens to 4 bits with a scale per 32, and read back
+  linear   moe_linear_mxfp4           dense product of 4-bit operands with bias, activation and residual
+  grouped  moe_grouped_linear_mxfp4   the experts' products of 4-bit operands over permuted or gathered rows
+  few      moe_few_tokens             a whole MoE layer for up to 64 tokens, bf16 or 4-bit experts
+
+With `own` false, `run` computes the same in elementary torch operations in fp32.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    return [
+        # Tokens of a decode step, quantised ahead of a 4-bit product: the smallest call.
+        dict(name="quant_tokens", op="quant", R=64, K=7168, dtype="bf16"),
+        # One weight matrix of every expert of the fine-grained layer, at load time.
+        dict(name="quant_weights", op="quant", R=64 * 1408, K=2048, dtype="bf16"),
+        # fp32 rows of an odd number and an odd number of blocks.
+        dict(name="quant_ragged", op="quant", R=5003, K=1440, dtype="fp32"),
+        # Serving, one token: the shared expert's gate and up products at the decode layer's width.
+        dict(name="linear_token", op="linear", M=1, N=2048, K=7168, act="swiglu", bias=False, residual=False, out="bf16"),
+        # A prompt through a dense SwiGLU layer of the Mixtral shape.
+        dict(name="linear_swiglu", op="linear", M=4096, N=14336, K=4096, act="swiglu", bias=False, residual=False, out="bf16"),
+        # Odd numbers of rows and columns, half a stage over, everything the epilogue does.
+        dict(name="linear_ragged", op="linear", M=1003, N=1001, K=1408, act="gelu", bias=True, residual=True, out="fp32"),
+        # Gate and up products of the expert-parallel share, rows gathered from the tokens.
+        dict(name="grouped_up_gather", op="grouped", T=16384, k=8, E=64, E_loc=8, tile_m=256, N=2048, K=4096, act="swiglu",
+             gather=True, out="bf16"),
+        # Down product of the fine-grained layer: many experts, fp32 rows for the combine.
+        dict(name="grouped_down", op="grouped", T=8192, k=6, E=64, E_loc=64, tile_m=256, N=2048, K=1408, act="none",
+             gather=False, out="fp32"),
+        # Small batch, a few rows an expert: weight bytes count.
+        dict(name="grouped_small", op="grouped", T=64, k=6, E=64, E_loc=64, tile_m=16, N=1408, K=2048, act="swiglu",
+             gather=True, out="bf16"),
+        # One token through the fine-grained layer.
+        dict(name="few_token", op="few", T=1, H=2048, F=1408, E=64, E_loc=64, k=6, act="swiglu", weights="bf16", logits=True),
+        # A ragged handful of tokens on an expert-parallel share, routed beforehand.
+        dict(name="few_share", op="few", T=13, H=4096, F=2048, E=64, E_loc=8, k=8, act="swiglu", weights="bf16", logits=False),
+        # The decode-sized layer with 4-bit experts: nearly every expert is hit.
+        dict(name="few_decode", op="few", T=64, H=7168, F=2048, E=256, E_loc=256, k=8, act="swiglu", weights="mxfp4", logits=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["quant", "linear", "linear", "grouped", "grouped", "few", "few", "few"])
+    if op == "quant":
+        while True:
+            R, K = _log(rng, 1, 100000), 32 * _log(rng, 1, 448)
+            if R * K <= 1.8e8:
+                return dict(op=op, R=R, K=K, dtype=rng.choice(["bf16", "fp32"]))
+    act = rng.choice(["none", "gelu", "silu", "swiglu", "swiglu"])
+    if op == "linear":
+        while True:
+            M, N, K = _log(rng, 1, 8192), _log(rng, 1, 14336), 128 * _log(rng, 1, 112)
+            if 2.0 * M * N * K <= 4.0e11:
+                break
+        if rng.random() < 0.5 and N > 64:
+            N = N // 64 * 64
+        return dict(op=op, M=M, N=N, K=K, act=act, bias=rng.random() < 0.4, residual=rng.random() < 0.4,
+                    out=rng.choice(["bf16", "fp32"]))
+    if op == "grouped":
+        while True:
+            E, k = rng.choice([(8, 2), (64, 6), (64, 8), (32, 4), (16, 1), (48, 5)])
+            E_loc = rng.choice([E, E // 2, E // 8])
+            T, tile_m = _log(rng, 1, 16384), rng.choice([16, 32, 64, 128, 256])
+            N, K = _log(rng, 8, 8192), 128 * _log(rng, 1, 64)
+            if rng.random() < 0.7 and N > 128:
+                N = N // 128 * 128
+            rows = T * k * E_loc / E
+            if E_loc < E and rows < 12:  # (a share that most draws of so few tokens would leave without a row)
+                continue
+            if 2.0 * rows * N * K <= 2.0e11 and E_loc * N * K <= 4e8 and T * k <= 1000 * tile_m:
+                break
+        return dict(op=op, T=T, k=k, E=E, E_loc=E_loc, tile_m=tile_m, N=N, K=K, act=act, gather=rng.random() < 0.5,
+                    out=rng.choice(["bf16", "fp32"]))
+    while True:
+        E = rng.choice([1, 4, 8, 16, 60, 64, 128, 256])
+        E_loc = max(1, rng.choice([E, E, E // 2, E // 8]))
+        T, k = _log(rng, 1, 64), rng.randint(1, min(E, 10))
+        H, F = 128 * _log(rng, 1, 56), 128 * _log(rng, 1, 112)
+        if E_loc * H * F <= 1.0e9 and (E_loc == E or T * k * E_loc / E >= 12):
+            break
+    return dict(op=op, T=T, H=H, F=F, E=E, E_loc=E_loc, k=k,
+                act=rng.choice(["swiglu", "swiglu", "gelu"]), weights=rng.choice(["bf16", "mxfp4"]), logits=rng.random() < 0.6)
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 in elementary operations: blocks of 32 along the last axis, scale 2^(byte - 127), codes e2m1
+# ---------------------------------------------------------------------------
+
+def _quantize(x):
+    """Codes (one a byte, not packed) and scale bytes of finite x: nearest, ties to even, saturated at 6."""
+    b = x.float().unflatten(-1, (-1, 32))
+    top = b.abs().amax(dim=-1, keepdim=True)
+    s = ((top.view(torch.int32) >> 23) - 2).clamp(min=0)                       # biased floor(log2) - 2
+    y = (b.abs() * ((254 - s) << 23).view(F32))
+    code = ((y > 0.25).to(torch.uint8) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0))
+    code = code + torch.signbit(b).to(torch.uint8) * 8
+    return code.flatten(-2), s.squeeze(-1).to(torch.uint8)
+
+
+def _values(code, s):
+    """fp32 values of unpacked codes and scale bytes."""
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], device=code.device)
+    scale = torch.where(s == 0, 2.0 ** -127, (s.to(torch.int32) << 23).view(F32))
+    return (lut[code.to(torch.int32)].unflatten(-1, (-1, 32)) * scale.unsqueeze(-1)).flatten(-2)
+
+
+def _dequantize(q):
+    """fp32 values of packed codes: the even element in the low four bits."""
+    c, s = q
+    return _values(torch.stack((c & 15, c >> 4), dim=-1).flatten(-2), s)
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _rand(g, shape, std=1.0, dtype=BF):
+    return (torch.randn(*shape, device=DEV, generator=g) * std).to(dtype)
+
+
+def _packed(g, shape, std=1.0):
+    """A normal matrix (or one for each expert) in MXFP4, rounded from bf16."""
+    codes = torch.empty(*shape[:-1], shape[-1] // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(*shape[:-1], shape[-1] // 32, dtype=torch.uint8, device=DEV)
+    flat_c, flat_s = codes.view(-1, shape[-1] // 2), scales.view(-1, shape[-1] // 32)
+    step = max(1, (1 << 27) // shape[-1])
+    for r in range(0, flat_c.shape[0], step):
+        c, s = _quantize(_rand(g, (min(step, flat_c.shape[0] - r), shape[-1]), std))
+        flat_c[r:r + step] = c[:, 0::2] | (c[:, 1::2] << 4)
+        flat_s[r:r + step] = s
+    return codes, scales
+
+
+def _weights(g, kind, shape):
+    if kind == "mxfp4":
+        return _packed(g, shape, 0.02)
+    w = torch.empty(*shape, dtype=BF, device=DEV)
+    for e in range(shape[0]):
+        w[e] = _rand(g, shape[1:], 0.02)
+    return w
+
+
+def _inputs(c, seed):
+    g = _gen(seed)
+    if c["op"] == "quant":
+        # rows of different magnitudes, as tokens' are
+        x = torch.randn(c["R"], c["K"], device=DEV, generator=g) * torch.exp(torch.randn(c["R"], 1, device=DEV, generator=g))
+        return dict(x=x.to(BF if c["dtype"] == "bf16" else F32))
+    if c["op"] == "linear":
+        M, N, K, dual = c["M"], c["N"], c["K"], c["act"] == "swiglu"
+        odt = BF if c["out"] == "bf16" else F32
+        return dict(x=_packed(g, (M, K)), w=_packed(g, (N, K), 0.02), w_up=_packed(g, (N, K), 0.02) if dual else None,
+                    bias=_rand(g, (N,), 0.1, F32) if c["bias"] else None,
+                    bias_up=_rand(g, (N,), 0.1, F32) if c["bias"] and dual else None,
+                    residual=_rand(g, (M, N), 1.0, odt) if c["residual"] else None)
+    if c["op"] == "grouped":
+        T, k, E, El, tm, N, K = (c[n] for n in ("T", "k", "E", "E_loc", "tile_m", "N", "K"))
+        e = torch.rand(T, E, device=DEV, generator=g).topk(k, dim=1).indices.reshape(-1)  # distinct experts of a token
+        order = torch.argsort(e * (T * k) + torch.arange(T * k, device=DEV))              # by expert, then token
+        counts = torch.bincount(e, minlength=E)
+        first = torch.cumsum(counts, 0) - counts
+        pad = (counts[:El] + tm - 1) // tm * tm
+        ends = torch.cumsum(pad, 0)
+        off = torch.cat((torch.zeros(1, dtype=ends.dtype, device=DEV), ends))
+        R_cap = T * min(k, El) + El * (tm - 1)
+        tcap = T * min(k, El) // tm + El
+        es = e[order]
+        mine = es < El
+        row = (off[es.clamp(max=El)] + torch.arange(T * k, device=DEV) - first[es])[mine]
+        row_src = torch.full((R_cap,), -1, dtype=torch.int32, device=DEV)
+        row_src[row] = order[mine].to(torch.int32)
+        inv = torch.full((T * k,), -1, dtype=torch.int32, device=DEV)
+        inv[order[mine]] = row.to(torch.int32)
+        nt = pad // tm
+        n_tiles = int(nt.sum())
+        te = torch.repeat_interleave(torch.arange(El, device=DEV), nt)
+        tiles = torch.zeros(tcap, 2, dtype=torch.int32, device=DEV)
+        tiles[:n_tiles, 0] = te.to(torch.int32)
+        tiles[:n_tiles, 1] = (torch.arange(n_tiles, device=DEV) * tm).to(torch.int32)
+        dual = c["act"] == "swiglu"
+        return dict(x=_packed(g, (T if c["gather"] else R_cap, K)), w=_packed(g, (El, N, K), 0.02),
+                    w_up=_packed(g, (El, N, K), 0.02) if dual else None, counts=counts[:El].to(torch.int32).contiguous(),
+                    offsets=off.to(torch.int32), row_src=row_src, inv=inv.view(T, k), tiles=tiles,
+                    num_tiles=torch.tensor([n_tiles], dtype=torch.int32, device=DEV), R_cap=R_cap, tcap=tcap,
+                    most=int(counts[:El].max()))  # rows of the fullest expert: what a batched product is padded to
+    T, H, F, E, El, k = (c[n] for n in ("T", "H", "F", "E", "E_loc", "k"))
+    d = dict(x=_rand(g, (T, H)), logits=torch.randn(T, E, device=DEV, generator=g))
+    if not c["logits"]:  # routed beforehand: a padding token now and then, scaled sigmoid weights
+        v, i = torch.topk(d["logits"], k, dim=1)
+        none = torch.rand(T, 1, device=DEV, generator=g) < 0.1
+        none[0] = False
+        d["idx"] = torch.where(none, -1, i).to(torch.int32).contiguous()
+        w = torch.sigmoid(v)
+        d["gate"] = torch.where(none, 0.0, 2.5 * w / w.sum(dim=1, keepdim=True)).contiguous()
+        d["logits"] = None
+    d["w0"] = _weights(g, c["weights"], (El, F, H))
+    d["w0_up"] = _weights(g, c["weights"], (El, F, H)) if c["act"] == "swiglu" else None
+    d["w1"] = _weights(g, c["weights"], (El, H, F))
+    return d
+
+
+def prepare(case, seed):
+    d = _inputs(case, seed)
+    c = d["case"] = case
+    # What a serving program keeps from call to call: output buffers (the operator's workspace joins them at the first call).
+    if c["op"] == "quant":
+        d["codes"] = torch.empty(c["R"], c["K"] // 2, dtype=torch.uint8, device=DEV)
+        d["scales"] = torch.empty(c["R"], c["K"] // 32, dtype=torch.uint8, device=DEV)
+        d["out"] = torch.empty_like(d["x"])
+    elif c["op"] == "linear":
+        d["out"] = torch.empty(c["M"], c["N"], dtype=BF if c["out"] == "bf16" else F32, device=DEV)
+    elif c["op"] == "grouped":  # rows behind an expert's last token are never written
+        d["out"] = torch.zeros(d["R_cap"], c["N"], dtype=BF if c["out"] == "bf16" else F32, device=DEV)
+    else:
+        d["out"] = torch.empty(c["T"], c["H"], device=DEV)
+        if c["logits"]:
+            d["idx"] = torch.empty(c["T"], c["k"], dtype=torch.int32, device=DEV)
+            d["gate"] = torch.empty(c["T"], c["k"], device=DEV)
+    return d
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+
+def _mx(ffi, s, name):
+    return None if s[name] is None else ffi.Mxfp4(*s[name])
+
+
+def run(state):
+    s, c = state, state["case"]
+    if own:
+        from mixture_experts_layer_moe_amd import ffi
+        if c["op"] == "quant":
+            q = ffi.moe_mxfp4_quantize(s["x"], out=ffi.Mxfp4(s["codes"], s["scales"]))
+            return ffi.moe_mxfp4_dequantize(q, out=s["out"])
+        if c["op"] == "linear":
+            if "ws" not in s:
+                s["ws"] = ffi.alloc_linear_mxfp4_workspace(c["M"], c["N"], c["K"], c["act"], DEV)
+            return ffi.moe_linear_mxfp4(_mx(ffi, s, "x"), _mx(ffi, s, "w"), w_up=_mx(ffi, s, "w_up"), bias=s["bias"],
+                                        bias_up=s["bias_up"], act=c["act"], residual=s["residual"], out=s["out"],
+                                        ws=s["ws"], use_workspace=False)
+        if c["op"] == "grouped":
+            p = ffi.Permuted(None, s["counts"], s["offsets"], s["row_src"], s["inv"], s["tiles"], s["num_tiles"],
+                             c["tile_m"], s["R_cap"], s["tcap"])
+            return ffi.moe_grouped_linear_mxfp4(p, _mx(ffi, s, "x"), _mx(ffi, s, "w"), w_up=_mx(ffi, s, "w_up"),
+                                                act=c["act"], gather=c["gather"], out=s["out"])
+        if "ws" not in s:
+            s["ws"] = ffi.alloc_few_tokens_workspace(c["T"], c["k"], c["F"], DEV)
+        mx = c["weights"] == "mxfp4"
+        w0, w0_up, w1 = (_mx(ffi, s, n) if mx else s[n] for n in ("w0", "w0_up", "w1"))
+        ffi.moe_few_tokens(s["x"], w0, w0_up, w1, c["act"], logits=s["logits"], topk_idx=s["idx"], topk_w=s["gate"],
+                           out=s["out"], ws=s["ws"])
+        return (s["out"], s["idx"], s["gate"]) if c["logits"] else s["out"]
+    return {"quant": _quant, "linear": _linear, "grouped": _grouped, "few": _few}[c["op"]](s, c)
+
+
+def _quant(s, c):
+    return _values(*_quantize(s["x"])).to(s["x"].dtype)
+
+
+def _activate(act, z, u):
+    if act == "swiglu":
+        return z * torch.sigmoid(z) * u
+    if act == "silu":
+        return z * torch.sigmoid(z)
+    if act == "gelu":
+        return 0.5 * z * (1.0 + torch.erf(z * math.sqrt(0.5)))
+    return z
+
+
+def _linear(s, c):
+    x = _dequantize(s["x"])
+    z = x @ _dequantize(s["w"]).T
+    if s["bias"] is not None:
+        z = z + s["bias"]
+    u = None
+    if c["act"] == "swiglu":
+        u = x @ _dequantize(s["w_up"]).T
+        if s["bias_up"] is not None:
+            u = u + s["bias_up"]
+    y = _activate(c["act"], z, u)
+    if s["residual"] is not None:
+        y = y + s["residual"].float()
+    return y.to(s["out"].dtype)
+
+
+def _grouped(s, c):
+    # Each expert's rows, padded to the fullest expert's number, in one batched product.
+    at = s["offsets"][:-1, None].long() + torch.arange(s["most"], device=DEV)
+    real = torch.arange(s["most"], device=DEV) < s["counts"][:, None]
+    at = torch.where(real, at, s["R_cap"])                                     # (a row past the last, dropped below)
+    src = at.clamp(max=s["R_cap"] - 1)
+    if c["gather"]:
+        src = s["row_src"][src].long().clamp(min=0) // c["k"]
+    x = _dequantize(s["x"])[src]
+    z = torch.bmm(x, _dequantize(s["w"]).transpose(1, 2))
+    u = torch.bmm(x, _dequantize(s["w_up"]).transpose(1, 2)) if c["act"] == "swiglu" else None
+    out = torch.zeros(s["R_cap"] + 1, c["N"], dtype=s["out"].dtype, device=DEV)
+    out[at.view(-1)] = _activate(c["act"], z, u).flatten(0, 1).to(out.dtype)
+    return out[:-1]
+
+
+def _few(s, c):
+    T, k, El = c["T"], c["k"], c["E_loc"]
+    if c["logits"]:
+        l, i = torch.sort(s["logits"], dim=1, descending=True, stable=True)
+        gate = torch.exp(l[:, :k] - l[:, :1])
+        gate, idx = gate / gate.sum(dim=1, keepdim=True), i[:, :k].contiguous()
+    else:
+        gate, idx = s["gate"], s["idx"].long()
+    local = (idx >= 0) & (idx < El)
+    g = torch.where(local, gate, 0.0)
+    mx = c["weights"] == "mxfp4"
+    x = s["x"].float()
+    if T * k <= El:  # the chosen experts' weights, slot by slot
+        e = torch.where(local, idx, 0).view(-1)
+        w = lambda n: _dequantize((s[n][0][e], s[n][1][e])) if mx else s[n][e].float()  # noqa: E731
+        xs = x.repeat_interleave(k, dim=0).unsqueeze(2)
+        z = torch.bmm(w("w0"), xs)
+        u = torch.bmm(w("w0_up"), xs) if c["act"] == "swiglu" else None
+        y = torch.bmm(w("w1"), _activate(c["act"], z, u)).view(T, k, c["H"])
+        out = (y * g.unsqueeze(2)).sum(dim=1)
+    else:            # every token through every local expert, with the gate weights of those it did not choose zero
+        w = lambda n: _dequantize(s[n]) if mx else s[n].float()  # noqa: E731
+        dense = torch.zeros(T, El + 1, device=DEV).scatter_add_(1, torch.where(local, idx, El), g)[:, :El]
+        z = (x @ w("w0").flatten(0, 1).T).view(T, El, -1)
+        u = (x @ w("w0_up").flatten(0, 1).T).view(T, El, -1) if c["act"] == "swiglu" else None
+        a = _activate(c["act"], z, u) * dense.unsqueeze(2)
+        out = torch.bmm(a.transpose(0, 1), w("w1").transpose(1, 2)).sum(dim=0)
+    return (out, idx.to(torch.int32), gate) if c["logits"] else out
+
+
+# ---------------------------------------------------------------------------
+# What a pass cannot do without, and the definition in 64 bits
+# ---------------------------------------------------------------------------
+
+def work(case):
+    c = case
+    fp4 = 0.5 + 1.0 / 32
+    if c["op"] == "quant":
+        n = c["R"] * c["K"]
+        return {"bytes": n * (2 * (2 if c["dtype"] == "bf16" else 4) + 2 * fp4), "flops": 8 * n}
+    mats = 2 if c["act"] == "swiglu" else 1
+    if c["op"] == "linear":
+        M, N, K, ob = c["M"], c["N"], c["K"], 2 if c["out"] == "bf16" else 4
+        b = (M + mats * N) * K * fp4 + M * N * ob * (2 if c["residual"] else 1) + (4 * N * mats if c["bias"] else 0)
+        return {"bytes": b, "flops": 2 * M * N * K * mats}
+    hit = c["E_loc"] * (1.0 - (1.0 - c["k"] / c["E"]) ** c["T"])  # local experts that some token chooses, on average
+    rows = c["T"] * c["k"] * c["E_loc"] / c["E"]
+    if c["op"] == "grouped":
+        N, K, ob = c["N"], c["K"], 2 if c["out"] == "bf16" else 4
+        read = min(c["T"], rows) if c["gather"] else rows
+        return {"bytes": (read + mats * hit * N) * K * fp4 + rows * N * ob + 4 * rows, "flops": 2 * rows * N * K * mats}
+    wb = fp4 if c["weights"] == "mxfp4" else 2
+    b = (mats + 1) * hit * c["H"] * c["F"] * wb + c["T"] * (6 * c["H"] + 8 * c["k"] + (4 * c["E"] if c["logits"] else 0))
+    return {"bytes": b, "flops": 2 * rows * c["H"] * c["F"] * (mats + 1)}
+
+
+def _wide(q):
+    """Values of packed codes in 64 bits, from the format's definition: sign, two bits of exponent, one of mantissa."""
+    c, s = q
+    n = torch.stack((c % 16, c // 16), dim=-1).flatten(-2).to(torch.float64)
+    sign, mag = 1.0 - 2.0 * (n >= 8), n % 8
+    e, m = torch.div(mag, 2, rounding_mode="floor"), mag % 2
+    v = sign * torch.where(e > 0, (1.0 + 0.5 * m) * torch.pow(2.0, e - 1.0), 0.5 * m)
+    return v * torch.pow(2.0, s.to(torch.float64) - 127.0).repeat_interleave(32, dim=-1)
+
+
+def _act64(act, z, u):
+    if act == "swiglu":
+        return torch.nn.functional.silu(z) * u
+    return {"none": lambda t: t, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu}[act](z)
+
+
+def exact(case, seed):
+    c = case
+    if c["op"] == "quant" and c["R"] * c["K"] > 1e8:
+        return None
+    d = _inputs(c, seed)
+    f = torch.float64
+    if c["op"] == "quant":
+        x = d["x"].to(f).view(c["R"], -1, 32)
+        top = x.abs().amax(dim=2, keepdim=True)
+        s = torch.clamp(torch.frexp(top).exponent - 3, min=-127)  # top = m 2^e with m in [1/2, 1)
+        s = torch.where(top > 0, s, -127)
+        y = torch.ldexp(x, -s)
+        # spacing of the grid at |y|: 1/2 below 2, 1 below 4, 2 above; round() takes ties to even multiples
+        step = torch.where(y.abs() < 2, 0.5, torch.where(y.abs() < 4, 1.0, 2.0)).to(f)
+        y = (torch.round(y / step) * step).clamp(-6.0, 6.0)
+        return torch.ldexp(y, s).view(c["R"], c["K"])
+    if c["op"] == "linear":
+        x = _wide(d["x"])
+        z = torch.nn.functional.linear(x, _wide(d["w"]), None if d["bias"] is None else d["bias"].to(f))
+        u = None
+        if c["act"] == "swiglu":
+            u = torch.nn.functional.linear(x, _wide(d["w_up"]), None if d["bias_up"] is None else d["bias_up"].to(f))
+        y = _act64(c["act"], z, u)
+        return y if d["residual"] is None else y + d["residual"].to(f)
+    if c["op"] == "grouped":
+        out = torch.zeros(d["R_cap"], c["N"], dtype=f, device=DEV)
+        off, cnt = d["offsets"].tolist(), d["counts"].tolist()
+        for e in range(c["E_loc"]):
+            if cnt[e]:
+                r = torch.arange(off[e], off[e] + cnt[e], device=DEV)
+                q = torch.div(d["row_src"][r].long(), c["k"], rounding_mode="floor") if c["gather"] else r
+                x = _wide((d["x"][0][q], d["x"][1][q]))
+                z = x @ _wide((d["w"][0][e], d["w"][1][e])).T
+                u = x @ _wide((d["w_up"][0][e], d["w_up"][1][e])).T if c["act"] == "swiglu" else None
+                out[r] = _act64(c["act"], z, u)
+        return out
+    if c["logits"]:
+        v, idx = d["logits"].to(f).topk(c["k"], dim=1)  # (normal logits: no ties that reach the choice)
+        gate = torch.softmax(v, dim=1)
+    else:
+        gate, idx = d["gate"].to(f), d["idx"].long()
+    out = torch.zeros(c["T"], c["H"], dtype=f, device=DEV)
+    one = lambda n, e: _wide((d[n][0][e], d[n][1][e])) if c["weights"] == "mxfp4" else d[n][e].to(f)  # noqa: E731
+    for e in sorted(set(idx.view(-1).tolist()) & set(range(c["E_loc"]))):
+        t, j = torch.nonzero(idx == e, as_tuple=True)
+        x = d["x"][t].to(f)
+        z = x @ one("w0", e).T
+        u = x @ one("w0_up", e).T if c["act"] == "swiglu" else None
+        out[t] += gate[t, j][:, None] * (_act64(c["act"], z, u) @ one("w1", e).T)
+    return (out, None, gate) if c["logits"] else out
