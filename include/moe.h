@@ -30,6 +30,14 @@
  *   moe_route_grouped_backward, moe_route_grouped_bias_backward,
  *   moe_combine_backward, moe_linear_backward
  *                               gradients of the two and of moe_combine
+ *   moe_mxfp4_quantize, moe_mxfp4_dequantize
+ *                               weights or tokens to 4 bits with a scale per
+ *                               32 values, and back
+ *   moe_linear_mxfp4, moe_grouped_linear_mxfp4
+ *                               moe_linear, and the experts' products, of two
+ *                               such operands
+ *   moe_few_tokens              the whole layer for at most 64 tokens in two
+ *                               launches, over bf16 or 4-bit experts
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer unless stated otherwise, and
@@ -472,6 +480,140 @@ moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, 
                                const void* z_up, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype,
                                void* d_x, void* d_w, void* d_w_up, float* d_bias, float* d_bias_up, void* ws,
                                size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* 4-bit operands (MXFP4)                                                     */
+/* ------------------------------------------------------------------------- */
+
+/*
+ * The OCP microscaling format MXFP4, for matrices [R, K] whose rows are whole
+ * blocks of 32 values:
+ *   codes   [R, K / 2] bytes: e2m1 values (sign bit; 0, 0.5, 1, 1.5, 2, 3, 4,
+ *           6), element 2 i of a row in the low half of byte i, 2 i + 1 in the
+ *           high half
+ *   scales  [R, K / 32] bytes: a block's values are 2^(s - 127) times its
+ *           codes'; s = 255: the whole block is NaN
+ */
+
+/*
+ * moe_mxfp4_quantize -- codes and scales of x [R, K] of x_dtype (moe_dtype).
+ *
+ * s - 127 = max(floor(log2 of the block's largest magnitude) - 2, -127), and a
+ * code is x / 2^(s - 127) rounded to the nearest value, ties to the even code,
+ * magnitudes above 6 to 6 (those of a block lie below 8).  A block with an
+ * infinity or NaN gets s = 255; a block of zeros s = 0.  Signs of zeros are
+ * kept.  Outputs must not overlap x or one another (checked).
+ * Requires K % 32 == 0, R * K <= 2^36.  R == 0: nothing to do.
+ */
+moe_status moe_mxfp4_quantize(const void* x, int64_t R, int32_t K, int32_t x_dtype, void* codes, void* scales,
+                              void* stream);
+
+/*
+ * moe_mxfp4_dequantize -- the values of codes and scales as out [R, K] of
+ * out_dtype: exact, but where 2^(s - 127) times a code passes the type's
+ * largest value (s > 252): infinity.  out must not overlap the inputs
+ * (checked).  Requires K % 32 == 0, R * K <= 2^36.  R == 0: nothing to do.
+ */
+moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R, int32_t K, int32_t out_dtype, void* out,
+                                void* stream);
+
+/* Bytes of the optional device workspace of moe_linear_mxfp4 on the current
+ * device (0 when this size needs none; 0 on invalid arguments). */
+size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
+
+/*
+ * moe_linear_mxfp4 -- moe_linear of two MXFP4 operands, on the scaled matrix
+ * instructions:
+ *
+ *   z   = x . w^T + bias          z_up = x . w_up^T + bias_up   (SwiGLU only)
+ *   out = act(z) + residual       SwiGLU: out = silu(z) * z_up + residual
+ *
+ *   x_codes, x_scales              x [M, K]
+ *   w_codes, w_scales              w [N, K] (output-major);  w_up_*: w_up [N, K], only for SwiGLU
+ *   bias, bias_up  [N] fp32, or NULL;  residual [M, N] of out's type, or NULL; may be out itself
+ *   out       [M, N] out_dtype (moe_dtype)
+ * Products of codes and scales are exact; accumulation, bias, activation and
+ * residual are fp32; each output is rounded once.  Results are deterministic.
+ * out and ws must not overlap the inputs or one another (checked; residual ==
+ * out excepted).
+ * ws / ws_bytes: optional device scratch (NULL / 0 is allowed) of at least
+ * moe_linear_mxfp4_workspace_bytes(), which small products split their
+ * reduction into; a non-NULL ws that is too small returns MOE_ERR_WORKSPACE.
+ * Requires K % 128 == 0; N, K <= 1048576; M <= 2^31 - 1, and at most 4 million
+ * tiles of 128 rows and 128 columns (SwiGLU: 64; up to 64 rows: 16 columns);
+ * more may return MOE_ERR_UNSUPPORTED.  M == 0: nothing to do.
+ */
+moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                            const void* w_up_codes, const void* w_up_scales, const float* bias, const float* bias_up,
+                            const void* residual, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype, void* out,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_grouped_linear_mxfp4 -- one product of every local expert with its rows,
+ * both in MXFP4: the two GEMMs of moe_grouped_ffn are two such calls, with the
+ * activations quantised between them.
+ *
+ *   out[p, :] = act( x[p, :] . w[e]^T )    SwiGLU: silu(x . w[e]^T) * (x . w_up[e]^T)
+ * for every real row p of every local expert e.
+ *   x_codes, x_scales   row_src NULL: x [R_cap, K], the permuted rows.  Else the tokens' x [T, K]: row p is token
+ *                       row_src[p] / k (a row whose row_src is negative or beyond T * k reads as zeros).
+ *   w_codes, w_scales   w [E_loc, N, K];  w_up_*: w_up [E_loc, N, K], only for SwiGLU
+ *   out                 [R_cap, N] out_dtype; only real rows are written
+ * expert_counts, expert_offsets, row_src, tiles and num_tiles are moe_permute's
+ * outputs for the same tile_m, R_cap and tiles_cap the capacities they were
+ * allocated with; T and k are not looked at where row_src is NULL.  act: any of
+ * moe_linear's.  Arithmetic as in moe_linear_mxfp4.  out must not overlap an
+ * input (checked).
+ * Requires K % 128 == 0; N, K <= 1048576; tile_m in {16, 32, 64, 128, 256};
+ * k <= 32 and T * K / 2 <= 2^31 - 1 where rows are gathered; at most 4 million
+ * tiles of tile_m (at most 128) rows and 64 columns (tile_m <= 64: 16); more
+ * may return MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_grouped_linear_mxfp4(const void* x_codes, const void* x_scales, const int32_t* row_src, int64_t T, int32_t k,
+                                    const int32_t* expert_counts, const int32_t* expert_offsets, const int32_t* tiles,
+                                    const int32_t* num_tiles, const void* w_codes, const void* w_scales,
+                                    const void* w_up_codes, const void* w_up_scales, int32_t E_loc, int32_t N, int32_t K,
+                                    int32_t act, int32_t tile_m, int64_t R_cap, int64_t tiles_cap, int32_t out_dtype,
+                                    void* out, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* The layer for a few tokens                                                 */
+/* ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace moe_few_tokens needs (0 on invalid arguments or no token). */
+size_t moe_few_tokens_workspace_bytes(int64_t T, int32_t k, int32_t F);
+
+/*
+ * moe_few_tokens -- routing, experts and combine of at most 64 tokens in two
+ * launches, each chosen expert's weights read once:
+ *
+ *   a[t, e] = act(x[t] . W0[e]^T (, x[t] . W0up[e]^T))           moe_grouped_ffn's activations
+ *   out[t, :] = sum over the token's chosen local experts e of g[t, e] * (a[t, e] . W1[e]^T)
+ * with g[t, e] the sum of topk_w over the token's slots that name e; a token
+ * without a local expert gets a zero row.
+ *
+ *   x         [T, H] bf16
+ *   logits    [T, E] fp32: the tokens are routed as moe_route_topk does it, and topk_idx, topk_w [T, k] are outputs.
+ *             A -inf or NaN logit bars its expert (not chosen, no part in the softmax's sum), +inf counts as the
+ *             largest finite fp32, and slots left over hold -1 with weight 0.
+ *             NULL: topk_idx and topk_w are inputs (moe_route_grouped's, or any; ids outside the local range,
+ *             -1 among them, are not local), and renormalize is not looked at.
+ *   w0, w0_up, w1   moe_grouped_ffn's weights [E_loc, F, H], [E_loc, F, H] (SwiGLU only), [E_loc, H, F] in bf16, with
+ *             the three *_scales NULL; or MXFP4 codes [.., / 2] with their scales [.., / 32]
+ *   out       [T, H] fp32 out
+ * Weights enter the products exactly, accumulation is fp32, and activations
+ * keep 16 bits of mantissa between the two products.  Results are
+ * deterministic.  Outputs and ws must not overlap the inputs or one another
+ * (checked).
+ * ws / ws_bytes: device scratch of at least moe_few_tokens_workspace_bytes();
+ * nothing in it has to start at zero or is kept for the next call.
+ * Requires T <= 64, E <= 1024, k <= 32, H % 128 == 0, F % 128 == 0,
+ * H, F <= 1048576, act MOE_ACT_GELU or MOE_ACT_SWIGLU.  T == 0: nothing to do.
+ */
+moe_status moe_few_tokens(const void* x, const float* logits, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                          int32_t expert_begin, int32_t E_loc, const void* w0, const void* w0_scales, const void* w0_up,
+                          const void* w0_up_scales, const void* w1, const void* w1_scales, int32_t H, int32_t F, int32_t act,
+                          int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["moe_api.hip", "route_topk.hip", "permute.hip", "grouped_gemm.hip", "combine.hip",
-           "route_grouped.hip", "combine_backward.hip", "linear.hip"]
+           "route_grouped.hip", "combine_backward.hip", "linear.hip", "mxfp4.hip", "linear_mxfp4.hip", "few_tokens.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

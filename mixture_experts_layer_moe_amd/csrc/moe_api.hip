@@ -488,3 +488,176 @@ moe_status moe_linear_backward(const void* d_out, const void* x, const void* w, 
 }
 
 }  // extern "C"
+
+namespace {
+
+// Sizes of the products of MXFP4 operands, but for the rows.
+moe_status mxfp4_sizes(int32_t N, int32_t K, int32_t act) {
+  if (N < 1 || K < 1 || !act_ok(act)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0 || N > (1 << 20) || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status mxfp4_blocks(int64_t R, int32_t K, int32_t dtype) {
+  if (R < 0 || K < 1 || (dtype != MOE_BF16 && dtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (K % 32 != 0 || R > ((int64_t)1 << 36) / K) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_mxfp4_quantize(const void* x, int64_t R, int32_t K, int32_t x_dtype, void* codes, void* scales,
+                              void* stream) {
+  const moe_status st = mxfp4_blocks(R, K, x_dtype);
+  if (st != MOE_OK || R == 0) return st;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)R * K;
+  const Span outs[] = {{codes, n / 2}, {scales, n / 32}}, ins[] = {{x, n * (x_dtype == MOE_F32 ? 4 : 2)}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
+  return launched(moe::launch_mxfp4_quantize(x, x_dtype == MOE_F32, R * (K / 32), static_cast<uint8_t*>(codes),
+                                             static_cast<uint8_t*>(scales), static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R, int32_t K, int32_t out_dtype, void* out,
+                                void* stream) {
+  const moe_status st = mxfp4_blocks(R, K, out_dtype);
+  if (st != MOE_OK || R == 0) return st;
+  if (!out || !codes || !scales || !aligned16(out) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)R * K;
+  const Span outs[] = {{out, n * (out_dtype == MOE_F32 ? 4 : 2)}}, ins[] = {{codes, n / 2}, {scales, n / 32}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
+  return launched(moe::launch_mxfp4_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                               R * (K / 32), out_dtype == MOE_F32, out, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act) {
+  if (M < 0 || M > INT32_MAX || mxfp4_sizes(N, K, act) != MOE_OK) return 0;
+  return moe::linear_mxfp4_ws_bytes(M, N, K, act);
+}
+
+moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                            const void* w_up_codes, const void* w_up_scales, const float* bias, const float* bias_up,
+                            const void* residual, int64_t M, int32_t N, int32_t K, int32_t act, int32_t out_dtype, void* out,
+                            void* ws, size_t ws_bytes, void* stream) {
+  if (M < 0 || (out_dtype != MOE_BF16 && out_dtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = mxfp4_sizes(N, K, act);
+  if (st != MOE_OK) return st;
+  if (M > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const bool dual = act == MOE_ACT_SWIGLU;
+  if (!dual && (w_up_codes || w_up_scales || bias_up)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !out || (dual && (!w_up_codes || !w_up_scales)))
+    return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x_codes, x_scales, w_codes, w_scales, w_up_codes, w_up_scales, bias, bias_up, residual, out, ws};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (ws && ws_bytes < moe::linear_mxfp4_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
+  const size_t mn = (size_t)M * N * (out_dtype == MOE_F32 ? 4 : 2), mk = (size_t)M * K, nk = (size_t)N * K, nb = (size_t)N * 4;
+  const Span outs[] = {{out, mn}, {ws, ws_bytes}};
+  const Span ins[] = {{x_codes, mk / 2}, {x_scales, mk / 32}, {w_codes, nk / 2}, {w_scales, nk / 32}, {w_up_codes, nk / 2},
+                      {w_up_scales, nk / 32}, {bias, nb}, {bias_up, nb}, {residual == out ? nullptr : residual, mn}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
+  moe::MxLinearArgs a{};
+  a.x = {static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales)};
+  a.w = {static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales)};
+  a.w_up = {static_cast<const uint8_t*>(w_up_codes), static_cast<const uint8_t*>(w_up_scales)};
+  a.bias = bias;
+  a.bias_up = bias_up;
+  a.residual = residual;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.out_f32 = out_dtype == MOE_F32;
+  a.out = out;
+  a.ws = ws;
+  return linear_launched(moe::launch_linear_mxfp4(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_grouped_linear_mxfp4(const void* x_codes, const void* x_scales, const int32_t* row_src, int64_t T, int32_t k,
+                                    const int32_t* expert_counts, const int32_t* expert_offsets, const int32_t* tiles,
+                                    const int32_t* num_tiles, const void* w_codes, const void* w_scales,
+                                    const void* w_up_codes, const void* w_up_scales, int32_t E_loc, int32_t N, int32_t K,
+                                    int32_t act, int32_t tile_m, int64_t R_cap, int64_t tiles_cap, int32_t out_dtype,
+                                    void* out, void* stream) {
+  if (E_loc < 1 || R_cap < 0 || tiles_cap < 0 || (out_dtype != MOE_BF16 && out_dtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (row_src && (T < 0 || k < 1)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = mxfp4_sizes(N, K, act);
+  if (st != MOE_OK) return st;
+  if (!tile_m_ok(tile_m) || R_cap > INT32_MAX || tiles_cap > INT32_MAX / 32) return MOE_ERR_UNSUPPORTED;
+  if (row_src && (k > 32 || T > (int64_t)INT32_MAX / (K / 2))) return MOE_ERR_UNSUPPORTED;
+  const bool dual = act == MOE_ACT_SWIGLU;
+  if (!dual && (w_up_codes || w_up_scales)) return MOE_ERR_INVALID_ARG;
+  if (R_cap == 0 || tiles_cap == 0 || (row_src && T == 0)) return MOE_OK;
+  const void* ptrs[] = {x_codes, x_scales, expert_counts, expert_offsets, tiles, num_tiles, w_codes, w_scales, out};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(row_src) || !aligned16(w_up_codes) || !aligned16(w_up_scales)) return MOE_ERR_INVALID_ARG;
+  if (dual && (!w_up_codes || !w_up_scales)) return MOE_ERR_INVALID_ARG;
+  const size_t xk = (size_t)(row_src ? T : R_cap) * K, nk = (size_t)E_loc * N * K, e4 = (size_t)E_loc * 4;
+  const Span outs[] = {{out, (size_t)R_cap * N * (out_dtype == MOE_F32 ? 4 : 2)}};
+  const Span ins[] = {{x_codes, xk / 2}, {x_scales, xk / 32}, {row_src, (size_t)R_cap * 4}, {expert_counts, e4},
+                      {expert_offsets, e4 + 4}, {tiles, (size_t)tiles_cap * 8}, {num_tiles, 4}, {w_codes, nk / 2},
+                      {w_scales, nk / 32}, {w_up_codes, nk / 2}, {w_up_scales, nk / 32}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
+  moe::MxLinearArgs a{};
+  a.x = {static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales)};
+  a.w = {static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales)};
+  a.w_up = {static_cast<const uint8_t*>(w_up_codes), static_cast<const uint8_t*>(w_up_scales)};
+  a.M = row_src ? T : R_cap;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.out_f32 = out_dtype == MOE_F32;
+  a.out = out;
+  a.counts = expert_counts;
+  a.offsets = expert_offsets;
+  a.tiles = tiles;
+  a.num_tiles = num_tiles;
+  a.row_src = row_src;
+  a.topk = k;
+  a.tile_m = tile_m;
+  a.tiles_cap = tiles_cap;
+  a.R_cap = R_cap;
+  return linear_launched(moe::launch_grouped_linear_mxfp4(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_few_tokens_workspace_bytes(int64_t T, int32_t k, int32_t F) {
+  if (T < 1 || T > moe::kFewTokens || k < 1 || k > 32 || F < 1 || F > (1 << 20)) return 0;
+  return moe::few_tokens_ws_bytes((int)T, k, F);
+}
+
+moe_status moe_few_tokens(const void* x, const float* logits, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                          int32_t expert_begin, int32_t E_loc, const void* w0, const void* w0_scales, const void* w0_up,
+                          const void* w0_up_scales, const void* w1, const void* w1_scales, int32_t H, int32_t F, int32_t act,
+                          int32_t* topk_idx, float* topk_w, float* out, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || E_loc < 1 || expert_begin < 0 || (int64_t)expert_begin + E_loc > E || H < 1 || F < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (act != MOE_ACT_GELU && act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+  const bool dual = act == MOE_ACT_SWIGLU, mx = w0_scales != nullptr;
+  if (!dual && (w0_up || w0_up_scales)) return MOE_ERR_INVALID_ARG;
+  if ((w1_scales != nullptr) != mx || (dual && (w0_up_scales != nullptr) != mx)) return MOE_ERR_INVALID_ARG;
+  if (T > moe::kFewTokens || E > 1024 || k > 32 || H % 128 != 0 || F % 128 != 0 || H > (1 << 20) || F > (1 << 20))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const void* ptrs[] = {x, w0, w1, topk_idx, topk_w, out, ws};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if ((dual && !w0_up) || !aligned16(w0_up) || !aligned16(logits) || !aligned16(w0_scales) || !aligned16(w0_up_scales) ||
+      !aligned16(w1_scales))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe::few_tokens_ws_bytes((int)T, k, F)) return MOE_ERR_WORKSPACE;
+  const size_t n = (size_t)E_loc * F * H, wb = mx ? n / 2 : n * 2, tk = (size_t)T * k * 4;
+  const Span ins[] = {{x, (size_t)T * H * 2}, {logits, (size_t)T * E * 4}, {w0, wb}, {w0_up, wb}, {w1, wb},
+                      {w0_scales, n / 32}, {w0_up_scales, n / 32}, {w1_scales, n / 32}};
+  const Span outs[] = {{out, (size_t)T * H * 4}, {ws, ws_bytes}, {topk_idx, tk}, {topk_w, tk}};
+  if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
+  const moe::FewArgs a{static_cast<const uint16_t*>(x), logits, (int)T, E, k, expert_begin, E_loc, H, F, act, renormalize != 0,
+                       w0, w0_up, w1, static_cast<const uint8_t*>(w0_scales), static_cast<const uint8_t*>(w0_up_scales),
+                       static_cast<const uint8_t*>(w1_scales), topk_idx, topk_w, out, ws};
+  return launched(moe::launch_few_tokens(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

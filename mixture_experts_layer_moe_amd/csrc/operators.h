@@ -67,4 +67,47 @@ struct LinearBwdArgs {
 size_t linear_backward_ws_bytes(int64_t M, int N, int K, int act);
 hipError_t launch_linear_backward(const LinearBwdArgs& a, hipStream_t s);
 
+// MXFP4 (codes of two values a byte, a scale byte per 32 values).
+hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t blocks, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, bool f32, void* out,
+                                   hipStream_t s);
+
+struct Mx {
+  const uint8_t *q, *s;  // codes, scales
+};
+struct MxLinearArgs {
+  Mx x, w, w_up;  // w_up: SwiGLU only
+  const float *bias, *bias_up;
+  const void* residual;
+  int64_t M;  // dense: rows; grouped: rows of x
+  int N, K, act;
+  bool out_f32;
+  void* out;
+  void* ws;
+  // Grouped: row tiles of the permutation (counts null: dense).
+  const int32_t *counts, *offsets, *tiles, *num_tiles, *row_src;  // row_src null: x's rows are the permuted ones
+  int topk, tile_m;
+  int64_t tiles_cap, R_cap;
+};
+size_t linear_mxfp4_ws_bytes(int64_t M, int N, int K, int act);
+hipError_t launch_linear_mxfp4(const MxLinearArgs& a, hipStream_t s);
+hipError_t launch_grouped_linear_mxfp4(const MxLinearArgs& a, hipStream_t s);
+
+// A whole layer for at most kFewTokens tokens.
+constexpr int kFewTokens = 64;
+struct FewArgs {
+  const uint16_t* x;
+  const float* logits;  // null: topk_idx and topk_w are given
+  int T, E, k, expert_begin, E_loc, H, F, act;
+  bool renormalize;
+  const void *w0, *w0_up, *w1;           // bf16, or MXFP4 codes
+  const uint8_t *s0, *s0_up, *s1;        // MXFP4 scales, or null
+  int32_t* topk_idx;
+  float* topk_w;
+  float* out;
+  void* ws;
+};
+size_t few_tokens_ws_bytes(int T, int k, int F);
+hipError_t launch_few_tokens(const FewArgs& a, hipStream_t s);
+
 }  // namespace moe

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional, Union
 
 import torch
 
@@ -64,6 +64,15 @@ _SIGNATURES = {
     "moe_linear_backward_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
     "moe_linear_backward": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p,
                                            _p, _sz, _p]),
+    "moe_mxfp4_quantize": (ctypes.c_int, [_p, _i64, _i32, _i32, _p, _p, _p]),
+    "moe_mxfp4_dequantize": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _p, _p]),
+    "moe_linear_mxfp4_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "moe_linear_mxfp4": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32, _p, _p, _sz, _p]),
+    "moe_grouped_linear_mxfp4": (ctypes.c_int, [_p, _p, _p, _i64, _i32, _p, _p, _p, _p, _p, _p, _p, _p, _i32, _i32, _i32,
+                                                _i32, _i32, _i64, _i64, _i32, _p, _p]),
+    "moe_few_tokens_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "moe_few_tokens": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _i32, _i32, _i32,
+                                      _p, _p, _p, _p, _sz, _p]),
 }
 
 
@@ -535,3 +544,225 @@ def moe_linear_backward(d_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor, w
             _choice(OUT_DTYPES, d_out.dtype, "d_out's type"), _take(d_x, "d_x", bf, mk, dev, True),
             _take(d_w, "d_w", bf, nk, dev, True), _take(d_w_up, "d_w_up", bf, nk, dev, True),
             _take(d_bias, "d_bias", f32, (N,), dev, True), _take(d_bias_up, "d_bias_up", f32, (N,), dev, True), wsp, wsn)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit operands (MXFP4) and the layer for a few tokens; checks and devices as above.
+# ---------------------------------------------------------------------------
+
+class Mxfp4(NamedTuple):
+    """A matrix (or a stack of them) in MXFP4: codes [..., K / 2] and scales [..., K / 32], both uint8 (see include/moe.h)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        """Of the values."""
+        return (*self.codes.shape[:-1], self.codes.shape[-1] * 2)
+
+
+def alloc_mxfp4(shape, device) -> Mxfp4:
+    u8 = dict(dtype=torch.uint8, device=device)
+    return Mxfp4(torch.empty((*shape[:-1], shape[-1] // 2), **u8), torch.empty((*shape[:-1], shape[-1] // 32), **u8))
+
+
+def _mx(t: Optional[Mxfp4], name: str, shape, dev: int, optional: bool = False):
+    """Addresses (codes, scales) of a checked MXFP4 argument of that value shape."""
+    if t is None:
+        if optional:
+            return None, None
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, Mxfp4):
+        raise TypeError(f"{name} must be an Mxfp4, got {type(t).__name__}")
+    u8, lead, K = torch.uint8, tuple(shape[:-1]), shape[-1]
+    return (_take(t.codes, f"{name}.codes", u8, (*lead, K // 2), dev),
+            _take(t.scales, f"{name}.scales", u8, (*lead, K // 32), dev))
+
+
+def _mx_shape(t, name: str, dims: int):
+    """(device number, value shape) of an MXFP4 argument of `dims` dimensions."""
+    if not isinstance(t, Mxfp4):
+        raise TypeError(f"{name} must be an Mxfp4, got {type(t).__name__}")
+    if t.codes.get_device() < 0:
+        raise ValueError(f"{name} must be on a device")
+    if t.codes.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.codes.dim()}")
+    return t.codes.get_device(), t.shape
+
+
+def _need_k(K: int, multiple: int, name: str):
+    if K < 1 or K % multiple:
+        raise ValueError(f"the last dimension of {name} must be a multiple of {multiple}, got {K}")
+
+
+def moe_mxfp4_quantize(x: torch.Tensor, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
+    """x (bf16 or fp32, [..., K]) in MXFP4, blocks of 32 along the last dimension."""
+    if stream is not None:
+        _same_device(stream, x, out)
+        return _on(stream, moe_mxfp4_quantize, x, out)
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or x.dim() < 1:
+        raise ValueError("x must be a device tensor of at least one dimension")
+    K = shape[-1]
+    _need_k(K, 32, "x")
+    if out is None:
+        out = alloc_mxfp4(shape, x.device)
+    codes, scales = _mx(out, "out", shape, dev)
+    _launch((_lib or lib()).moe_mxfp4_quantize, "moe_mxfp4_quantize", dev, _take(x, "x", x.dtype, shape, dev), x.numel() // K, K,
+            _choice(OUT_DTYPES, x.dtype, "x's type"), codes, scales)
+    return out
+
+
+def moe_mxfp4_dequantize(q: Mxfp4, out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                         stream=None) -> torch.Tensor:
+    """The values of q; out's type wins over out_dtype."""
+    if stream is not None:
+        _same_device(stream, q, out)
+        return _on(stream, moe_mxfp4_dequantize, q, out, out_dtype)
+    if not isinstance(q, Mxfp4) or q.codes.get_device() < 0 or q.codes.dim() < 1:
+        raise ValueError("q must be an Mxfp4 on a device")
+    dev, shape = q.codes.get_device(), q.shape
+    K = shape[-1]
+    _need_k(K, 32, "q")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.codes.device)
+    codes, scales = _mx(q, "q", shape, dev)
+    _launch((_lib or lib()).moe_mxfp4_dequantize, "moe_mxfp4_dequantize", dev, codes, scales, out.numel() // K, K,
+            _choice(OUT_DTYPES, out.dtype, "out's type"), _take(out, "out", out.dtype, shape, dev))
+    return out
+
+
+def _same_device(stream, *operands):
+    """MXFP4 operands' and weights' devices against a stream's (tensors among them are looked at by _on)."""
+    for q in operands:
+        if isinstance(q, Mxfp4):
+            for t in q:
+                if t.device != stream.device:
+                    raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+
+
+def linear_mxfp4_workspace_bytes(M: int, N: int, K: int, act: str) -> int:
+    return int(lib().moe_linear_mxfp4_workspace_bytes(M, N, K, _choice(LINEAR_ACTS, act, "act")))
+
+
+def alloc_linear_mxfp4_workspace(M: int, N: int, K: int, act: str, device) -> Optional[torch.Tensor]:
+    """Workspace of moe_linear_mxfp4 on that device (None where this size needs none)."""
+    with torch.cuda.device(device):
+        return _alloc_ws(linear_mxfp4_workspace_bytes(M, N, K, act), device)
+
+
+def moe_linear_mxfp4(x: Mxfp4, w: Mxfp4, w_up: Optional[Mxfp4] = None, bias: Optional[torch.Tensor] = None,
+                     bias_up: Optional[torch.Tensor] = None, act: str = "none", residual: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                     ws: Optional[torch.Tensor] = None, stream=None, use_workspace: bool = True) -> torch.Tensor:
+    """moe_linear of MXFP4 operands x [M, K], w and w_up [N, K]; out may be residual itself, its type wins over out_dtype."""
+    if stream is not None:
+        _same_device(stream, x, w, w_up)
+        return _on(stream, moe_linear_mxfp4, x, w, w_up, bias, bias_up, act, residual, out, out_dtype, ws,
+                   use_workspace=use_workspace)
+    (dev, (M, K)), (_, (N, _)) = _mx_shape(x, "x", 2), _mx_shape(w, "w", 2)
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.codes.device)
+    odt = out.dtype
+    a = _choice(LINEAR_ACTS, act, "act")
+    if ws is None and use_workspace:
+        ws = alloc_linear_mxfp4_workspace(M, N, K, act, x.codes.device)
+    wsp, wsn = _ws(ws, dev)
+    _launch((_lib or lib()).moe_linear_mxfp4, "moe_linear_mxfp4", dev, *_mx(x, "x", (M, K), dev), *_mx(w, "w", (N, K), dev),
+            *_mx(w_up, "w_up", (N, K), dev, True), _take(bias, "bias", f32, (N,), dev, True),
+            _take(bias_up, "bias_up", f32, (N,), dev, True), _take(residual, "residual", odt, (M, N), dev, True), M, N, K, a,
+            _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, (M, N), dev), wsp, wsn)
+    return out
+
+
+def moe_grouped_linear_mxfp4(p: Permuted, x: Mxfp4, w: Mxfp4, w_up: Optional[Mxfp4] = None, act: str = "none",
+                             gather: bool = False, out: Optional[torch.Tensor] = None,
+                             out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """act(x . w[e]^T) for the rows of every local expert e.  gather: x holds the tokens [T, K], read through p.row_src;
+    else the permuted rows [R_cap, K].  Rows of out that no token has are left as they were."""
+    if stream is not None:
+        _same_device(stream, x, w, w_up)
+        return _on(stream, moe_grouped_linear_mxfp4, p, x, w, w_up, act, gather, out, out_dtype)
+    (dev, (rows, K)), (_, (E_loc, N, _)) = _mx_shape(x, "x", 2), _mx_shape(w, "w", 3)
+    i32 = torch.int32
+    T, k = p.inv_perm.shape if gather else (0, 0)
+    if out is None:
+        out = torch.empty((p.R_cap, N), dtype=out_dtype, device=x.codes.device)
+    odt = out.dtype
+    _launch((_lib or lib()).moe_grouped_linear_mxfp4, "moe_grouped_linear_mxfp4", dev,
+            *_mx(x, "x", (T if gather else p.R_cap, K), dev), _take(p.row_src, "row_src", i32, (p.R_cap,), dev) if gather else None,
+            T, k, _take(p.expert_counts, "expert_counts", i32, (E_loc,), dev),
+            _take(p.expert_offsets, "expert_offsets", i32, (E_loc + 1,), dev), _take(p.tiles, "tiles", i32, (p.tiles_cap, 2), dev),
+            _take(p.num_tiles, "num_tiles", i32, (1,), dev), *_mx(w, "w", (E_loc, N, K), dev),
+            *_mx(w_up, "w_up", (E_loc, N, K), dev, True), E_loc, N, K, _choice(LINEAR_ACTS, act, "act"), p.tile_m, p.R_cap,
+            p.tiles_cap, _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, (p.R_cap, N), dev))
+    return out
+
+
+FEW_TOKENS = 64  # the most tokens moe_few_tokens takes
+
+Weight = Union[torch.Tensor, Mxfp4]
+
+
+def few_tokens_workspace_bytes(T: int, k: int, F: int) -> int:
+    return int(lib().moe_few_tokens_workspace_bytes(T, k, F))
+
+
+def alloc_few_tokens_workspace(T: int, k: int, F: int, device) -> Optional[torch.Tensor]:
+    return _alloc_ws(few_tokens_workspace_bytes(T, k, F), device)
+
+
+def moe_few_tokens(x: torch.Tensor, w0: Weight, w0_up: Optional[Weight], w1: Weight, act: str,
+                   logits: Optional[torch.Tensor] = None, k: Optional[int] = None, renormalize: bool = True,
+                   topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None, expert_begin: int = 0,
+                   num_experts: Optional[int] = None, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The whole layer for x [T <= 64, H] over bf16 or MXFP4 experts.
+
+    With logits [T, E] the tokens are routed to their k best experts (topk_idx and topk_w, where given, receive the
+    choice); without, topk_idx and topk_w are the choice, over num_experts experts (default: the local range's end).
+    """
+    if stream is not None:
+        _same_device(stream, w0, w0_up, w1)
+        return _on(stream, moe_few_tokens, x, w0, w0_up, w1, act, logits, k, renormalize, topk_idx, topk_w, expert_begin,
+                   num_experts, out, ws)
+    (T, H), dev = _matrix(x, "x"), x.get_device()
+    mx, bf, f32 = isinstance(w0, Mxfp4), torch.bfloat16, torch.float32
+    E_loc, F = w0.shape[:2] if len(w0.shape) == 3 else (0, 0)
+    if logits is not None:
+        E = _matrix(logits, "logits")[1]
+        if k is None:
+            if topk_idx is None:
+                raise ValueError("k is required")
+            k = _matrix(topk_idx, "topk_idx")[1]
+        if topk_idx is None:
+            topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, max(k, 0)), dtype=f32, device=x.device)
+    else:
+        if topk_idx is None or topk_w is None:
+            raise ValueError("topk_idx and topk_w are required where there are no logits")
+        k = _matrix(topk_idx, "topk_idx")[1]
+        E = expert_begin + E_loc if num_experts is None else num_experts
+        E = max(E, k)  # (ids beyond the local range name experts elsewhere)
+    if out is None:
+        out = torch.empty((T, H), dtype=f32, device=x.device)
+    if ws is None:
+        ws = alloc_few_tokens_workspace(T, k, F, x.device)
+    wsp, wsn = _ws(ws, dev)
+
+    def weight(w, name, shape, optional=False):
+        if mx:
+            return _mx(w, name, shape, dev, optional)
+        if isinstance(w, Mxfp4):
+            raise TypeError(f"{name} is an Mxfp4, w0 is not")
+        return _take(w, name, bf, shape, dev, optional), None
+
+    up, down = (E_loc, F, H), (E_loc, H, F)
+    _launch((_lib or lib()).moe_few_tokens, "moe_few_tokens", dev, _take(x, "x", bf, (T, H), dev),
+            _take(logits, "logits", f32, (T, E), dev, True), T, E, k, 1 if renormalize else 0, expert_begin, E_loc,
+            *weight(w0, "w0", up), *weight(w0_up, "w0_up", up, True), *weight(w1, "w1", down), H, F, _choice(ACTS, act, "act"),
+            _take(topk_idx, "topk_idx", torch.int32, (T, k), dev), _take(topk_w, "topk_w", f32, (T, k), dev),
+            _take(out, "out", f32, (T, H), dev), wsp, wsn)
+    return out
