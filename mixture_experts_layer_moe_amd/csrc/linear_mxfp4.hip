@@ -9,6 +9,8 @@
 // The weights feed the instruction's rows and the tokens its columns, so that a lane's results belong to one token.
 #include "activation.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -69,6 +71,22 @@ __device__ __forceinline__ Rows rows_of(const Product& p, int ti, int bm) {
 // ---------------------------------------------------------------------------
 // Epilogue
 // ---------------------------------------------------------------------------
+template <int V>
+__device__ __forceinline__ void load_bias(const float* b, int left, bool whole, float (&v)[V]) {
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const floatx4 q = *reinterpret_cast<const floatx4*>(b + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i + e] = q[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < left) v[i] = b[i];
+  }
+}
+
 // V values of one row from column n: bias, activation, residual, rounding, stores.  `at` is the element's index in out.
 template <int V>
 __device__ __forceinline__ void finish(const MxLinearArgs& a, int64_t at, int n, float (&z)[V], const float (&u)[V]) {
@@ -78,10 +96,9 @@ __device__ __forceinline__ void finish(const MxLinearArgs& a, int64_t at, int n,
   const bool whole = left >= V && a.N % 8 == 0;  // (then every row's groups of V are 16-byte aligned)
   float bz[V], bu[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bz[i] = a.bias && i < left ? a.bias[n + i] : 0.f;
-    bu[i] = a.bias_up && i < left ? a.bias_up[n + i] : 0.f;
-  }
+  for (int i = 0; i < V; ++i) bz[i] = bu[i] = 0.f;
+  if (a.bias) load_bias<V>(a.bias + n, left, whole, bz);
+  if (a.bias_up) load_bias<V>(a.bias_up + n, left, whole, bu);
   switch (a.act) {
     case ACT_NONE:
 #pragma unroll
@@ -158,30 +175,39 @@ __device__ __forceinline__ void tile_of(int bid, int mt, int nt, int& ti, int& t
 }
 
 // Physical 16-byte chunk of logical chunk c in LDS row r is c ^ swz(r).  The 16 lanes that a 16-byte LDS read serves
-// together are lanes 0-3, 12-15, 20-27 or 4-11, 16-19, 28-31 (and 32 on): this spreads both the token fragment's rows
-// (lane) and the weight fragment's (weight_row) over all 64 banks.
+// together are lanes 0-3, 12-15, 20-27 or 4-11, 16-19, 28-31 (and 32 on): this spreads a fragment's rows over all
+// 64 banks.
 __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
-
-// The weight row, of a block of 32, that feeds row r of the matrix instruction.  Result element i of lane half h is
-// instruction row 8 (i / 4) + 4 h + i % 4; fed by weight row 16 h + i, a lane's 16 results are 16 columns side by side.
-__device__ __forceinline__ constexpr int weight_row(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
 // BM rows by BN columns (NMAT = 2: BN of each matrix), WM x WN wavefronts.
 //
-// A stage of 256 reduction indices (128 bytes a row, and 8 scale bytes) goes straight from global memory to one of two
-// LDS buffers while the other is multiplied.  Lane half h takes the stage's blocks 4 h .. 4 h + 3, one for each of four
-// instructions, so that the four scales are the bytes of one word, selected by the instruction.
+// Two LDS buffers and register-staged codes: while a stage of 256 reduction indices (128 bytes a row: whole cache lines)
+// is multiplied from one buffer, the next stage goes from registers into the other and the registers reload with the one
+// after it.  A stage is four steps, each a matrix instruction of 64 indices per accumulator; a step's fragments are read
+// during the step before, and the writes and loads are spread over the first three.  When the last step begins the
+// stage has been read: there the workgroup synchronises, and the last step reads the next stage's first fragments.
+//
+// The scales go straight to LDS for two stages at a time, 16 bytes a row: a row's bytes of one stage would each time be
+// an access of their own to the row's cache line, nearly as many as the codes need (340 us instead of 294 at
+// 4096 x 14336 x 4096 SwiGLU with 128-wide stages).  Lane half h takes the stage's blocks 4 h .. 4 h + 3, one for each
+// step, whose scales are the bytes of the word that it reads.
 template <int BM, int BN, int NMAT, int WM, int WN>
 struct Tile {
   static constexpr int NW = WM * WN;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  static constexpr int SA = A_BYTES + NMAT * B_BYTES, SB = SA + BM * 8;  // the scales' places in a stage
-  static constexpr int STAGE = SB + NMAT * BN * 8;
+  static constexpr int STAGE = A_BYTES + NMAT * B_BYTES;
+  static constexpr int ROWS = BM + NMAT * BN;  // of x, then of the matrices
+  static constexpr int SCALES = 2 * STAGE;    // two places of 16 bytes a row
+  static constexpr int SMEM = SCALES + 2 * ROWS * 16;
+  static constexpr int PITCH = NMAT * BN / WN + 4, EPI = 32 * PITCH * 4;  // floats a staged row, bytes of 32 of them
   static constexpr int WT_M = BM / WM, WT_N = BN / WN;
   static constexpr int TM = WT_M / 32, TN = WT_N / 32, NB = NMAT * TN;
   static constexpr int A_PIECES = BM / (8 * NW), B_PIECES = BN / (8 * NW);
-  static_assert(BM == 32 * NW && NMAT * BN == 32 * NW, "a wavefront loads 32 rows' scales of either operand");
-  static_assert(A_PIECES >= 1 && B_PIECES >= 1 && TM >= 1 && TN >= 1, "tile too small for the wavefronts");
+  static constexpr int S_ALL = ROWS / 64, S_PIECES = (S_ALL + NW - 1) / NW;
+  static constexpr int LOADS = A_PIECES + NMAT * B_PIECES;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "whole pieces");
+  static_assert(TM >= 1 && TN >= 1, "tile");
+  static_assert(NW * EPI <= SMEM, "room for the results");
 
   template <bool GROUPED>
   static __device__ __forceinline__ void run(char* smem, const Product& p, const Rows& rw, int n0) {
@@ -192,62 +218,65 @@ struct Tile {
     const bool gather = GROUPED && a.row_src != nullptr;
     const int cols = a.N - n0 < BN ? a.N - n0 : BN;
 
-    // Resources: x's rows (gathered: all of x), the tile's weight rows.
+    // Resources: x's rows (gathered: all of x), the tile's weight rows.  Rows past them read zeros.
     const int64_t x0 = gather ? 0 : rw.row0, xr = gather ? a.M : rw.valid;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x.q + x0 * kb, xr * kb), rxs = make_rsrc(a.x.s + x0 * sb, xr * sb);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x.q + x0 * kb, xr * kb);
     const int64_t w0 = (int64_t)rw.expert * a.N + n0;
     const __amdgpu_buffer_rsrc_t rwq[2] = {make_rsrc(a.w.q + w0 * kb, (int64_t)cols * kb),
                                            make_rsrc((NMAT == 2 ? a.w_up.q : a.w.q) + w0 * kb, (int64_t)cols * kb)};
-    // This lane's offsets.  Codes: rows of 8 lanes, 16 bytes each.  Scales: rows of 2 lanes, a word each; the wavefront
-    // loads those of 32 rows of x and of 32 rows of the matrices one after the other.
+    // Row r of the tile in x, kOut where there is none.
+    auto row_of = [&](int r) -> uint32_t {
+      if (r >= rw.valid) return kOut;
+      if (!gather) return (uint32_t)r;
+      const int src = a.row_src[rw.row0 + r];
+      const uint32_t t = (uint32_t)src / (uint32_t)a.topk;
+      return src >= 0 && t < a.M ? t : kOut;
+    };
+    // This lane's offsets.  Codes: rows of 8 lanes, 16 bytes each.  Scales: a row a lane.
     const int r_in = lane >> 3, chunk = (lane & 7) ^ swz(wave * 8 + r_in);
-    uint32_t off_a[A_PIECES], off_b = (uint32_t)((wave * 8 + r_in) * kb + chunk * 16);
-    uint32_t off_sa, off_sb;
+    uint32_t off_a[A_PIECES], off_s[S_PIECES];
+    __amdgpu_buffer_rsrc_t rs[S_PIECES];
 #pragma unroll
     for (int q = 0; q < A_PIECES; ++q) {
-      const int r = (q * NW + wave) * 8 + r_in;
-      uint32_t row = (uint32_t)r;
-      bool in = r < rw.valid;
-      if (gather) {
-        const int src = in ? a.row_src[rw.row0 + r] : -1;
-        row = (uint32_t)src / (uint32_t)a.topk;
-        in = src >= 0 && row < a.M;
-      }
-      off_a[q] = in ? row * (uint32_t)kb + chunk * 16 : kOut;
+      const uint32_t row = row_of((q * NW + wave) * 8 + r_in);
+      off_a[q] = row != kOut ? row * (uint32_t)kb + chunk * 16 : kOut;
     }
-    {
-      const int r = wave * 32 + (lane >> 1);
-      uint32_t row = (uint32_t)r;
-      bool in = r < rw.valid;
-      if (gather) {
-        const int src = in ? a.row_src[rw.row0 + r] : -1;
-        row = (uint32_t)src / (uint32_t)a.topk;
-        in = src >= 0 && row < a.M;
+    const uint32_t off_b = (uint32_t)((wave * 8 + r_in) * kb + chunk * 16);
+#pragma unroll
+    for (int q = 0; q < S_PIECES; ++q) {
+      const int first = ((q * NW + wave) % S_ALL) * 64;  // (a last piece over is loaded twice)
+      if (first < BM) {
+        const uint32_t row = row_of(first + lane);
+        off_s[q] = row != kOut ? row * (uint32_t)sb : kOut;
+        rs[q] = make_rsrc(a.x.s + x0 * sb, xr * sb);
+      } else {
+        const int c = first - BM, m = NMAT == 2 && c >= BN;
+        off_s[q] = (uint32_t)((c - m * BN + lane) * sb);
+        rs[q] = make_rsrc((m ? a.w_up.s : a.w.s) + w0 * sb, (int64_t)cols * sb);
       }
-      off_sa = in ? row * (uint32_t)sb + (lane & 1) * 4 : kOut;
-      off_sb = (uint32_t)((r % BN) * sb + (lane & 1) * 4);
     }
-    const bool up_scales = NMAT == 2 && wave * 32 >= BN;
-    const __amdgpu_buffer_rsrc_t rws = make_rsrc((up_scales ? a.w_up.s : a.w.s) + w0 * sb, (int64_t)cols * sb);
+
     // K is a multiple of 128: where the last stage is half a stage, the later half of each row reads zeros.
     const bool odd = (a.K & 128) != 0;
-    const uint32_t cut_c = chunk >= 4 ? kOut : 0, cut_s = (lane & 1) ? kOut : 0;
-
-    auto issue = [&](int kt, int buf) {
-      char* st = smem + buf * STAGE;
-      const bool cut = odd && kt == nk - 1;
-      const uint32_t at = (uint32_t)kt * 128, cc = cut ? cut_c : 0, cs = cut ? cut_s : 0;
+    const uint32_t cut = chunk >= 4 ? kOut : 0;
+    // Stage kt's codes, piece by piece: from global memory to registers, from there to LDS.
+    u32x4 stg[LOADS];
+    auto load = [&](int q, int kt) {  // (stages past the last load from past the resources)
+      const uint32_t none = kt < nk ? (odd && kt == nk - 1 ? cut : 0) : kOut, at = (uint32_t)kt * 128;
+      if (q < A_PIECES) stg[q] = __builtin_amdgcn_raw_buffer_load_b128(rx, (off_a[q < A_PIECES ? q : 0] + at) | none, 0, 0);
+      else stg[q] = __builtin_amdgcn_raw_buffer_load_b128(rwq[(q - A_PIECES) / B_PIECES],
+                                                          (off_b + (q - A_PIECES) % B_PIECES * 8 * NW * kb + at) | none, 0, 0);
+    };
+    auto write = [&](int q, int kt) {
+      const int line = q < A_PIECES ? q * NW : BM / 8 + (q - A_PIECES) / B_PIECES * (BN / 8) + (q - A_PIECES) % B_PIECES * NW;
+      *reinterpret_cast<u32x4*>(smem + (kt % 2) * STAGE + (line + wave) * 1024 + lane * 16) = stg[q];
+    };
+    // The scales of stages kt and kt + 1 (16 bytes may run into the next row's, which no stage uses).
+    auto issue_scales = [&](int kt) {
 #pragma unroll
-      for (int q = 0; q < A_PIECES; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(st + (q * NW + wave) * 1024), 16, (off_a[q] + at) | cc, 0, 0, 0);
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-        for (int q = 0; q < B_PIECES; ++q)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rwq[m], (lds_void*)(st + A_BYTES + m * B_BYTES + (q * NW + wave) * 1024), 16,
-                                                   (off_b + q * 8 * NW * kb + at) | cc, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (lds_void*)(st + SA + wave * 256), 4, (off_sa + kt * 8) | cs, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rws, (lds_void*)(st + SB + wave * 256), 4, (off_sb + kt * 8) | cs, 0, 0, 0);
+      for (int q = 0; q < S_PIECES; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs[q], (lds_void*)(smem + SCALES + (kt / 2 % 2) * (ROWS * 16) + ((q * NW + wave) % S_ALL) * 1024), 16, off_s[q] + kt * 8, 0, 0, 0);
     };
 
     floatx16 acc[NB][TM];
@@ -257,69 +286,159 @@ struct Tile {
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
-    const int brow = weight_row(l32);
 
-    issue(0, 0);
-    wait_vmcnt<0>();
-    ring_barrier();
-    for (int kt = 0; kt < nk; ++kt) {
-      const char* st = smem + (kt & 1) * STAGE;
-      if (kt + 1 < nk) issue(kt + 1, (kt & 1) ^ 1);
-      int sa[TM], sw[NB];
+    struct Frags {
+      u32x4 a[TM], b[NB];
+    };
+    struct Scales {
+      int a[TM], b[NB];
+    };
+    auto read = [&](Frags& f, int kt, int step) {
+      const char* st = smem + (kt % 2) * STAGE;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const int*>(st + SA + (wm * WT_M + i * 32 + l32) * 8 + half * 4);
+      for (int j = 0; j < NB; ++j) {
+        const int row = wn * WT_N + (j % TN) * 32 + l32;
+        f.b[j] = *reinterpret_cast<const u32x4*>(st + A_BYTES + (j / TN) * B_BYTES + row * 128 + (((half * 4 + step) ^ swz(row)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int row = wm * WT_M + i * 32 + l32;
+        f.a[i] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((half * 4 + step) ^ swz(row)) << 4));
+      }
+    };
+    auto read_scales = [&](Scales& f, int kt) {
+      const char* sc = smem + SCALES + (kt / 2 % 2) * (ROWS * 16) + (kt % 2) * 8 + half * 4;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) f.a[i] = *reinterpret_cast<const int*>(sc + (wm * WT_M + i * 32 + l32) * 16);
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        sw[j] = *reinterpret_cast<const int*>(st + SB + ((j / TN) * BN + wn * WT_N + (j % TN) * 32 + brow) * 8 + half * 4);
-#define MOE_STEP(S_)                                                                                              \
-  {                                                                                                               \
-    u32x4 fa[TM], fb[NB];                                                                                         \
-    _Pragma("unroll") for (int j = 0; j < NB; ++j) {                                                              \
-      const int row = wn * WT_N + (j % TN) * 32 + brow;                                                           \
-      fb[j] = *reinterpret_cast<const u32x4*>(st + A_BYTES + (j / TN) * B_BYTES + row * 128 + (((half * 4 + S_) ^ swz(row)) << 4)); \
-    }                                                                                                             \
-    _Pragma("unroll") for (int i = 0; i < TM; ++i) {                                                              \
-      const int row = wm * WT_M + i * 32 + l32;                                                                   \
-      fa[i] = *reinterpret_cast<const u32x4*>(st + row * 128 + (((half * 4 + S_) ^ swz(row)) << 4));              \
-    }                                                                                                             \
-    _Pragma("unroll") for (int j = 0; j < NB; ++j) _Pragma("unroll") for (int i = 0; i < TM; ++i)                 \
-        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fb[j]), widen(fa[i]), acc[j][i], kFp4, kFp4, S_, \
-                                                                    sw[j], S_, sa[i]);                            \
-  }
-      MOE_STEP(0)
-      MOE_STEP(1)
-      MOE_STEP(2)
-      MOE_STEP(3)
-#undef MOE_STEP
-      wait_vmcnt<0>();
-      wait_lgkm0();
-      ring_barrier();
-    }
-
-    // Lane: row l32 of each 32-row block, 16 columns side by side of each 32-column block.  One block at a time in a
-    // loop, so that the activations' code is there once.
-    constexpr int BLOCKS = TN * TM;
-#pragma unroll 1
-    for (int b = 0; b < BLOCKS; ++b) {
-      floatx16 z = acc[0][0], u = acc[0][0];
+        f.b[j] = *reinterpret_cast<const int*>(sc + (BM + (j / TN) * BN + wn * WT_N + (j % TN) * 32 + l32) * 16);
+    };
+    auto multiply = [&](auto step, const Frags& f, const Scales& s) {
+      constexpr int S = decltype(step)::value;
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-          if (j * TM + i == b) {
-            z = acc[j][i];
-            if (NMAT == 2) u = acc[NB - TN + j][i];
-          }
-      const int r = wm * WT_M + (b % TM) * 32 + l32;
-      if (r >= rw.valid) continue;
-      const int n = n0 + wn * WT_N + (b / TM) * 32 + half * 16;
-      float zv[16], uv[16];
+          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(f.b[j]), widen(f.a[i]), acc[j][i], kFp4, kFp4, S,
+                                                                      s.b[j], S, s.a[i]);
+      // (the instructions have no side effects: the use of the accumulators keeps them on this side of the barrier)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        zv[i] = z[i];
-        uv[i] = u[i];
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(acc[j][i]));
+    };
+    // Instruction order of a step: an LDS read after each matrix instruction while there are any, and the pieces' writes
+    // and loads in the places after those.
+    auto order = [&](auto reads, auto pieces) {
+      constexpr int nr = decltype(reads)::value, np = decltype(pieces)::value, nm = NB * TM;
+#pragma unroll
+      for (int t = 0; t < nm; ++t) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (t < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (t + nm < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (t >= nm - np) {
+          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
       }
-      finish<16>(a, (rw.row0 + r) * a.N + n, n, zv, uv);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    using std::integral_constant;
+    Frags f[2];
+    Scales sc, next;
+    issue_scales(0);
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) load(q, 0);
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) write(q, 0);  // (waits for the scales too, which went ahead)
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) load(q, 1);
+    wait_lgkm0();
+    ring_barrier();
+    read(f[0], 0, 0);
+    read_scales(next, 0);
+    constexpr int P0 = (LOADS + 2) / 3, P1 = 2 * P0 < LOADS ? 2 * P0 : LOADS;
+    for (int kt = 0; kt < nk; ++kt) {
+      if (kt % 2 == 0 && kt + 2 < nk) issue_scales(kt + 2);
+      auto pieces = [&](int from, int to) {
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+          if (q >= from && q < to) {
+            write(q, kt + 1);
+            load(q, kt + 2);
+          }
+      };
+      sc = next;
+      if (odd && kt == nk - 1 && half) {  // (no scales there; the codes are zeros)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sc.a[i] = 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) sc.b[j] = 0;
+      }
+      read(f[1], kt, 1);
+      pieces(0, P0);
+      multiply(integral_constant<int, 0>{}, f[0], sc);
+      order(integral_constant<int, TM + NB>{}, integral_constant<int, P0>{});
+      read(f[0], kt, 2);
+      pieces(P0, P1);
+      multiply(integral_constant<int, 1>{}, f[1], sc);
+      order(integral_constant<int, TM + NB>{}, integral_constant<int, P1 - P0>{});
+      read(f[1], kt, 3);
+      pieces(P1, LOADS);
+      multiply(integral_constant<int, 2>{}, f[0], sc);
+      order(integral_constant<int, TM + NB>{}, integral_constant<int, LOADS - P1>{});
+      wait_lgkm0();    // this wavefront's reads of stage kt and writes of stage kt + 1 are done
+      ring_barrier();  // so are all others'
+      __builtin_amdgcn_sched_barrier(0);
+      read(f[0], kt + 1, 0);
+      read_scales(next, kt + 1);
+      multiply(integral_constant<int, 3>{}, f[1], sc);
+      order(integral_constant<int, 2 * (TM + NB)>{}, integral_constant<int, 0>{});
+    }
+    ring_barrier();
+
+    // A lane holds, for row l32 of a 32-row block, columns 8 (v / 4) + 4 half + v % 4 of each 32-column block (v: element
+    // of the accumulator).  32 rows at a time go through this wavefront's part of LDS, so that stores run along rows.
+    float* sm = reinterpret_cast<float*>(smem + wave * EPI);
+#pragma unroll 1
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int ii = 0; ii < TM; ++ii) {
+        if (ii != i) continue;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; v += 4)
+            *reinterpret_cast<floatx4*>(sm + l32 * PITCH + j * 32 + 2 * v + half * 4) =
+                floatx4{acc[j][ii][v], acc[j][ii][v + 1], acc[j][ii][v + 2], acc[j][ii][v + 3]};
+      }
+      const int r0 = wm * WT_M + i * 32;
+      if (a.out_f32) store_rows<4>(a, rw, sm, r0, n0 + wn * WT_N, lane);
+      else store_rows<8>(a, rw, sm, r0, n0 + wn * WT_N, lane);
+    }
+  }
+
+  // The epilogue of 32 staged rows from row r0 of the tile: V columns a lane.
+  template <int V>
+  static __device__ __forceinline__ void store_rows(const MxLinearArgs& a, const Rows& rw, const float* sm, int r0, int n0,
+                                                    int lane) {
+    constexpr int LPR = WT_N / V, STEP = 64 / LPR;  // lanes a row, rows at a time
+    const int c = lane % LPR * V;
+#pragma unroll 1
+    for (int r = lane / LPR; r < 32; r += STEP) {
+      float z[V], u[V];
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const floatx4 p = *reinterpret_cast<const floatx4*>(sm + r * PITCH + c + v);
+        const floatx4 q = NMAT == 2 ? *reinterpret_cast<const floatx4*>(sm + r * PITCH + WT_N + c + v) : p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[v + e] = p[e];
+          u[v + e] = q[e];
+        }
+      }
+      if (r0 + r < rw.valid) finish<V>(a, (rw.row0 + r0 + r) * a.N + n0 + c, n0 + c, z, u);
     }
   }
 };
@@ -327,7 +446,7 @@ struct Tile {
 template <int BM, int BN, int NMAT, int WM, int WN, bool GROUPED>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
   using T = Tile<BM, BN / NMAT, NMAT, WM, WN>;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * T::STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
   int mt = p.mt;
   if (GROUPED) {
     const int n = *p.a.num_tiles * p.sub;
