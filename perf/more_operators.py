@@ -274,7 +274,7 @@ def run(state):
         mx = c["weights"] == "mxfp4"
         w0, w0_up, w1 = (_mx(ffi, s, n) if mx else s[n] for n in ("w0", "w0_up", "w1"))
         ffi.moe_few_tokens(s["x"], w0, w0_up, w1, c["act"], logits=s["logits"], topk_idx=s["idx"], topk_w=s["gate"],
-                           out=s["out"], ws=s["ws"])
+                           num_experts=c["E"], out=s["out"], ws=s["ws"])
         return (s["out"], s["idx"], s["gate"]) if c["logits"] else s["out"]
     return {"quant": _quant, "linear": _linear, "grouped": _grouped, "few": _few}[c["op"]](s, c)
 
