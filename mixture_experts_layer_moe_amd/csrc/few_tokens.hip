@@ -7,12 +7,18 @@
 // experts' weights: every weight is loaded once, straight into the matrix instructions' registers, by as many
 // wavefronts as it takes to keep HBM busy; nothing is permuted and no row is padded to a tile.
 //
-// v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and up to 16 tokens on its columns: a column's result
-// depends on its own token alone, so columns without a token hold anything.  MXFP4 weights are widened in registers to
-// bf16, which is exact.  x is bf16; the activations go between the launches as two bf16 terms (a value and the
-// remainder, 16 bits of mantissa), so that the output keeps fp32 accuracy: the second product costs twice the matrix
-// instructions, which the loads hide.
+// v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and tokens on its 16 columns: a column's result depends on
+// its own token alone, so columns without a token hold anything.  MXFP4 weights are widened in registers to bf16, which
+// is exact.  x is bf16; an activation goes between the launches in fp32 and enters the second product as three bf16
+// terms (its upper eight bits of mantissa, the next eight, the last eight), so that the output keeps fp32 accuracy.
+//
+// Loading the tokens' side costs as many accesses as the weights' where every step of 32 reduction indices has its own
+// load, most lanes of which have no token.  The narrow form gives an expert's tokens four at a time: one load has the
+// four steps of a unit in its 16 columns, and a step's fragment is that register shifted by DPP.  The wide form, for
+// more tokens an expert, has 16 at a time and a load a step.
 #include "activation.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -20,6 +26,8 @@ namespace {
 constexpr uint32_t kOut = 0x80000000u;  // a byte offset past every resource
 constexpr int kUnit = 128;              // reduction indices a wavefront loads at a time
 constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kTerms = 3;               // bf16 terms of an activation
+constexpr int kNarrow = 4, kWide = 16;  // tokens of an expert at a time
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -41,36 +49,63 @@ int max_entries(int T, int k, int E_loc, int batch) {
   const int rows = T * k, most = E_loc + rows / batch;
   return rows < most ? rows : most;
 }
-// (the device lays the arrays out for batches of 16, the smallest)
+// (the device lays the arrays out for the smallest batches)
+constexpr int kLeastBatch = kNarrow;
 size_t lists_bytes(int T, int k, int E_loc) {
-  return (size_t)E_loc * 12 + (size_t)(E_loc + T * k / 16) * 8 + (size_t)T * k * 16 + 32;
+  return (size_t)E_loc * 12 + (size_t)(E_loc + T * k / kLeastBatch) * 8 + (size_t)T * k * 16 + 32;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
+}
+// Reduction of a wavefront by DPP (rows of 16 lanes, then across them); every lane gets the result.
+template <typename F>
+__device__ __forceinline__ int wave_reduce(int v, int none, F f) {
+  v = f(v, dpp<0x111>(none, v));       // row_shr:1, 2, 4, 8
+  v = f(v, dpp<0x112>(none, v));
+  v = f(v, dpp<0x114>(none, v));
+  v = f(v, dpp<0x118>(none, v));
+  v = f(v, dpp<0x142, 0xa>(none, v));  // row_bcast:15 into rows 1 and 3
+  v = f(v, dpp<0x143, 0xc>(none, v));  // row_bcast:31 into rows 2 and 3
+  return __builtin_amdgcn_readlane(v, 63);
+}
+// Sums of lanes 0 .. l.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += dpp<0x111>(0, v);
+  v += dpp<0x112>(0, v);
+  v += dpp<0x114>(0, v);
+  v += dpp<0x118>(0, v);
+  v += dpp<0x142, 0xa>(0, v);
+  v += dpp<0x143, 0xc>(0, v);
   return v;
 }
+// A float's order as an int's.
+__device__ __forceinline__ int ordered(float f) {
+  const int b = __builtin_bit_cast(int, f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int b) { return __builtin_bit_cast(float, b ^ ((b >> 31) & 0x7fffffff)); }
 
 // Top-k of one row by one wavefront, as moe_route_topk does it: lane l holds logits l, l + 64, ...  Experts whose logit
 // is -inf or NaN are never chosen and have no part in a softmax's sum; +inf counts as the largest number.
 __device__ __forceinline__ void route_row(const float* row, int E, int k, bool renormalize, int32_t* idx, float* w) {
   constexpr int PL = 16;
+  constexpr int kNone = (int)0x80000000;  // below every number's key
   const int lane = threadIdx.x & 63, per = (E + 63) / 64;
-  const float ninf = -__builtin_inff();
-  float v[PL];
+  int v[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     if (i >= per) break;
     const int e = lane + i * 64;
-    const float l = e < E ? row[e] : ninf;
-    v[i] = l > ninf ? fminf(l, 3.402823466e38f) : ninf;
+    const float l = e < E ? row[e] : -__builtin_inff();
+    // (-0 and 0 are equal: adding 0 makes them the same)
+    v[i] = l > -__builtin_inff() ? ordered(fminf(l, 3.402823466e38f) + 0.0f) : kNone;
   }
   float top = 0.f, sum = 0.f, mine_v = 0.f, all = 0.f;
   int mine = -1;
   for (int j = 0; j < k; ++j) {
-    float best = ninf;
-    int id = 0x7fffffff;
+    int best = kNone, id = 0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       if (i >= per) break;
@@ -79,30 +114,30 @@ __device__ __forceinline__ void route_row(const float* row, int E, int k, bool r
         id = lane + i * 64;
       }
     }
-    const float m = wave_max(best);
-    if (!(m > ninf)) break;  // none left: this slot and those after it stay empty
+    const int m = wave_reduce(best, kNone, [](int a, int b) { return a > b ? a : b; });
+    if (m == kNone) break;  // none left: this slot and those after it stay empty
+    const float l = from_ordered(m);
     if (j == 0) {
-      top = m;
+      top = l;
       if (!renormalize) {
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
           if (i >= per) break;
-          if (v[i] > ninf) all += expf(v[i] - top);
+          if (v[i] != kNone) all += expf(from_ordered(v[i]) - top);
         }
       }
     }
-    int b = best == m ? id : 0x7fffffff;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      const int q = __shfl_xor(b, o);
-      b = q < b ? q : b;
-    }
+    // Equal logits: the lowest id.
+    const uint64_t holds = __ballot(best == m);
+    int b;
+    if ((holds & (holds - 1)) == 0) b = __builtin_amdgcn_readlane(id, __builtin_ctzll(holds));
+    else b = wave_reduce(best == m ? id : 0x7fffffff, 0x7fffffff, [](int a, int c) { return a < c ? a : c; });
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       if (i >= per) break;
-      if (b == lane + i * 64) v[i] = ninf;
+      if (b == lane + i * 64) v[i] = kNone;
     }
-    const float z = expf(m - top);
+    const float z = expf(l - top);
     sum += z;
     if (lane == j) {
       mine = b;
@@ -123,7 +158,7 @@ __device__ __forceinline__ void route_row(const float* row, int E, int k, bool r
 // Fills the lists; the whole workgroup takes part.  out: the workgroup that hands the routing's results out.
 template <int THREADS, int BATCH>
 __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logits, char* smem, bool out) {
-  const int pairs = a.T * a.k, entries = a.E_loc + pairs / 16;
+  const int pairs = a.T * a.k, entries = a.E_loc + pairs / kLeastBatch;
   Lists l;
   l.mask = reinterpret_cast<uint64_t*>(smem);
   l.first = reinterpret_cast<int32_t*>(l.mask + a.E_loc);
@@ -134,8 +169,10 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
   l.idx = reinterpret_cast<int32_t*>(l.gate + pairs);
   l.w = reinterpret_cast<float*>(l.idx + pairs);
   int32_t* total = reinterpret_cast<int32_t*>(l.w + pairs);
+  int32_t* twice = total + 1;  // some token's choice names an expert twice
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < a.E_loc; e += THREADS) l.mask[e] = 0;
+  if (tid == 0) *twice = 0;
   if (logits) {
     for (int t = wave; t < a.T; t += THREADS / 64)
       route_row(logits + (int64_t)t * a.E, a.E, a.k, a.renormalize, l.idx + t * a.k, l.w + t * a.k);
@@ -149,8 +186,10 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
   for (int p = tid; p < pairs; p += THREADS) {
     const int32_t id = l.idx[p];
     const uint32_t e = (uint32_t)id - (uint32_t)a.expert_begin;
-    if (id >= 0 && e < (uint32_t)a.E_loc)
-      atomicOr(reinterpret_cast<unsigned long long*>(l.mask + e), 1ull << (p / a.k));
+    if (id >= 0 && e < (uint32_t)a.E_loc) {
+      const unsigned long long bit = 1ull << (p / a.k);
+      if (atomicOr(reinterpret_cast<unsigned long long*>(l.mask + e), bit) & bit) *twice = 1;
+    }
     if (logits && out) {
       a.topk_idx[p] = id;
       a.topk_w[p] = l.w[p];
@@ -162,12 +201,7 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
     for (int e0 = 0; e0 < a.E_loc; e0 += 64) {
       const int e = e0 + lane;
       const int own = e < a.E_loc ? __popcll(l.mask[e]) : 0, parts = (own + BATCH - 1) / BATCH;
-      int c = own | parts << 16;  // running sums of both (rows <= 2048)
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int q = __shfl_up(c, o);
-        if (lane >= o) c += q;
-      }
+      const int c = wave_scan(own | parts << 16);  // running sums of both (rows <= 2048)
       const int r0 = rows + (c & 0xffff) - own, n0 = n + (c >> 16) - parts;
       if (e < a.E_loc) l.first[e] = r0;
       for (int i = 0; i < parts; ++i) {
@@ -175,7 +209,7 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
         l.entry[n0 + i] = (uint32_t)e | (uint32_t)(left < BATCH ? left : BATCH) << 16;
         l.row[n0 + i] = r0 + i * BATCH;
       }
-      const int last = __shfl(c, 63);
+      const int last = __builtin_amdgcn_readlane(c, 63);
       rows += last & 0xffff;
       n += last >> 16;
     }
@@ -183,16 +217,19 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
   }
   __syncthreads();
   // Each row's token and gate weight.  (A choice that names an expert twice has both weights in one row.)
+  const bool repeats = *twice != 0;
   for (int p = tid; p < pairs; p += THREADS) {
     const int32_t id = l.idx[p];
     const uint32_t e = (uint32_t)id - (uint32_t)a.expert_begin;
     if (id < 0 || e >= (uint32_t)a.E_loc) continue;
     const int t = p / a.k, end = (t + 1) * a.k;
-    bool again = false;
-    for (int q = t * a.k; q < p; ++q) again |= l.idx[q] == id;
-    if (again) continue;
     float w = l.w[p];
-    for (int q = p + 1; q < end; ++q) w += l.idx[q] == id ? l.w[q] : 0.f;
+    if (repeats) {
+      bool again = false;
+      for (int q = t * a.k; q < p; ++q) again |= l.idx[q] == id;
+      if (again) continue;
+      for (int q = p + 1; q < end; ++q) w += l.idx[q] == id ? l.w[q] : 0.f;
+    }
     const int r = l.first[e] + __popcll(l.mask[e] & ((1ull << t) - 1));
     l.token[r] = t;
     l.gate[r] = w;
@@ -202,32 +239,33 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
   return l;
 }
 
-// A unit of 16 weight rows: 128 reduction indices a row, as a lane holds them.
+// A unit of 16 weight rows: 128 reduction indices a row, as a lane holds them.  (Loads of 64 bytes a row, half a cache
+// line, that are not marked as streaming: the next unit's take the other half from the cache.  Marked, the bf16 layer
+// of 32 experts of 7168 x 2048 took 597 us instead of 524.)
 template <bool FP4>
 struct Weights;
 template <>
 struct Weights<false> {  // step s: indices 32 s + 8 (lane / 16) + 0..7 of row lane % 16
   u32x4 v[4];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t, uint32_t row, int K, int unit, bool in) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int K, int unit, bool in) {
     const int g = (threadIdx.x >> 4) & 3;
     const uint32_t at = row * (uint32_t)(K * 2) + unit * 256 + g * 16;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = __builtin_amdgcn_raw_buffer_load_b128(r, in ? at + s * 64 : kOut, 0, 2);
+    for (int s = 0; s < 4; ++s) v[s] = __builtin_amdgcn_raw_buffer_load_b128(r, in ? at + s * 64 : kOut, 0, 0);
   }
-  __device__ __forceinline__ bf16x8 get(int s) const { return __builtin_bit_cast(bf16x8, v[s]); }
+  __device__ __forceinline__ bf16x8 get(int s, uint32_t) const { return __builtin_bit_cast(bf16x8, v[s]); }
   static __device__ __forceinline__ uint32_t token_at(int unit, int s) { return unit * 256 + s * 64 + ((threadIdx.x >> 4) & 3) * 16; }
 };
 template <>
 struct Weights<true> {  // step s: indices 32 (lane / 16) + 8 s + 0..7 of row lane % 16: a lane has one block
   u32x4 v;
-  uint32_t s4;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t rs, uint32_t row, int K, int unit, bool in) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int K, int unit, bool in) {
     const int g = (threadIdx.x >> 4) & 3;
-    v = __builtin_amdgcn_raw_buffer_load_b128(r, in ? row * (uint32_t)(K / 2) + unit * 64 + g * 16 : kOut, 0, 2);
-    s4 = __builtin_amdgcn_raw_buffer_load_b32(rs, in ? row * (uint32_t)(K / 32) + unit * 4 : kOut, 0, 0);
+    v = __builtin_amdgcn_raw_buffer_load_b128(r, in ? row * (uint32_t)(K / 2) + unit * 64 + g * 16 : kOut, 0, 0);
   }
-  __device__ __forceinline__ bf16x8 get(int s) const {
-    const float scale = __builtin_bit_cast(float, ((s4 >> (8 * ((threadIdx.x >> 4) & 3))) & 255u) << 23);
+  // scales: the unit's four scale bytes of the row
+  __device__ __forceinline__ bf16x8 get(int s, uint32_t scales) const {
+    const float scale = __builtin_bit_cast(float, ((scales >> (8 * ((threadIdx.x >> 4) & 3))) & 255u) << 23);
     struct { bf16x2 p[4]; } o;
     o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[s], scale, 0);
     o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[s], scale, 1);
@@ -244,24 +282,61 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t codes_rsrc(const void* w, int6
   return make_rsrc(static_cast<const char*>(w) + row0 * b, rows * b);
 }
 
+// Units go in groups of four, whose scales, 16 bytes a row, come as one load: a load of four bytes a row for each unit
+// cost as many cache accesses as the codes (431 us instead of 310 without any for 64 experts of 7168 x 2048).
+constexpr int kGroup = 4;
+
+template <bool FP4, int M>
+struct GroupScales {
+  u32x4 v[M];
+};
+template <int M>
+struct GroupScales<false, M> {};
+
+// Columns i of each 16 get columns i + N.
+template <int N>
+__device__ __forceinline__ u32x4 shifted(u32x4 v) {
+  if constexpr (N == 0) return v;
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)dpp<0x100 + N>(0, (int)v[i]);  // row_shl:N
+  return o;
+}
+
+// Calls f with the steps 0..3 as constants.
+template <typename F>
+__device__ __forceinline__ void each_step(F f) {
+  f(std::integral_constant<int, 0>{});
+  f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{});
+}
+
 // ---------------------------------------------------------------------------
 // First launch
 // ---------------------------------------------------------------------------
-// An item is an entry's 16 R rows of the gate (and up) matrix; a workgroup's wavefronts share its reduction and add up
-// through LDS.  NB: blocks of 16 tokens of an entry.
-template <bool FP4, int NMAT, int NB>
-__global__ __launch_bounds__(kUpWaves * 64, NB == 1 ? 4 : 2) void up_kernel(FewArgs a) {
-  constexpr int R = FP4 ? 2 : 1, MR = NMAT * R, D = 2;
-  constexpr int RED = MR * NB * 256;
+// An item is an entry's 16 R rows of the gate (and up) matrix; a workgroup's wavefronts take turns at groups of its
+// reduction's units and add up through LDS.
+// Rows: fewer leave enough items for the CUs, more share a load of the tokens.
+constexpr int up_rows(bool fp4, bool wide) { return fp4 || wide ? 2 : 1; }
+// Workgroups a CU holds: as many as leave the registers that the loads in flight need.
+constexpr int up_per_cu(bool fp4, int nmat, bool wide) { return nmat == 2 && (wide || fp4) ? (wide && !fp4 ? 2 : 3) : 4 - wide; }
+
+template <bool FP4, int NMAT, bool WIDE>
+__global__ __launch_bounds__(kUpWaves * 64, up_per_cu(FP4, NMAT, WIDE)) void up_kernel(FewArgs a, bool zero) {
+  constexpr int R = up_rows(FP4, WIDE), MR = NMAT * R, D = 2, XL = WIDE ? 4 : 1;
+  constexpr int RED = MR * 256, STEP = kUpWaves * kGroup;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   float* red = reinterpret_cast<float*>(smem);
-  const Lists l = make_lists<kUpWaves * 64, 16 * NB>(a, a.logits, smem + kUpWaves * RED * 4, blockIdx.x == 0);
+  if (zero)  // the second launch adds to out
+    for (int i = blockIdx.x * (kUpWaves * 64) + threadIdx.x; i < a.T * a.H / 4; i += gridDim.x * (kUpWaves * 64))
+      reinterpret_cast<floatx4*>(a.out)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const Lists l = make_lists<kUpWaves * 64, WIDE ? kWide : kNarrow>(a, a.logits, smem + kUpWaves * RED * 4, blockIdx.x == 0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
+  const int l16 = lane & 15, g = lane >> 4, column = WIDE ? l16 : l16 & 3;
   const int blocks = a.F / (16 * R), items = l.n * blocks, units = a.H / kUnit;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (int64_t)a.T * a.H * 2);
-  uint16_t* hi = static_cast<uint16_t*>(a.ws);
-  uint16_t* lo = hi + (int64_t)a.T * a.k * a.F;
+  float* activations = static_cast<float*>(a.ws);
   const void* wp[2] = {a.w0, a.w0_up};
   const uint8_t* sp[2] = {a.s0, a.s0_up};
 
@@ -269,9 +344,7 @@ __global__ __launch_bounds__(kUpWaves * 64, NB == 1 ? 4 : 2) void up_kernel(FewA
     const int at = item / blocks, f0 = (item - at * blocks) * 16 * R;
     const uint32_t entry = (uint32_t)__builtin_amdgcn_readfirstlane((int)l.entry[at]);
     const int e = entry & 0xffff, n = entry >> 16, first = __builtin_amdgcn_readfirstlane(l.row[at]);
-    uint32_t xo[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) xo[b] = b * 16 + l16 < n ? (uint32_t)(l.token[first + b * 16 + l16] * a.H * 2) : kOut;
+    const uint32_t xo = column < n ? (uint32_t)(l.token[first + column] * a.H * 2) : kOut;
     const int64_t row0 = (int64_t)e * a.F + f0;
     __amdgpu_buffer_rsrc_t rw[NMAT], rs[NMAT];
 #pragma unroll
@@ -279,74 +352,66 @@ __global__ __launch_bounds__(kUpWaves * 64, NB == 1 ? 4 : 2) void up_kernel(FewA
       rw[m] = codes_rsrc<FP4>(wp[m], row0, 16 * R, a.H);
       rs[m] = FP4 ? make_rsrc(sp[m] + row0 * (a.H / 32), 16 * R * (a.H / 32)) : rw[m];
     }
-    floatx4 acc[MR][NB];
+    floatx4 acc[MR];
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) acc[m][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MR; ++m) acc[m] = floatx4{0.f, 0.f, 0.f, 0.f};
     Weights<FP4> w[D][MR];
-    u32x4 x[D][NB][4];
+    u32x4 x[D][XL];
     auto load = [&](int q, int u) {
       const bool in = u < units;
 #pragma unroll
-      for (int m = 0; m < MR; ++m) w[q][m].load(rw[m / R], rs[m / R], (m % R) * 16 + l16, a.H, u, in);
+      for (int m = 0; m < MR; ++m) w[q][m].load(rw[m / R], (m % R) * 16 + l16, a.H, u, in);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          x[q][b][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo[b] + Weights<FP4>::token_at(u, s) : kOut, 0, 0);
+      for (int s = 0; s < XL; ++s)
+        x[q][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo + Weights<FP4>::token_at(u, WIDE ? s : l16 >> 2) : kOut, 0, 0);
     };
+    GroupScales<FP4, MR> sc, next;
+    auto load_scales = [&](GroupScales<FP4, MR>& v, int u) {  // (may run into the next row's, which no unit uses)
+      if constexpr (FP4)
 #pragma unroll
-    for (int q = 0; q < D; ++q) load(q, wave + q * kUpWaves);
-    for (int u = wave; u < units; u += D * kUpWaves) {
+        for (int m = 0; m < MR; ++m)
+          v.v[m] = __builtin_amdgcn_raw_buffer_load_b128(
+              rs[m / R], u < units ? (uint32_t)(((m % R) * 16 + l16) * (a.H / 32) + u * 4) : kOut, 0, 0);
+    };
+    load_scales(next, wave * kGroup);
 #pragma unroll
-      for (int q = 0; q < D; ++q) {
+    for (int q = 0; q < D; ++q) load(q, wave * kGroup + q);
+    for (int u = wave * kGroup; u < units; u += STEP) {
+      sc = next;
+      load_scales(next, u + STEP);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+      for (int j = 0; j < kGroup; ++j) {
+        each_step([&](auto step) {
+          constexpr int S = decltype(step)::value;
+          const bf16x8 t = __builtin_bit_cast(bf16x8, WIDE ? x[j % D][WIDE ? S : 0] : shifted<WIDE ? 0 : 4 * S>(x[j % D][0]));
 #pragma unroll
           for (int m = 0; m < MR; ++m) {
-            const bf16x8 f = w[q][m].get(s);
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              acc[m][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, x[q][b][s]), acc[m][b], 0, 0, 0);
+            uint32_t scales = 0;  // (past the row's end the codes are zeros, and so is their scale)
+            if constexpr (FP4) scales = u + j < units ? sc.v[m][j] : 0;
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j % D][m].get(S, scales), t, acc[m], 0, 0, 0);
           }
-        load(q, u + (q + D) * kUpWaves);
+        });
+        load(j % D, j + D < kGroup ? u + j + D : u + STEP + j + D - kGroup);
       }
     }
     __syncthreads();  // (the last item's sums have been read)
 #pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) *reinterpret_cast<floatx4*>(red + wave * RED + (m * NB + b) * 256 + lane * 4) = acc[m][b];
+    for (int m = 0; m < MR; ++m) *reinterpret_cast<floatx4*>(red + wave * RED + m * 256 + lane * 4) = acc[m];
     __syncthreads();
-    // Lane: row l16 of a block of 16 of the entry's, weight rows 4 g + 0..3 of a block of 16.
-    for (int q = wave; q < R * NB; q += kUpWaves) {
-      const int r = q / NB, b = q % NB, p = b * 16 + l16;
+    // Lane: the entry's row l16, weight rows 4 g + 0..3 of a block of 16.
+    for (int r = wave; r < R; r += kUpWaves) {
       floatx4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
 #pragma unroll
       for (int v = 0; v < kUpWaves; ++v) {
-        z += *reinterpret_cast<const floatx4*>(red + v * RED + (r * NB + b) * 256 + lane * 4);
-        if (NMAT == 2) u += *reinterpret_cast<const floatx4*>(red + v * RED + ((R + r) * NB + b) * 256 + lane * 4);
+        z += *reinterpret_cast<const floatx4*>(red + v * RED + r * 256 + lane * 4);
+        if (NMAT == 2) u += *reinterpret_cast<const floatx4*>(red + v * RED + (R + r) * 256 + lane * 4);
       }
-      if (p < n) {
-        const float gate = l.gate[first + p];
-        u32x2 h, m;
+      if (l16 < n) {
+        const float gate = l.gate[first + l16];
+        floatx4 y;
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          uint16_t hh[2], ll[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float y = (NMAT == 2 ? activate(ACT_SILU, z[i + c]) * u[i + c] : activate(ACT_GELU, z[i + c])) * gate;
-            hh[c] = f2bf_bits(y);
-            const float d = y - bf2f(hh[c]);
-            ll[c] = fabsf(d) < __builtin_inff() ? f2bf_bits(d) : 0;  // (an infinity or NaN is all in the first term)
-          }
-          h[i >> 1] = (uint32_t)hh[0] | (uint32_t)hh[1] << 16;
-          m[i >> 1] = (uint32_t)ll[0] | (uint32_t)ll[1] << 16;
-        }
-        const int64_t o = (int64_t)(first + p) * a.F + f0 + r * 16 + g * 4;
-        *reinterpret_cast<u32x2*>(hi + o) = h;
-        *reinterpret_cast<u32x2*>(lo + o) = m;
+        for (int i = 0; i < 4; ++i) y[i] = (NMAT == 2 ? activate(ACT_SILU, z[i]) * u[i] : activate(ACT_GELU, z[i])) * gate;
+        *reinterpret_cast<floatx4*>(activations + (int64_t)(first + l16) * a.F + f0 + r * 16 + g * 4) = y;
       }
     }
   }
@@ -355,85 +420,157 @@ __global__ __launch_bounds__(kUpWaves * 64, NB == 1 ? 4 : 2) void up_kernel(FewA
 // ---------------------------------------------------------------------------
 // Second launch
 // ---------------------------------------------------------------------------
-// A workgroup has 16 R output columns of every token.  Its wavefronts take turns at units of the entries' reductions and
-// add each unit's sums to the tokens' in LDS, a copy for each wavefront, so that the order of additions is fixed.
-template <bool FP4, int NB, int R>
-__global__ __launch_bounds__(kDownWaves * 64, NB == 1 ? 4 : 2) void down_kernel(FewArgs a) {
-  constexpr int D = 2, PITCH = 16 * R + 4;
+// Eight activations as three bf16 terms whose sum they are.  (An infinity or NaN is all in its first term.)
+struct Terms {
+  u32x4 t[kTerms];
+};
+__device__ __forceinline__ Terms split(floatx4 lo, floatx4 hi) {
+  Terms o;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    float a[2] = {i < 4 ? lo[i & 3] : hi[i & 3], i < 4 ? lo[(i & 3) + 1] : hi[(i & 3) + 1]};
+#pragma unroll
+    for (int c = 0; c < kTerms; ++c) {
+      const uint32_t b0 = __builtin_bit_cast(uint32_t, a[0]), b1 = __builtin_bit_cast(uint32_t, a[1]);
+      o.t[c][i >> 1] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);  // the upper halves
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float d = a[e] - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, a[e]) & 0xffff0000u);
+        a[e] = c == 0 && !(fabsf(a[e]) < __builtin_inff()) ? 0.f : d;
+      }
+    }
+  }
+  return o;
+}
+
+// The narrow form's fragment of step S: columns 4 c + p are term c of row p, from columns 4 S + p.
+template <int S, int C>
+__device__ __forceinline__ void place_term(u32x4& o, u32x4 t) {
+  constexpr int by = 4 * (S - C), ctrl = by == 0 ? 0xE4 : by > 0 ? 0x100 + by : 0x110 - by;  // quad_perm 0123, row_shl, row_shr
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)o[i], (int)t[i], ctrl, 0xf, 1 << C, false);
+}
+
+// A workgroup has 16 R output columns of every token, of all units or (S = 2) of half of them; its wavefronts take turns
+// at the entries' groups of units, and each adds each group's sums to the tokens' in LDS, a copy for each wavefront, so
+// that the order of additions is fixed.  With S = 2 the two workgroups add to out, which the first launch has cleared:
+// two terms make the same sum in either order.
+constexpr int down_rows(bool fp4) { return fp4 ? 2 : 1; }
+
+template <bool FP4, bool WIDE>
+__global__ __launch_bounds__(kDownWaves * 64, WIDE ? 2 : 4) void down_kernel(FewArgs a, int S) {
+  constexpr int R = down_rows(FP4), D = 2, G = kGroup, PITCH = 16 * R + 4, XL = WIDE ? 4 : 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   float* sums = reinterpret_cast<float*>(smem);  // [wavefront][token][PITCH]
   const int each = a.T * PITCH;
   for (int i = threadIdx.x; i < kDownWaves * each / 4; i += kDownWaves * 64)
     reinterpret_cast<floatx4*>(sums)[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const Lists l = make_lists<kDownWaves * 64, 16 * NB>(a, nullptr, smem + kDownWaves * each * 4, false);
+  const Lists l = make_lists<kDownWaves * 64, WIDE ? kWide : kNarrow>(a, nullptr, smem + kDownWaves * each * 4, false);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
-  const int h0 = blockIdx.x * 16 * R, per = a.F / kUnit, units = l.n * per;
-  const uint16_t* hi = static_cast<const uint16_t*>(a.ws);
-  const int64_t terms = (int64_t)a.T * a.k * a.F;
+  const int l16 = lane & 15, g = lane >> 4, column = WIDE ? l16 : l16 & 3;
+  const int h0 = (int)(blockIdx.x / S) * 16 * R, per = a.F / kUnit, pg = (per + G - 1) / G;
+  const int part = (int)(blockIdx.x % S), g0 = (int)((int64_t)part * l.n * pg / S), g1 = (int)((int64_t)(part + 1) * l.n * pg / S);
+  const float* activations = static_cast<const float*>(a.ws);
   float* mine = sums + wave * each;
 
-  struct Unit {
-    Weights<FP4> w[R];
-    u32x4 hi[NB][4], lo[NB][4];
-    int token[NB];  // of this lane's column, -1: none
+  struct Group {
+    __amdgpu_buffer_rsrc_t rw, rs, rt;
+    uint32_t off;  // of this lane's activation row
+    int unit, n, first;
   };
-  Unit q[D];
-  auto load = [&](Unit& v, int u) {
-    const bool in = u < units;
-    const int at = in ? u / per : 0, kf = in ? u - at * per : 0;
+  auto group = [&](int i) {
+    Group v;
+    const bool in = i < g1;
+    const int at = in ? i / pg : 0;
     const uint32_t entry = in ? (uint32_t)__builtin_amdgcn_readfirstlane((int)l.entry[at]) : 0;
-    const int e = entry & 0xffff, n = entry >> 16, first = in ? __builtin_amdgcn_readfirstlane(l.row[at]) : 0;
+    const int e = entry & 0xffff;
+    v.n = entry >> 16;
+    v.first = in ? __builtin_amdgcn_readfirstlane(l.row[at]) : 0;
+    v.unit = in ? (i - at * pg) * G : per;  // (units from `per` on load from past the resources)
     const int64_t row0 = (int64_t)e * a.H + h0;
-    const __amdgpu_buffer_rsrc_t rw = codes_rsrc<FP4>(a.w1, row0, 16 * R, a.F);
-    const __amdgpu_buffer_rsrc_t rs = FP4 ? make_rsrc(a.s1 + row0 * (a.F / 32), 16 * R * (a.F / 32)) : rw;
-#pragma unroll
-    for (int r = 0; r < R; ++r) v.w[r].load(rw, rs, r * 16 + l16, a.F, kf, in);
-    const __amdgpu_buffer_rsrc_t rh = make_rsrc(hi + (int64_t)first * a.F, (int64_t)n * a.F * 2);
-    const __amdgpu_buffer_rsrc_t rl = make_rsrc(hi + terms + (int64_t)first * a.F, (int64_t)n * a.F * 2);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int p = b * 16 + l16;
-      v.token[b] = p < n ? l.token[first + p] : -1;
-      const uint32_t o = p < n ? (uint32_t)(p * a.F * 2) : kOut;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        v.hi[b][s] = __builtin_amdgcn_raw_buffer_load_b128(rh, o + Weights<FP4>::token_at(kf, s), 0, 0);
-        v.lo[b][s] = __builtin_amdgcn_raw_buffer_load_b128(rl, o + Weights<FP4>::token_at(kf, s), 0, 0);
-      }
-    }
+    v.rw = codes_rsrc<FP4>(a.w1, row0, 16 * R, a.F);
+    v.rs = FP4 ? make_rsrc(a.s1 + row0 * (a.F / 32), 16 * R * (a.F / 32)) : v.rw;
+    v.rt = make_rsrc(activations + (int64_t)v.first * a.F, (int64_t)v.n * a.F * 4);
+    v.off = column < v.n ? (uint32_t)(column * a.F * 4) : kOut;
+    return v;
   };
-  auto multiply = [&](const Unit& v) {
-    floatx4 acc[R][NB];
+  Weights<FP4> w[D][R];
+  floatx4 x[D][XL][2];
+  auto load = [&](int q, const Group& v, int j) {  // the group's j-th unit
+    const int u = v.unit + j;
+    const bool in = u < per;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) w[q][r].load(v.rw, r * 16 + l16, a.F, u, in);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[r][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < XL; ++s)
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+      for (int h = 0; h < 2; ++h)
+        x[q][s][h] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(
+                         v.rt, in ? v.off + 2 * Weights<FP4>::token_at(u, WIDE ? s : l16 >> 2) + 16 * h : kOut, 0, 0));
+  };
+  auto load_scales = [&](GroupScales<FP4, R>& s, const Group& v) {
+    if constexpr (FP4)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bf16x8 f = v.w[r].get(s);
+      for (int r = 0; r < R; ++r)
+        s.v[r] = __builtin_amdgcn_raw_buffer_load_b128(
+            v.rs, v.unit < per ? (uint32_t)((r * 16 + l16) * (a.F / 32) + v.unit * 4) : kOut, 0, 0);
+  };
+  GroupScales<FP4, R> sc, next;
+  Group cur = group(g0 + wave);
+  load_scales(next, cur);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, v.hi[b][s]), acc[r][b], 0, 0, 0);
-          acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, v.lo[b][s]), acc[r][b], 0, 0, 0);
+  for (int q = 0; q < D; ++q) load(q, cur, q);
+  for (int i = g0 + wave; i < g1; i += kDownWaves) {
+    const Group ahead = group(i + kDownWaves);
+    sc = next;
+    load_scales(next, ahead);
+    floatx4 acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      Terms t;
+      if constexpr (!WIDE) t = split(x[j % D][0][0], x[j % D][0][1]);
+      each_step([&](auto step) {
+        constexpr int T = decltype(step)::value;
+        if constexpr (WIDE) {
+          t = split(x[j % D][T][0], x[j % D][T][1]);
         }
-      }
+        u32x4 b = {0, 0, 0, 0};
+        if constexpr (!WIDE) {
+          place_term<T, 0>(b, t.t[0]);
+          place_term<T, 1>(b, t.t[1]);
+          place_term<T, 2>(b, t.t[2]);
+        }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (v.token[b] >= 0)
+        for (int r = 0; r < R; ++r) {
+          uint32_t scales = 0;
+          if constexpr (FP4) scales = cur.unit + j < per ? sc.v[r][j] : 0;
+          const bf16x8 f = w[j % D][r].get(T, scales);
+          if constexpr (WIDE) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) *reinterpret_cast<floatx4*>(mine + v.token[b] * PITCH + r * 16 + g * 4) += acc[r][b];
-  };
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(q[d], wave + d * kDownWaves);
-  for (int u = wave; u < units; u += D * kDownWaves) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      multiply(q[d]);
-      load(q[d], u + (d + D) * kDownWaves);
+            for (int c = 0; c < kTerms; ++c)
+              acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, t.t[c]), acc[r], 0, 0, 0);
+          } else {
+            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, b), acc[r], 0, 0, 0);
+          }
+        }
+      });
+      if (j + D < G) load(j % D, cur, j + D);
+      else load(j % D, ahead, j + D - G);
     }
+    const int token = l16 < cur.n ? l.token[cur.first + l16] : 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      floatx4 t = acc[r];
+      if constexpr (!WIDE) {  // the terms' columns, smallest first
+        const u32x4 bits = __builtin_bit_cast(u32x4, t);
+        t = __builtin_bit_cast(floatx4, shifted<8>(bits)) + __builtin_bit_cast(floatx4, shifted<4>(bits)) + t;
+      }
+      if (l16 < cur.n) *reinterpret_cast<floatx4*>(mine + token * PITCH + r * 16 + g * 4) += t;
+    }
+    cur = ahead;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * 4 * R; i += kDownWaves * 64) {
@@ -441,7 +578,13 @@ __global__ __launch_bounds__(kDownWaves * 64, NB == 1 ? 4 : 2) void down_kernel(
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < kDownWaves; ++v) o += *reinterpret_cast<const floatx4*>(sums + v * each + t * PITCH + c);
-    *reinterpret_cast<floatx4*>(a.out + (int64_t)t * a.H + h0 + c) = o;
+    float* to = a.out + (int64_t)t * a.H + h0 + c;
+    if (S == 1) {
+      *reinterpret_cast<floatx4*>(to) = o;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) unsafeAtomicAdd(to + v, o[v]);
+    }
   }
 }
 
@@ -452,22 +595,27 @@ int cu_count() {
   return n;
 }
 
-template <bool FP4, int NB>
-hipError_t launch(const FewArgs& a, hipStream_t s) {
-  constexpr int R = FP4 ? 2 : 1, R2 = FP4 ? 2 : 1;
-  const bool dual = a.w0_up != nullptr;
+template <bool FP4, int NMAT, bool WIDE>
+hipError_t launch_both(const FewArgs& a, hipStream_t s) {
+  constexpr int R = up_rows(FP4, WIDE), R2 = down_rows(FP4);
   const size_t lists = lists_bytes(a.T, a.k, a.E_loc);
-  const int64_t items = (int64_t)max_entries(a.T, a.k, a.E_loc, 16 * NB) * (a.F / (16 * R));
-  const int64_t most = (int64_t)cu_count() * 4;
-  const dim3 grid((unsigned)(items < most ? items : most));
-  const size_t red = (size_t)kUpWaves * (dual ? 2 : 1) * R * NB * 1024;
-  if (dual) hipLaunchKernelGGL((up_kernel<FP4, 2, NB>), grid, dim3(kUpWaves * 64), red + lists, s, a);
-  else hipLaunchKernelGGL((up_kernel<FP4, 1, NB>), grid, dim3(kUpWaves * 64), red + lists, s, a);
-  hipError_t e = hipGetLastError();
+  const int cus = cu_count();
+  // Too few column blocks for two workgroups a CU: half of the reduction each.
+  const int columns = a.H / (16 * R2), S = columns < 2 * cus ? 2 : 1;
+  const int64_t items = (int64_t)max_entries(a.T, a.k, a.E_loc, WIDE ? kWide : kNarrow) * (a.F / (16 * R));
+  const int64_t most = (int64_t)cus * up_per_cu(FP4, NMAT, WIDE);
+  hipLaunchKernelGGL((up_kernel<FP4, NMAT, WIDE>), dim3((unsigned)(items < most ? items : most)), dim3(kUpWaves * 64),
+                     (size_t)kUpWaves * NMAT * R * 1024 + lists, s, a, S == 2);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t sums = (size_t)kDownWaves * a.T * (16 * R2 + 4) * 4;
-  hipLaunchKernelGGL((down_kernel<FP4, NB, R2>), dim3((unsigned)(a.H / (16 * R2))), dim3(kDownWaves * 64), sums + lists, s, a);
+  hipLaunchKernelGGL((down_kernel<FP4, WIDE>), dim3((unsigned)(columns * S)), dim3(kDownWaves * 64),
+                     (size_t)kDownWaves * a.T * (16 * R2 + 4) * 4 + lists, s, a, S);
   return hipGetLastError();
+}
+
+template <bool FP4, bool WIDE>
+hipError_t launch(const FewArgs& a, hipStream_t s) {
+  return a.w0_up ? launch_both<FP4, 2, WIDE>(a, s) : launch_both<FP4, 1, WIDE>(a, s);
 }
 
 }  // namespace
@@ -475,9 +623,10 @@ hipError_t launch(const FewArgs& a, hipStream_t s) {
 size_t few_tokens_ws_bytes(int T, int k, int F) { return (size_t)T * k * F * 4; }
 
 hipError_t launch_few_tokens(const FewArgs& a, hipStream_t s) {
-  const bool wide = a.T > 16 && a.T * a.k > 8 * a.E;
-  if (a.s0) return wide ? launch<true, 2>(a, s) : launch<true, 1>(a, s);
-  return wide ? launch<false, 2>(a, s) : launch<false, 1>(a, s);
+  // The wide form where experts have more than three tokens on average.
+  const bool wide = a.T > kNarrow && a.T * a.k > 3 * a.E;
+  if (a.s0) return wide ? launch<true, true>(a, s) : launch<true, false>(a, s);
+  return wide ? launch<false, true>(a, s) : launch<false, false>(a, s);
 }
 
 }  // namespace moe
