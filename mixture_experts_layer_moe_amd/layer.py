@@ -10,7 +10,12 @@ the grouped FFN and the combine run as one launch with tile-level signals
 (moe_ffn_combine_fused; 256-row tiles).  With a Gating the tokens are routed
 by moe_route_grouped instead of moe_route_topk; with a SharedExpert every token
 also goes through a dense FFN (two moe_linear calls) whose down product is
-added to the combined output.
+added to the combined output.  With experts in MXFP4 (ffi.Mxfp4 weights) the
+tokens and the activations are quantised too and the grouped FFN is two
+moe_grouped_linear_mxfp4 calls; a SharedExpert in MXFP4 runs the same way on
+moe_linear_mxfp4.  With few_tokens=True, for at most 64 tokens, routing,
+experts and combine are one moe_few_tokens call over bf16 or MXFP4 experts,
+whose activations stay in full precision.
 """
 from __future__ import annotations
 
@@ -20,6 +25,7 @@ from typing import Optional
 import torch
 
 from . import ffi
+from .ffi import Mxfp4, Weight
 from .workloads import MoEConfig
 
 
@@ -36,21 +42,35 @@ class Gating:
 
 @dataclass
 class SharedExpert:
-    """A dense FFN of the layer's activation that every token goes through (bf16, output-major).
+    """A dense FFN of the layer's activation that every token goes through (output-major; bf16, or all in MXFP4).
 
     Where several GPUs' outputs are summed (shares of the experts), one of them has it.
     """
-    w0: torch.Tensor               # [F_s, H]: W_gate^T (SwiGLU) or W1^T (GELU)
-    w0_up: Optional[torch.Tensor]  # [F_s, H]: W_up^T (SwiGLU only)
-    w1: torch.Tensor               # [H, F_s]
+    w0: Weight               # [F_s, H]: W_gate^T (SwiGLU) or W1^T (GELU)
+    w0_up: Optional[Weight]  # [F_s, H]: W_up^T (SwiGLU only)
+    w1: Weight               # [H, F_s]
+
+
+def _all_mxfp4(what: str, *weights) -> bool:
+    """Whether the weights are in MXFP4: all of them or none."""
+    mx = {isinstance(w, Mxfp4) for w in weights if w is not None}
+    if len(mx) > 1:
+        raise ValueError(f"{what} must all be in MXFP4, or none")
+    return mx == {True}
 
 
 class MoELayer:
     def __init__(self, cfg: MoEConfig, x: torch.Tensor, logits: torch.Tensor,
-                 src_rank: Optional[torch.Tensor], w0: torch.Tensor, w0_up: Optional[torch.Tensor],
-                 w1: torch.Tensor, tile_m: Optional[int] = None, renormalize: bool = True,
+                 src_rank: Optional[torch.Tensor], w0: Weight, w0_up: Optional[Weight],
+                 w1: Weight, tile_m: Optional[int] = None, renormalize: bool = True,
                  fused_gather: bool = False, signalled: bool = False,
-                 gating: Optional[Gating] = None, shared: Optional[SharedExpert] = None):
+                 gating: Optional[Gating] = None, shared: Optional[SharedExpert] = None,
+                 few_tokens: bool = False):
+        self.mxfp4 = _all_mxfp4("the experts' weights", w0, w0_up, w1)
+        if signalled and (self.mxfp4 or few_tokens):
+            raise ValueError("signalled runs bf16 experts, and not the form for a few tokens")
+        if few_tokens and (fused_gather or cfg.T > ffi.FEW_TOKENS):
+            raise ValueError(f"few_tokens takes at most {ffi.FEW_TOKENS} tokens, and permutes none")
         if shared is not None:
             Fs = shared.w0.shape[0]
             if (shared.w0_up is not None) != (cfg.act == "swiglu"):
@@ -59,9 +79,11 @@ class MoELayer:
                                 ("w1", shared.w1, (cfg.H, Fs))):
                 if t is not None and t.shape != shape:
                     raise ValueError(f"shared.{n} must have shape {shape}, got {tuple(t.shape)}")
+            self.shared_mxfp4 = _all_mxfp4("the shared expert's weights", shared.w0, shared.w0_up, shared.w1)
         self.cfg = cfg
         self.gating, self.shared = gating, shared
-        self.fused_gather = fused_gather
+        self.few_tokens = few_tokens
+        self.fused_gather = fused_gather or self.mxfp4  # (quantised tokens are gathered by their product)
         self.signalled = signalled
         self.tile_m = tile_m or cfg.tile_m
         self.renormalize = renormalize
@@ -71,19 +93,28 @@ class MoELayer:
         T, H, k, El = cfg.T, cfg.H, cfg.k, cfg.n_local
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        self.perm = ffi.alloc_permuted(T, H, k, El, self.tile_m, dev, rows=not fused_gather)
-        nbytes = ffi.permute_workspace_bytes(T, k, El, cfg.num_ranks)
-        self.ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        self.act_buf = torch.empty((self.perm.R_cap, cfg.F_loc), dtype=torch.bfloat16, device=dev)
-        self.y_perm = torch.empty((self.perm.R_cap, H), dtype=torch.float32, device=dev)
-        ffn_bytes = ffi.grouped_ffn_workspace_bytes(self.tile_m, H)
-        self.ffn_ws = torch.empty(ffn_bytes, dtype=torch.uint8, device=dev) if ffn_bytes else None
         self.out = torch.empty((T, H), dtype=torch.float32, device=dev)
-        self.fused_ws = ffi.alloc_fused_workspace(self.perm.tiles_cap, H, dev) if signalled else None
+        if few_tokens:
+            self.few_ws = ffi.alloc_few_tokens_workspace(T, k, cfg.F_loc, dev)
+        else:
+            self.perm = ffi.alloc_permuted(T, H, k, El, self.tile_m, dev, rows=not self.fused_gather)
+            nbytes = ffi.permute_workspace_bytes(T, k, El, cfg.num_ranks)
+            self.ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+            self.act_buf = torch.empty((self.perm.R_cap, cfg.F_loc), dtype=torch.bfloat16, device=dev)
+            self.y_perm = torch.empty((self.perm.R_cap, H), dtype=torch.float32, device=dev)
+            ffn_bytes = 0 if self.mxfp4 else ffi.grouped_ffn_workspace_bytes(self.tile_m, H)
+            self.ffn_ws = torch.empty(ffn_bytes, dtype=torch.uint8, device=dev) if ffn_bytes else None
+            self.fused_ws = ffi.alloc_fused_workspace(self.perm.tiles_cap, H, dev) if signalled else None
+            if self.mxfp4:
+                self.act_q = ffi.alloc_mxfp4(self.act_buf.shape, dev)
+        quantized = (self.mxfp4 and not few_tokens) or (shared is not None and self.shared_mxfp4)
+        self.x_q = ffi.alloc_mxfp4((T, H), dev) if quantized else None
         if shared is not None:
             self.shared_h = torch.empty((T, Fs), dtype=torch.bfloat16, device=dev)
-            self.shared_ws = [ffi.alloc_linear_workspace(T, Fs, H, cfg.act, dev),
-                              ffi.alloc_linear_workspace(T, H, Fs, "none", dev)]
+            alloc = ffi.alloc_linear_mxfp4_workspace if self.shared_mxfp4 else ffi.alloc_linear_workspace
+            self.shared_ws = [alloc(T, Fs, H, cfg.act, dev), alloc(T, H, Fs, "none", dev)]
+            if self.shared_mxfp4:
+                self.shared_q = ffi.alloc_mxfp4((T, Fs), dev)
 
     @classmethod
     def from_inputs(cls, cfg: MoEConfig, inputs: dict, **kw) -> "MoELayer":
@@ -105,8 +136,17 @@ class MoELayer:
                         c.num_ranks, self.tile_m, out=self.perm, ws=self.ws, stream=stream,
                         copy_rows=not self.fused_gather)
 
+    def quantize_tokens(self, stream=None):
+        """The tokens in MXFP4, for experts or a shared expert in MXFP4."""
+        ffi.moe_mxfp4_quantize(self.x, out=self.x_q, stream=stream)
+
     def ffn(self, stream=None):
-        if self.fused_gather:
+        if self.mxfp4:  # (rows behind an expert's last token are quantised as they lie and belong to no product)
+            ffi.moe_grouped_linear_mxfp4(self.perm, self.x_q, self.w0, w_up=self.w0_up, act=self.cfg.act, gather=True,
+                                         out=self.act_buf, stream=stream)
+            ffi.moe_mxfp4_quantize(self.act_buf, out=self.act_q, stream=stream)
+            ffi.moe_grouped_linear_mxfp4(self.perm, self.act_q, self.w1, out=self.y_perm, stream=stream)
+        elif self.fused_gather:
             ffi.moe_grouped_ffn_gather(self.x, self.perm, self.w0, self.w0_up, self.w1, self.cfg.act,
                                        self.act_buf, self.y_perm, self.ffn_ws, stream, use_workspace=False)
         else:
@@ -124,19 +164,40 @@ class MoELayer:
     def shared_expert(self, stream=None):
         """The shared expert's FFN, added to the combined output."""
         s = self.shared
+        if self.shared_mxfp4:
+            ffi.moe_linear_mxfp4(self.x_q, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, ws=self.shared_ws[0],
+                                 stream=stream, use_workspace=False)
+            ffi.moe_mxfp4_quantize(self.shared_h, out=self.shared_q, stream=stream)
+            ffi.moe_linear_mxfp4(self.shared_q, s.w1, residual=self.out, out=self.out, ws=self.shared_ws[1],
+                                 stream=stream, use_workspace=False)
+            return
         ffi.moe_linear(self.x, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, ws=self.shared_ws[0],
                        stream=stream, use_workspace=False)
         ffi.moe_linear(self.shared_h, s.w1, residual=self.out, out=self.out, ws=self.shared_ws[1], stream=stream,
                        use_workspace=False)
 
+    def few(self, stream=None):
+        """Experts and combine, and the routing where no Gating does it, in one call for a few tokens."""
+        c = self.cfg
+        ffi.moe_few_tokens(self.x, self.w0, self.w0_up, self.w1, c.act, logits=None if self.gating else self.logits,
+                           renormalize=self.renormalize, topk_idx=self.topk_idx, topk_w=self.topk_w,
+                           expert_begin=c.expert_begin, num_experts=c.E, out=self.out, ws=self.few_ws, stream=stream)
+
     def run(self, stream=None) -> torch.Tensor:
-        self.route(stream)
-        self.permute(stream)
-        if self.signalled:
-            self.ffn_combine(stream)
+        if self.x_q is not None:
+            self.quantize_tokens(stream)
+        if self.few_tokens:
+            if self.gating is not None:
+                self.route(stream)
+            self.few(stream)
         else:
-            self.ffn(stream)
-            self.combine(stream)
+            self.route(stream)
+            self.permute(stream)
+            if self.signalled:
+                self.ffn_combine(stream)
+            else:
+                self.ffn(stream)
+                self.combine(stream)
         if self.shared is not None:
             self.shared_expert(stream)
         return self.out
