@@ -71,35 +71,66 @@ __device__ __forceinline__ Rows rows_of(const Product& p, int ti, int bm) {
 // ---------------------------------------------------------------------------
 // Epilogue
 // ---------------------------------------------------------------------------
+// V values side by side, at any alignment their type allows (rows of odd lengths), `left` of which exist.
 template <int V>
-__device__ __forceinline__ void load_bias(const float* b, int left, bool whole, float (&v)[V]) {
-  if (whole) {
+using words = uint32_t __attribute__((__vector_size__(V * 4)));
+
+template <int V, bool F32>
+__device__ __forceinline__ void load_values(const void* p, int64_t at, int left, float (&v)[V]) {
+  if (left >= V) {
+    if constexpr (F32) {
+      typedef words<4> quad __attribute__((aligned(4)));
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const floatx4 q = *reinterpret_cast<const floatx4*>(b + i);
+      for (int i = 0; i < V; i += 4) {
+        const words<4> q = *reinterpret_cast<const quad*>(static_cast<const float*>(p) + at + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i + e] = q[e];
+        for (int e = 0; e < 4; ++e) v[i + e] = __builtin_bit_cast(float, (uint32_t)q[e]);
+      }
+    } else {
+      typedef words<V / 2> halves __attribute__((aligned(2)));
+      const words<V / 2> q = *reinterpret_cast<const halves*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = bf2f((uint16_t)(q[e >> 1] >> (16 * (e & 1))));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = 0.f;
+      if (i < left) v[i] = F32 ? static_cast<const float*>(p)[at + i] : bf2f(static_cast<const uint16_t*>(p)[at + i]);
+    }
+  }
+}
+
+template <int V, bool F32>
+__device__ __forceinline__ void store_values(void* p, int64_t at, int left, const float (&v)[V]) {
+  if (left >= V) {
+    if constexpr (F32) {
+      typedef words<4> quad __attribute__((aligned(4)));
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<quad*>(static_cast<float*>(p) + at + i) =
+            __builtin_bit_cast(words<4>, floatx4{v[i], v[i + 1], v[i + 2], v[i + 3]});
+    } else {
+      typedef words<V / 2> halves __attribute__((aligned(2)));
+      words<V / 2> h;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) h[e] = (uint32_t)f2bf_bits(v[2 * e]) | ((uint32_t)f2bf_bits(v[2 * e + 1]) << 16);
+      *reinterpret_cast<halves*>(static_cast<uint16_t*>(p) + at) = h;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < left) v[i] = b[i];
+      if (i < left) {
+        if (F32) static_cast<float*>(p)[at + i] = v[i];
+        else static_cast<uint16_t*>(p)[at + i] = f2bf_bits(v[i]);
+      }
   }
 }
 
-// V values of one row from column n: bias, activation, residual, rounding, stores.  `at` is the element's index in out.
+// Activations of V columns: z (and u) are the sums, bz and bu the biases.
 template <int V>
-__device__ __forceinline__ void finish(const MxLinearArgs& a, int64_t at, int n, float (&z)[V], const float (&u)[V]) {
-  constexpr int W = V < 8 ? V : 8;  // bf16 values per access
-  const int left = a.N - n;         // columns that exist
-  if (left <= 0) return;
-  const bool whole = left >= V && a.N % 8 == 0;  // (then every row's groups of V are 16-byte aligned)
-  float bz[V], bu[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) bz[i] = bu[i] = 0.f;
-  if (a.bias) load_bias<V>(a.bias + n, left, whole, bz);
-  if (a.bias_up) load_bias<V>(a.bias_up + n, left, whole, bu);
-  switch (a.act) {
+__device__ __forceinline__ void activate_row(int act, float (&z)[V], const float (&u)[V], const float (&bz)[V], const float (&bu)[V]) {
+  switch (act) {
     case ACT_NONE:
 #pragma unroll
       for (int i = 0; i < V; ++i) z[i] += bz[i];
@@ -116,51 +147,40 @@ __device__ __forceinline__ void finish(const MxLinearArgs& a, int64_t at, int n,
 #pragma unroll
       for (int i = 0; i < V; ++i) z[i] = activate(ACT_SILU, z[i] + bz[i]) * (u[i] + bu[i]);
   }
-  if (a.out_f32) {
-    float* o = static_cast<float*>(a.out) + at;
-    const float* r = static_cast<const float*>(a.residual);
-    if (whole) {
+}
+
+// The epilogue of C rows, V columns each from column n: sums(c, z, u) gives row c's, row(c) its index in out, or -1
+// where there is none.  The rows' residuals are loaded together, ahead of the first store.
+template <int V, bool F32, int C, typename Sums, typename Row>
+__device__ __forceinline__ void finish(const MxLinearArgs& a, int n, Sums sums, Row row) {
+  const int left = a.N - n;  // columns that exist
+  if (left <= 0) return;
+  float bz[V], bu[V], res[C][V];
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        floatx4 v = {z[i], z[i + 1], z[i + 2], z[i + 3]};
-        if (r) v += *reinterpret_cast<const floatx4*>(r + at + i);
-        *reinterpret_cast<floatx4*>(o + i) = v;
-      }
-    } else {
+  for (int i = 0; i < V; ++i) bz[i] = bu[i] = 0.f;
+  if (a.bias) load_values<V, true>(a.bias, n, left, bz);
+  if (a.bias_up) load_values<V, true>(a.bias_up, n, left, bu);
+  if (a.residual)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < left) o[i] = r ? z[i] + r[at + i] : z[i];
-    }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-    const uint16_t* r = static_cast<const uint16_t*>(a.residual);
-    if (whole) {
-      typedef __attribute__((__vector_size__(W * 2))) uint32_t words;  // W values
+    for (int c = 0; c < C; ++c)
+      if (row(c) >= 0) load_values<V, F32>(a.residual, row(c) * a.N + n, left, res[c]);
 #pragma unroll
-      for (int i = 0; i < V; i += W) {
-        words h;
-        if (r) {
-          const words q = *reinterpret_cast<const words*>(r + at + i);
+  for (int c = 0; c < C; ++c) {
+    if (row(c) < 0) continue;
+    float z[V], u[V];
+    sums(c, z, u);
+    activate_row<V>(a.act, z, u, bz, bu);
+    if (a.residual)
 #pragma unroll
-          for (int e = 0; e < W; ++e) z[i + e] += bf2f((uint16_t)(q[e >> 1] >> (16 * (e & 1))));
-        }
-#pragma unroll
-        for (int e = 0; e < W / 2; ++e)
-          h[e] = (uint32_t)f2bf_bits(z[i + 2 * e]) | ((uint32_t)f2bf_bits(z[i + 2 * e + 1]) << 16);
-        *reinterpret_cast<words*>(o + i) = h;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < left) o[i] = f2bf_bits(r ? z[i] + bf2f(r[at + i]) : z[i]);
-    }
+      for (int i = 0; i < V; ++i) z[i] += res[c][i];
+    store_values<V, F32>(a.out, row(c) * a.N + n, left, z);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Tiles through LDS
 // ---------------------------------------------------------------------------
-constexpr int kXcds = 8;
+constexpr int kXcds = 8, kCus = 256;
 constexpr int kGroupM = 8;  // row tiles per rasterisation group
 
 // Workgroup -> tile: workgroups go round-robin to the XCDs; each XCD's run is contiguous in an order of groups of
@@ -191,14 +211,16 @@ __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
 // an access of their own to the row's cache line, nearly as many as the codes need (340 us instead of 294 at
 // 4096 x 14336 x 4096 SwiGLU with 128-wide stages).  Lane half h takes the stage's blocks 4 h .. 4 h + 3, one for each
 // step, whose scales are the bytes of the word that it reads.
-template <int BM, int BN, int NMAT, int WM, int WN>
+template <int BM, int BN, int NMAT, int WM, int WN, int NS>
 struct Tile {
+  static constexpr bool RING = NS > 2;  // straight to LDS, several stages ahead
   static constexpr int NW = WM * WN;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + NMAT * B_BYTES;
   static constexpr int ROWS = BM + NMAT * BN;  // of x, then of the matrices
-  static constexpr int SCALES = 2 * STAGE;    // two places of 16 bytes a row
-  static constexpr int SMEM = SCALES + 2 * ROWS * 16;
+  static constexpr int SCALES = NS * STAGE;    // PLACES of 16 bytes a row
+  static constexpr int PLACES = RING ? NS / 2 + 1 : 2;  // (pairs of the stages from kt + 1 to kt + NS)
+  static constexpr int SMEM = SCALES + PLACES * ROWS * 16;
   static constexpr int PITCH = NMAT * BN / WN + 4, EPI = 32 * PITCH * 4;  // floats a staged row, bytes of 32 of them
   static constexpr int WT_M = BM / WM, WT_N = BN / WN;
   static constexpr int TM = WT_M / 32, TN = WT_N / 32, NB = NMAT * TN;
@@ -206,7 +228,7 @@ struct Tile {
   static constexpr int S_ALL = ROWS / 64, S_PIECES = (S_ALL + NW - 1) / NW;
   static constexpr int LOADS = A_PIECES + NMAT * B_PIECES;
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "whole pieces");
-  static_assert(TM >= 1 && TN >= 1, "tile");
+  static_assert(TM >= 1 && TN >= 1 && (NS - 2) * LOADS < 64, "tile");
   static_assert(NW * EPI <= SMEM, "room for the results");
 
   template <bool GROUPED>
@@ -259,24 +281,33 @@ struct Tile {
     // K is a multiple of 128: where the last stage is half a stage, the later half of each row reads zeros.
     const bool odd = (a.K & 128) != 0;
     const uint32_t cut = chunk >= 4 ? kOut : 0;
-    // Stage kt's codes, piece by piece: from global memory to registers, from there to LDS.
-    u32x4 stg[LOADS];
-    auto load = [&](int q, int kt) {  // (stages past the last load from past the resources)
+    // Stage kt's codes, piece by piece: to registers and from there to LDS, or straight to LDS.  (Stages past the last
+    // load from past the resources.)
+    auto source = [&](int q, int kt) -> uint32_t {
       const uint32_t none = kt < nk ? (odd && kt == nk - 1 ? cut : 0) : kOut, at = (uint32_t)kt * 128;
-      if (q < A_PIECES) stg[q] = __builtin_amdgcn_raw_buffer_load_b128(rx, (off_a[q < A_PIECES ? q : 0] + at) | none, 0, 0);
-      else stg[q] = __builtin_amdgcn_raw_buffer_load_b128(rwq[(q - A_PIECES) / B_PIECES],
-                                                          (off_b + (q - A_PIECES) % B_PIECES * 8 * NW * kb + at) | none, 0, 0);
+      return ((q < A_PIECES ? off_a[q < A_PIECES ? q : 0] : off_b + (q - A_PIECES) % B_PIECES * 8 * NW * kb) + at) | none;
     };
-    auto write = [&](int q, int kt) {
+    auto resource = [&](int q) { return q < A_PIECES ? rx : rwq[(q - A_PIECES) / B_PIECES]; };
+    auto place = [&](int q, int kt) {
       const int line = q < A_PIECES ? q * NW : BM / 8 + (q - A_PIECES) / B_PIECES * (BN / 8) + (q - A_PIECES) % B_PIECES * NW;
-      *reinterpret_cast<u32x4*>(smem + (kt % 2) * STAGE + (line + wave) * 1024 + lane * 16) = stg[q];
+      return smem + (kt % NS) * STAGE + (line + wave) * 1024;
     };
+    u32x4 stg[RING ? 1 : LOADS];
+    auto load = [&](int q, int kt) { stg[q] = __builtin_amdgcn_raw_buffer_load_b128(resource(q), source(q, kt), 0, 0); };
+    auto write = [&](int q, int kt) { *reinterpret_cast<u32x4*>(place(q, kt) + lane * 16) = stg[q]; };
     // The scales of stages kt and kt + 1 (16 bytes may run into the next row's, which no stage uses).
     auto issue_scales = [&](int kt) {
 #pragma unroll
       for (int q = 0; q < S_PIECES; ++q)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs[q], (lds_void*)(smem + SCALES + (kt / 2 % 2) * (ROWS * 16) + ((q * NW + wave) % S_ALL) * 1024), 16, off_s[q] + kt * 8, 0, 0, 0);
+            rs[q], (lds_void*)(smem + SCALES + (kt / 2 % PLACES) * (ROWS * 16) + ((q * NW + wave) % S_ALL) * 1024), 16, off_s[q] + kt * 8, 0, 0, 0);
+    };
+    // A whole stage straight to LDS, its scales ahead of it.
+    auto issue = [&](int kt) {
+      if (kt % 2 == 0 && kt < nk) issue_scales(kt);
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(q), (lds_void*)place(q, kt), 16, source(q, kt), 0, 0, 0);
     };
 
     floatx16 acc[NB][TM];
@@ -294,7 +325,7 @@ struct Tile {
       int a[TM], b[NB];
     };
     auto read = [&](Frags& f, int kt, int step) {
-      const char* st = smem + (kt % 2) * STAGE;
+      const char* st = smem + (kt % NS) * STAGE;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int row = wn * WT_N + (j % TN) * 32 + l32;
@@ -307,12 +338,20 @@ struct Tile {
       }
     };
     auto read_scales = [&](Scales& f, int kt) {
-      const char* sc = smem + SCALES + (kt / 2 % 2) * (ROWS * 16) + (kt % 2) * 8 + half * 4;
+      const char* sc = smem + SCALES + (kt / 2 % PLACES) * (ROWS * 16) + (kt % 2) * 8 + half * 4;
 #pragma unroll
       for (int i = 0; i < TM; ++i) f.a[i] = *reinterpret_cast<const int*>(sc + (wm * WT_M + i * 32 + l32) * 16);
 #pragma unroll
       for (int j = 0; j < NB; ++j)
         f.b[j] = *reinterpret_cast<const int*>(sc + (BM + (j / TN) * BN + wn * WT_N + (j % TN) * 32 + l32) * 16);
+    };
+    auto blank = [&](Scales& s, int kt) {  // (no scales past the row's end; the codes are zeros)
+      if (odd && kt == nk - 1 && half) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) s.a[i] = 0;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s.b[j] = 0;
+      }
     };
     auto multiply = [&](auto step, const Frags& f, const Scales& s) {
       constexpr int S = decltype(step)::value;
@@ -323,10 +362,11 @@ struct Tile {
           acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(f.b[j]), widen(f.a[i]), acc[j][i], kFp4, kFp4, S,
                                                                       s.b[j], S, s.a[i]);
       // (the instructions have no side effects: the use of the accumulators keeps them on this side of the barrier)
+      if constexpr (!RING)
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(acc[j][i]));
+          for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(acc[j][i]));
     };
     // Instruction order of a step: an LDS read after each matrix instruction while there are any, and the pieces' writes
     // and loads in the places after those.
@@ -345,6 +385,41 @@ struct Tile {
       __builtin_amdgcn_sched_barrier(0);
     };
     using std::integral_constant;
+    if constexpr (RING) {
+#pragma unroll
+      for (int kt = 0; kt < NS; ++kt) issue(kt);
+      wait_vmcnt<(NS - 1) * LOADS>();
+      ring_barrier();
+      struct Whole {
+        Frags f[4];
+        Scales s;
+      };
+      Whole w[2];
+      auto read_stage = [&](Whole& v, int kt) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) read(v.f[q], kt, q);
+        read_scales(v.s, kt);
+      };
+      auto stage = [&](Whole& cur, Whole& next, int kt) {
+        wait_lgkm0();                     // this wavefront's reads of stage kt are done
+        wait_vmcnt<(NS - 2) * LOADS>();   // its loads of stage kt + 1, with their scales, have landed
+        ring_barrier();                   // so are and have all others'
+        issue(kt + NS);                   // into the place of stage kt
+        read_stage(next, kt + 1);
+        blank(cur.s, kt);
+        multiply(integral_constant<int, 0>{}, cur.f[0], cur.s);
+        multiply(integral_constant<int, 1>{}, cur.f[1], cur.s);
+        multiply(integral_constant<int, 2>{}, cur.f[2], cur.s);
+        multiply(integral_constant<int, 3>{}, cur.f[3], cur.s);
+      };
+      read_stage(w[0], 0);
+      for (int kt = 0; kt < nk; kt += 2) {
+        stage(w[0], w[1], kt);
+        if (kt + 1 < nk) stage(w[1], w[0], kt + 1);
+      }
+      wait_vmcnt<0>();  // (the empty stages' writes to LDS)
+      wait_lgkm0();
+    } else {
     Frags f[2];
     Scales sc, next;
     issue_scales(0);
@@ -370,12 +445,7 @@ struct Tile {
           }
       };
       sc = next;
-      if (odd && kt == nk - 1 && half) {  // (no scales there; the codes are zeros)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sc.a[i] = 0;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) sc.b[j] = 0;
-      }
+      blank(sc, kt);
       read(f[1], kt, 1);
       pieces(0, P0);
       multiply(integral_constant<int, 0>{}, f[0], sc);
@@ -396,6 +466,7 @@ struct Tile {
       multiply(integral_constant<int, 3>{}, f[1], sc);
       order(integral_constant<int, 2 * (TM + NB)>{}, integral_constant<int, 0>{});
     }
+    }
     ring_barrier();
 
     // A lane holds, for row l32 of a 32-row block, columns 8 (v / 4) + 4 half + v % 4 of each 32-column block (v: element
@@ -414,38 +485,43 @@ struct Tile {
                 floatx4{acc[j][ii][v], acc[j][ii][v + 1], acc[j][ii][v + 2], acc[j][ii][v + 3]};
       }
       const int r0 = wm * WT_M + i * 32;
-      if (a.out_f32) store_rows<4>(a, rw, sm, r0, n0 + wn * WT_N, lane);
-      else store_rows<8>(a, rw, sm, r0, n0 + wn * WT_N, lane);
+      if (a.out_f32) store_rows<4, true>(a, rw, sm, r0, n0 + wn * WT_N, lane);
+      else store_rows<8, false>(a, rw, sm, r0, n0 + wn * WT_N, lane);
     }
   }
 
-  // The epilogue of 32 staged rows from row r0 of the tile: V columns a lane.
-  template <int V>
+  // The epilogue of 32 staged rows from row r0 of the tile: V columns a lane, up to eight rows of a lane together (one by
+  // one, 4096 x 14336 x 512 with an fp32 residual took 217 us instead of 130).
+  template <int V, bool F32>
   static __device__ __forceinline__ void store_rows(const MxLinearArgs& a, const Rows& rw, const float* sm, int r0, int n0,
                                                     int lane) {
-    constexpr int LPR = WT_N / V, STEP = 64 / LPR;  // lanes a row, rows at a time
-    const int c = lane % LPR * V;
-#pragma unroll 1
-    for (int r = lane / LPR; r < 32; r += STEP) {
-      float z[V], u[V];
+    constexpr int LPR = WT_N / V, STEP = 64 / LPR, C = 32 / STEP;  // lanes a row, rows at a time
+    const int c0 = lane % LPR * V, r = lane / LPR;
+    finish<V, F32, C>(
+        a, n0 + c0,
+        [&](int c, float (&z)[V], float (&u)[V]) {
+          const float* s = sm + (r + c * STEP) * PITCH + c0;
 #pragma unroll
-      for (int v = 0; v < V; v += 4) {
-        const floatx4 p = *reinterpret_cast<const floatx4*>(sm + r * PITCH + c + v);
-        const floatx4 q = NMAT == 2 ? *reinterpret_cast<const floatx4*>(sm + r * PITCH + WT_N + c + v) : p;
+          for (int v = 0; v < V; v += 4) {
+            const floatx4 p = *reinterpret_cast<const floatx4*>(s + v);
+            const floatx4 q = NMAT == 2 ? *reinterpret_cast<const floatx4*>(s + WT_N + v) : p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[v + e] = p[e];
-          u[v + e] = q[e];
-        }
-      }
-      if (r0 + r < rw.valid) finish<V>(a, (rw.row0 + r0 + r) * a.N + n0 + c, n0 + c, z, u);
-    }
+            for (int e = 0; e < 4; ++e) {
+              z[v + e] = p[e];
+              u[v + e] = q[e];
+            }
+          }
+        },
+        [&](int c) -> int64_t {
+          const int q = r0 + r + c * STEP;
+          return q < rw.valid ? rw.row0 + q : -1;
+        });
   }
 };
 
-template <int BM, int BN, int NMAT, int WM, int WN, bool GROUPED>
+template <int BM, int BN, int NMAT, int WM, int WN, int NS, bool GROUPED>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
-  using T = Tile<BM, BN / NMAT, NMAT, WM, WN>;
+  using T = Tile<BM, BN / NMAT, NMAT, WM, WN, NS>;
   __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
   int mt = p.mt;
   if (GROUPED) {
@@ -466,17 +542,26 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
 // Up to 16 MB rows by 16 columns a workgroup; its wavefronts take turns at units of 512 reduction indices and add up
 // through LDS.  v_mfma_scale_f32_16x16x128: lane l holds block l / 16 of four of row l % 16, so a load of 16 bytes a
 // lane is 64 contiguous bytes of each of 16 rows, and a unit's 16 scale bytes of a row come as one load.
-constexpr int kStreamWaves = 8;
+//
+// With at most four rows one load has x for the four steps of a unit, step s in columns 4 s .. 4 s + 3, and a step's
+// fragment is that register shifted by DPP (a column's result depends on its own row alone: the other columns hold
+// anything); a load a step would cost as many accesses as the weights.
+constexpr int kStreamWaves = 4;
 
-template <int MB, int NMAT, bool GROUPED>
-__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
+template <int N>
+__device__ __forceinline__ u32x4 shifted(u32x4 v) {
+  if constexpr (N == 0) return v;
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], 0x100 + N, 0xf, 0xf, false);  // row_shl:N
+  return o;
+}
+
+template <int MB, int NMAT, bool GROUPED, bool FOUR>
+__device__ __forceinline__ void stream_rows(const Product& p, const Rows& rw, int n0, float* red) {
   constexpr int RED = NMAT * MB * 256;  // floats of a wavefront's sums
-  __shared__ float red[kStreamWaves * RED];
+  constexpr int XL = FOUR ? 1 : 4, NWV = kStreamWaves;
   const MxLinearArgs& a = p.a;
-  const int ti = blockIdx.x / p.nt, n0 = (int)(blockIdx.x % p.nt) * 16;
-  if (GROUPED && ti >= *a.num_tiles * p.sub) return;
-  const Rows rw = rows_of<GROUPED>(p, ti, 16 * MB);
-  if (rw.valid <= 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int kb = a.K / 2, sb = a.K / 32, units = (a.K + 511) / 512;
@@ -492,7 +577,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
   uint32_t ox[MB], oxs[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int r = i * 16 + l16;
+    const int r = FOUR ? l16 & 3 : i * 16 + l16;
     uint32_t row = (uint32_t)r;
     bool in = r < rw.valid;
     if (gather) {
@@ -500,7 +585,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
       row = (uint32_t)src / (uint32_t)a.topk;
       in = src >= 0 && row < a.M;
     }
-    ox[i] = in ? row * (uint32_t)kb + g * 16 : kOut;
+    ox[i] = in ? row * (uint32_t)kb + g * 16 + (FOUR ? (l16 >> 2) * 64 : 0) : kOut;
     oxs[i] = in ? row * (uint32_t)sb : kOut;
   }
   const uint32_t ow = (uint32_t)(l16 * kb + g * 16), ows = (uint32_t)(l16 * sb);
@@ -511,37 +596,56 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[m][i] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  for (int u = wave; u < units; u += kStreamWaves) {
-    const int steps = (a.K - u * 512) / 128;  // (4 but for the last unit)
-    u32x4 w[NMAT][4], ws[NMAT], x[MB][4], xs[MB];
-    // (steps past the row's end load from past the resource; the scales of a unit may run into the next row's, which
-    // no step uses)
+  struct Unit {
+    u32x4 w[NMAT][4], ws[NMAT], x[MB][XL], xs[MB];
+  };
+  // (steps past the row's end load from past the resource; the scales of a unit may run into the next row's, which no
+  // step uses; loads marked as streaming, which leave no half lines for the next step, took 409 us there)
+  auto load = [&](Unit& v, int u) {
+    const int steps = (a.K - u * 512) / 128;  // (4 but for the last unit; none past it)
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        w[m][s] = __builtin_amdgcn_raw_buffer_load_b128(rwq[m], s < steps ? ow + u * 256 + s * 64 : kOut, 0, 2);
-      ws[m] = __builtin_amdgcn_raw_buffer_load_b128(rws[m], ows + u * 16, 0, 0);
+        v.w[m][s] = __builtin_amdgcn_raw_buffer_load_b128(rwq[m], s < steps ? ow + u * 256 + s * 64 : kOut, 0, 0);
+      v.ws[m] = __builtin_amdgcn_raw_buffer_load_b128(rws[m], steps > 0 ? ows + u * 16 : kOut, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, s < steps ? ox[i] + u * 256 + s * 64 : kOut, 0, 0);
-      xs[i] = __builtin_amdgcn_raw_buffer_load_b128(rxs, oxs[i] + u * 16, 0, 0);
+      for (int s = 0; s < XL; ++s)
+        v.x[i][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, (FOUR ? l16 >> 2 : s) < steps ? ox[i] + u * 256 + s * 64 : kOut, 0, 0);
+      v.xs[i] = __builtin_amdgcn_raw_buffer_load_b128(rxs, steps > 0 ? oxs[i] + u * 16 : kOut, 0, 0);
     }
+  };
+  auto multiply = [&](const Unit& v, int u) {
+    const int steps = (a.K - u * 512) / 128;
+    auto step = [&](auto s_) {
+      constexpr int S = decltype(s_)::value;
+      const bool in = S < steps;  // (past the row's end the codes are zeros, and so are their scales)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s >= steps) break;
+      for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-      for (int m = 0; m < NMAT; ++m) {
-        const int sw = (int)(ws[m][s] >> (8 * g));
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-          acc[m][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w[m][s]), widen(x[i][s]), acc[m][i], kFp4, kFp4, 0,
-                                                                       sw, 0, (int)(xs[i][s] >> (8 * g)));
-      }
-    }
+        for (int i = 0; i < MB; ++i) {
+          const u32x4 t = FOUR ? shifted<FOUR ? 4 * S : 0>(v.x[i][0]) : v.x[i][FOUR ? 0 : S];
+          acc[m][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              widen(v.w[m][S]), widen(t), acc[m][i], kFp4, kFp4, 0, in ? (int)(v.ws[m][S] >> (8 * g)) : 0, 0,
+              in ? (int)(v.xs[i][S] >> (8 * g)) : 0);
+        }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  // One unit's registers, loaded again as soon as they are multiplied: a second unit's took 340 us where this takes 260
+  // for gate and up products of 64 experts of 2048 x 7168, 16 rows each, because fewer wavefronts fit.  (The loads stand
+  // at the loop's end so that they are all issued together.)
+  Unit q;
+  load(q, wave);
+  for (int u = wave; u < units; u += NWV) {
+    multiply(q, u);
+    if (u + NWV < units) load(q, u + NWV);
   }
 #pragma unroll
   for (int m = 0; m < NMAT; ++m)
@@ -550,18 +654,36 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
   __syncthreads();
   // Lane l of a partial sum: row l % 16, columns 4 (l / 16) + 0..3.  One wavefront per 16 rows, in the units' order.
   if (wave < MB) {
-    float z[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int q = 0; q < kStreamWaves; ++q) {
-      const float* s = red + q * RED + wave * 256 + lane * 4;
+    floatx4 z = {0.f, 0.f, 0.f, 0.f}, v = z;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[e] += s[e];
-        if (NMAT == 2) v[e] += s[MB * 256 + e];
-      }
+    for (int w = 0; w < NWV; ++w) {
+      const float* s = red + w * RED + wave * 256 + lane * 4;
+      z += *reinterpret_cast<const floatx4*>(s);
+      if (NMAT == 2) v += *reinterpret_cast<const floatx4*>(s + MB * 256);
     }
-    const int r = wave * 16 + l16, n = n0 + g * 4;
-    if (r < rw.valid) finish<4>(a, (rw.row0 + r) * a.N + n, n, z, v);
+    const int r = wave * 16 + l16;
+    auto sums = [&](int, float (&zv)[4], float (&uv)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        zv[i] = z[i];
+        uv[i] = v[i];
+      }
+    };
+    auto row = [&](int) -> int64_t { return r < rw.valid ? rw.row0 + r : -1; };
+    if (a.out_f32) finish<4, true, 1>(a, n0 + g * 4, sums, row);
+    else finish<4, false, 1>(a, n0 + g * 4, sums, row);
   }
+}
+
+template <int MB, int NMAT, bool GROUPED>
+__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
+  __shared__ float red[kStreamWaves * NMAT * MB * 256];
+  const int ti = blockIdx.x / p.nt, n0 = (int)(blockIdx.x % p.nt) * 16;
+  if (GROUPED && ti >= *p.a.num_tiles * p.sub) return;
+  const Rows rw = rows_of<GROUPED>(p, ti, 16 * MB);
+  if (rw.valid <= 0) return;
+  if (MB == 1 && rw.valid <= 4) stream_rows<MB, NMAT, GROUPED, MB == 1>(p, rw, n0, red);
+  else stream_rows<MB, NMAT, GROUPED, false>(p, rw, n0, red);
 }
 
 hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
@@ -575,19 +697,19 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
     hipLaunchKernelGGL((KERNEL_), dim3((unsigned)g), dim3(BLOCK_), 0, s, p);                               \
     return hipGetLastError();                                                                              \
   } while (0)
-#define MOE_TILE(BM_, BN_, WM_, WN_)                                                                       \
+#define MOE_TILE(BM_, BN_, BN2_, WM_, WN_, NS_)                                                            \
   do {                                                                                                     \
-    if (grouped && dual) MOE_LAUNCH((tile_kernel<BM_, BN_, 2, WM_, WN_, true>), WM_* WN_ * 64);            \
-    if (grouped) MOE_LAUNCH((tile_kernel<BM_, BN_, 1, WM_, WN_, true>), WM_* WN_ * 64);                    \
-    if (dual) MOE_LAUNCH((tile_kernel<BM_, BN_, 2, WM_, WN_, false>), WM_* WN_ * 64);                      \
-    MOE_LAUNCH((tile_kernel<BM_, BN_, 1, WM_, WN_, false>), WM_* WN_ * 64);                                \
+    if (grouped && dual) MOE_LAUNCH((tile_kernel<BM_, BN2_, 2, WM_, WN_, NS_, true>), WM_* WN_ * 64);      \
+    if (grouped) MOE_LAUNCH((tile_kernel<BM_, BN_, 1, WM_, WN_, NS_, true>), WM_* WN_ * 64);               \
+    if (dual) MOE_LAUNCH((tile_kernel<BM_, BN2_, 2, WM_, WN_, NS_, false>), WM_* WN_ * 64);                \
+    MOE_LAUNCH((tile_kernel<BM_, BN_, 1, WM_, WN_, NS_, false>), WM_* WN_ * 64);                           \
   } while (0)
 #define MOE_STREAM(MB_)                                                                                    \
   do {                                                                                                     \
-    if (grouped && dual) MOE_LAUNCH((stream_kernel<MB_, 2, true>), kStreamWaves * 64);                     \
-    if (grouped) MOE_LAUNCH((stream_kernel<MB_, 1, true>), kStreamWaves * 64);                             \
-    if (dual) MOE_LAUNCH((stream_kernel<MB_, 2, false>), kStreamWaves * 64);                               \
-    MOE_LAUNCH((stream_kernel<MB_, 1, false>), kStreamWaves * 64);                                         \
+    if (grouped && dual) MOE_LAUNCH((stream_kernel<MB_, 2, true>), kStreamWaves * 64);                  \
+    if (grouped) MOE_LAUNCH((stream_kernel<MB_, 1, true>), kStreamWaves * 64);                          \
+    if (dual) MOE_LAUNCH((stream_kernel<MB_, 2, false>), kStreamWaves * 64);                            \
+    MOE_LAUNCH((stream_kernel<MB_, 1, false>), kStreamWaves * 64);                                      \
   } while (0)
   auto tiles = [&](int bm, int bn) {
     if (grouped) {
@@ -600,17 +722,42 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
     p.nt = (p.a.N + bn - 1) / bn;
   };
   const int mats = dual ? 2 : 1;
-  if (rows <= 64) {
+  const int nk = (p.a.K + kStage - 1) / kStage;
+  // Tiles: the kind whose rounds over the CUs take least.  A round is a tile's stages and what comes before and after
+  // them, in us as measured on products that fill every CU once (fp32 and bf16 outputs, 4 to 32 stages).
+  struct Kind {
+    int bm, bn;
+    float stage, fixed;
+  };
+  const Kind kinds[] = {{256, 256, 2.0f, 11.f}, {256, 128, 1.22f, 9.5f}, {128, 128, 0.86f, 5.4f}, {64, dual ? 128 : 64, dual ? 0.45f : 0.31f, 4.f}};
+  int best = 3;
+  float least = 0.f;
+  for (int i = 3; i >= 0; --i) {
+    if (kinds[i].bm > rows && i < 3) continue;
+    tiles(kinds[i].bm, kinds[i].bn / mats);
+    const float t = ((int64_t)p.mt * p.nt + kCus - 1) / kCus * (nk * kinds[i].stage + kinds[i].fixed);
+    if (i == 3 || t < least) {
+      best = i;
+      least = t;
+    }
+  }
+  // Few rows: streamed where that takes less, us by the megabyte of codes as measured on 29 MB (17 rows of 4096 x 14336
+  // 11.7 us, 20.8 in tiles; of 14336 x 4096 13.3, 10.2 in tiles).  Grouped, tiles are never cut below 64 rows.
+  const float mb_codes = (float)p.a.N * p.a.K * mats * 0.5e-6f;
+  if (rows <= 16 || (grouped && rows < 64) || (!grouped && rows <= 32 && 4.f + 0.38f * mb_codes < least) ||
+      (!grouped && rows <= 64 && 5.f + 0.65f * mb_codes < least)) {
     const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     tiles(16 * mb, 16);
     if (mb == 1) MOE_STREAM(1);
     if (mb == 2) MOE_STREAM(2);
-    MOE_STREAM(4);
+    if (dual) MOE_LAUNCH((stream_kernel<4, 2, false>), kStreamWaves * 64);
+    MOE_LAUNCH((stream_kernel<4, 1, false>), kStreamWaves * 64);
   }
-  tiles(256, 256 / mats);
-  if (rows >= 256 && (int64_t)p.mt * p.nt >= 192) MOE_TILE(256, 256, 2, 4);
-  tiles(128, 128 / mats);
-  MOE_TILE(128, 128, 2, 2);
+  tiles(kinds[best].bm, kinds[best].bn / mats);
+  if (best == 0) MOE_TILE(256, 256, 256, 2, 4, 2);
+  if (best == 1) MOE_TILE(256, 128, 128, 4, 2, 3);
+  if (best == 2) MOE_TILE(128, 128, 128, 4, 2, 4);
+  MOE_TILE(64, 64, 128, 2, 2, 5);
 #undef MOE_LAUNCH
 #undef MOE_TILE
 #undef MOE_STREAM

@@ -566,33 +566,39 @@ def alloc_mxfp4(shape, device) -> Mxfp4:
     return Mxfp4(torch.empty((*shape[:-1], shape[-1] // 2), **u8), torch.empty((*shape[:-1], shape[-1] // 32), **u8))
 
 
-def _mx(t: Optional[Mxfp4], name: str, shape, dev: int, optional: bool = False):
-    """Addresses (codes, scales) of a checked MXFP4 argument of that value shape."""
-    if t is None:
-        if optional:
-            return None, None
-        raise ValueError(f"{name} is required")
+def _mx(t: Optional[Mxfp4], name: str, codes, scales, dev: int, optional: bool = False):
+    """Addresses (codes, scales) of a checked MXFP4 argument with codes and scales of those shapes."""
+    if t is None and optional:
+        return None, None
     if not isinstance(t, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4, got {type(t).__name__}")
-    u8, lead, K = torch.uint8, tuple(shape[:-1]), shape[-1]
-    return (_take(t.codes, f"{name}.codes", u8, (*lead, K // 2), dev),
-            _take(t.scales, f"{name}.scales", u8, (*lead, K // 32), dev))
+    c, s = t
+    u8 = torch.uint8
+    if (c.dtype is u8 and c.shape == codes and c.get_device() == dev and c.is_contiguous() and s.dtype is u8
+            and s.shape == scales and s.get_device() == dev and s.is_contiguous()):
+        return c.data_ptr(), s.data_ptr()
+    return _take(c, f"{name}.codes", u8, codes, dev), _take(s, f"{name}.scales", u8, scales, dev)
 
 
-def _mx_shape(t, name: str, dims: int):
-    """(device number, value shape) of an MXFP4 argument of `dims` dimensions."""
+def _mx_codes(t, name: str, dims: int):
+    """The codes of an MXFP4 argument of `dims` dimensions (0: any) on a device."""
     if not isinstance(t, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4, got {type(t).__name__}")
-    if t.codes.get_device() < 0:
+    c = t.codes
+    if c.get_device() < 0:
         raise ValueError(f"{name} must be on a device")
-    if t.codes.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.codes.dim()}")
-    return t.codes.get_device(), t.shape
+    if c.dim() != dims and (dims or not c.dim()):
+        raise ValueError(f"{name} must have {dims or 'some'} dimensions, got {c.dim()}")
+    return c
 
 
-def _need_k(K: int, multiple: int, name: str):
-    if K < 1 or K % multiple:
-        raise ValueError(f"the last dimension of {name} must be a multiple of {multiple}, got {K}")
+def _mx_shapes(shape):
+    """Shapes of the codes and scales of values of that shape, whose last dimension has to be whole blocks."""
+    K = shape[-1]
+    if K < 1 or K % 32:
+        raise ValueError(f"the last dimension must be a multiple of 32, got {K}")
+    lead = tuple(shape[:-1])
+    return (*lead, K // 2), (*lead, K // 32)
 
 
 def moe_mxfp4_quantize(x: torch.Tensor, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
@@ -601,15 +607,15 @@ def moe_mxfp4_quantize(x: torch.Tensor, out: Optional[Mxfp4] = None, stream=None
         _same_device(stream, x, out)
         return _on(stream, moe_mxfp4_quantize, x, out)
     dev, shape = x.get_device(), x.shape
-    if dev < 0 or x.dim() < 1:
+    if dev < 0 or not shape:
         raise ValueError("x must be a device tensor of at least one dimension")
-    K = shape[-1]
-    _need_k(K, 32, "x")
+    codes, scales = _mx_shapes(shape)
     if out is None:
         out = alloc_mxfp4(shape, x.device)
-    codes, scales = _mx(out, "out", shape, dev)
-    _launch((_lib or lib()).moe_mxfp4_quantize, "moe_mxfp4_quantize", dev, _take(x, "x", x.dtype, shape, dev), x.numel() // K, K,
-            _choice(OUT_DTYPES, x.dtype, "x's type"), codes, scales)
+    K, dt = shape[-1], x.dtype
+    c, s = _mx(out, "out", codes, scales, dev)
+    _launch((_lib or lib()).moe_mxfp4_quantize, "moe_mxfp4_quantize", dev, _take(x, "x", dt, shape, dev), x.numel() // K, K,
+            _choice(OUT_DTYPES, dt, "x's type"), c, s)
     return out
 
 
@@ -619,16 +625,16 @@ def moe_mxfp4_dequantize(q: Mxfp4, out: Optional[torch.Tensor] = None, out_dtype
     if stream is not None:
         _same_device(stream, q, out)
         return _on(stream, moe_mxfp4_dequantize, q, out, out_dtype)
-    if not isinstance(q, Mxfp4) or q.codes.get_device() < 0 or q.codes.dim() < 1:
-        raise ValueError("q must be an Mxfp4 on a device")
-    dev, shape = q.codes.get_device(), q.shape
-    K = shape[-1]
-    _need_k(K, 32, "q")
+    codes = _mx_codes(q, "q", 0)
+    dev, cs = codes.get_device(), codes.shape
+    shape = (*cs[:-1], cs[-1] * 2)
+    cs, ss = _mx_shapes(shape)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.codes.device)
-    codes, scales = _mx(q, "q", shape, dev)
-    _launch((_lib or lib()).moe_mxfp4_dequantize, "moe_mxfp4_dequantize", dev, codes, scales, out.numel() // K, K,
-            _choice(OUT_DTYPES, out.dtype, "out's type"), _take(out, "out", out.dtype, shape, dev))
+        out = torch.empty(shape, dtype=out_dtype, device=codes.device)
+    K, dt = shape[-1], out.dtype
+    c, s = _mx(q, "q", cs, ss, dev)
+    _launch((_lib or lib()).moe_mxfp4_dequantize, "moe_mxfp4_dequantize", dev, c, s, out.numel() // K, K,
+            _choice(OUT_DTYPES, dt, "out's type"), _take(out, "out", dt, shape, dev))
     return out
 
 
@@ -660,19 +666,21 @@ def moe_linear_mxfp4(x: Mxfp4, w: Mxfp4, w_up: Optional[Mxfp4] = None, bias: Opt
         _same_device(stream, x, w, w_up)
         return _on(stream, moe_linear_mxfp4, x, w, w_up, bias, bias_up, act, residual, out, out_dtype, ws,
                    use_workspace=use_workspace)
-    (dev, (M, K)), (_, (N, _)) = _mx_shape(x, "x", 2), _mx_shape(w, "w", 2)
-    f32 = torch.float32
+    xc = _mx_codes(x, "x", 2)
+    (M, Kh), N, dev = xc.shape, _mx_codes(w, "w", 2).shape[0], xc.get_device()
+    K, Kb, f32 = 2 * Kh, Kh // 16, torch.float32
+    mn, nk, nb = (M, N), (N, Kh), (N, Kb)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.codes.device)
+        out = torch.empty(mn, dtype=out_dtype, device=xc.device)
     odt = out.dtype
     a = _choice(LINEAR_ACTS, act, "act")
     if ws is None and use_workspace:
-        ws = alloc_linear_mxfp4_workspace(M, N, K, act, x.codes.device)
+        ws = alloc_linear_mxfp4_workspace(M, N, K, act, xc.device)
     wsp, wsn = _ws(ws, dev)
-    _launch((_lib or lib()).moe_linear_mxfp4, "moe_linear_mxfp4", dev, *_mx(x, "x", (M, K), dev), *_mx(w, "w", (N, K), dev),
-            *_mx(w_up, "w_up", (N, K), dev, True), _take(bias, "bias", f32, (N,), dev, True),
-            _take(bias_up, "bias_up", f32, (N,), dev, True), _take(residual, "residual", odt, (M, N), dev, True), M, N, K, a,
-            _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, (M, N), dev), wsp, wsn)
+    _launch((_lib or lib()).moe_linear_mxfp4, "moe_linear_mxfp4", dev, *_mx(x, "x", (M, Kh), (M, Kb), dev), *_mx(w, "w", nk, nb, dev),
+            *_mx(w_up, "w_up", nk, nb, dev, True), _take(bias, "bias", f32, (N,), dev, True),
+            _take(bias_up, "bias_up", f32, (N,), dev, True), _take(residual, "residual", odt, mn, dev, True), M, N, K, a,
+            _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, mn, dev), wsp, wsn)
     return out
 
 
@@ -684,19 +692,21 @@ def moe_grouped_linear_mxfp4(p: Permuted, x: Mxfp4, w: Mxfp4, w_up: Optional[Mxf
     if stream is not None:
         _same_device(stream, x, w, w_up)
         return _on(stream, moe_grouped_linear_mxfp4, p, x, w, w_up, act, gather, out, out_dtype)
-    (dev, (rows, K)), (_, (E_loc, N, _)) = _mx_shape(x, "x", 2), _mx_shape(w, "w", 3)
-    i32 = torch.int32
+    xc = _mx_codes(x, "x", 2)
+    Kh, (E_loc, N, _), dev, i32 = xc.shape[1], _mx_codes(w, "w", 3).shape, xc.get_device(), torch.int32
     T, k = p.inv_perm.shape if gather else (0, 0)
+    rows, Kb, R = T if gather else p.R_cap, Kh // 16, p.R_cap
+    enk, enb = (E_loc, N, Kh), (E_loc, N, Kb)
     if out is None:
-        out = torch.empty((p.R_cap, N), dtype=out_dtype, device=x.codes.device)
+        out = torch.empty((R, N), dtype=out_dtype, device=xc.device)
     odt = out.dtype
-    _launch((_lib or lib()).moe_grouped_linear_mxfp4, "moe_grouped_linear_mxfp4", dev,
-            *_mx(x, "x", (T if gather else p.R_cap, K), dev), _take(p.row_src, "row_src", i32, (p.R_cap,), dev) if gather else None,
-            T, k, _take(p.expert_counts, "expert_counts", i32, (E_loc,), dev),
+    _launch((_lib or lib()).moe_grouped_linear_mxfp4, "moe_grouped_linear_mxfp4", dev, *_mx(x, "x", (rows, Kh), (rows, Kb), dev),
+            _take(p.row_src, "row_src", i32, (R,), dev) if gather else None, T, k,
+            _take(p.expert_counts, "expert_counts", i32, (E_loc,), dev),
             _take(p.expert_offsets, "expert_offsets", i32, (E_loc + 1,), dev), _take(p.tiles, "tiles", i32, (p.tiles_cap, 2), dev),
-            _take(p.num_tiles, "num_tiles", i32, (1,), dev), *_mx(w, "w", (E_loc, N, K), dev),
-            *_mx(w_up, "w_up", (E_loc, N, K), dev, True), E_loc, N, K, _choice(LINEAR_ACTS, act, "act"), p.tile_m, p.R_cap,
-            p.tiles_cap, _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, (p.R_cap, N), dev))
+            _take(p.num_tiles, "num_tiles", i32, (1,), dev), *_mx(w, "w", enk, enb, dev), *_mx(w_up, "w_up", enk, enb, dev, True),
+            E_loc, N, 2 * Kh, _choice(LINEAR_ACTS, act, "act"), p.tile_m, R, p.tiles_cap,
+            _choice(OUT_DTYPES, odt, "out's type"), _take(out, "out", odt, (R, N), dev))
     return out
 
 
@@ -729,7 +739,10 @@ def moe_few_tokens(x: torch.Tensor, w0: Weight, w0_up: Optional[Weight], w1: Wei
                    num_experts, out, ws)
     (T, H), dev = _matrix(x, "x"), x.get_device()
     mx, bf, f32 = isinstance(w0, Mxfp4), torch.bfloat16, torch.float32
-    E_loc, F = w0.shape[:2] if len(w0.shape) == 3 else (0, 0)
+    up = (w0.codes if mx else w0).shape if w0 is not None else ()
+    if len(up) != 3:
+        raise ValueError("w0 must have 3 dimensions: [E_loc, F, H]")
+    E_loc, F = up[:2]
     if logits is not None:
         E = _matrix(logits, "logits")[1]
         if k is None:
@@ -751,18 +764,19 @@ def moe_few_tokens(x: torch.Tensor, w0: Weight, w0_up: Optional[Weight], w1: Wei
     if ws is None:
         ws = alloc_few_tokens_workspace(T, k, F, x.device)
     wsp, wsn = _ws(ws, dev)
-
-    def weight(w, name, shape, optional=False):
-        if mx:
-            return _mx(w, name, shape, dev, optional)
-        if isinstance(w, Mxfp4):
-            raise TypeError(f"{name} is an Mxfp4, w0 is not")
-        return _take(w, name, bf, shape, dev, optional), None
-
-    up, down = (E_loc, F, H), (E_loc, H, F)
+    if mx:
+        upc, ups, dc, ds = (E_loc, F, H // 2), (E_loc, F, H // 32), (E_loc, H, F // 2), (E_loc, H, F // 32)
+        p0, s0 = _mx(w0, "w0", upc, ups, dev)
+        pu, su = _mx(w0_up, "w0_up", upc, ups, dev, True)
+        p1, s1 = _mx(w1, "w1", dc, ds, dev)
+    else:
+        if isinstance(w0_up, Mxfp4) or isinstance(w1, Mxfp4):
+            raise TypeError("the weights must all be in MXFP4, or none")
+        up, s0, su, s1 = (E_loc, F, H), None, None, None
+        p0, pu, p1 = _take(w0, "w0", bf, up, dev), _take(w0_up, "w0_up", bf, up, dev, True), _take(w1, "w1", bf, (E_loc, H, F), dev)
+    tk = (T, k)
     _launch((_lib or lib()).moe_few_tokens, "moe_few_tokens", dev, _take(x, "x", bf, (T, H), dev),
             _take(logits, "logits", f32, (T, E), dev, True), T, E, k, 1 if renormalize else 0, expert_begin, E_loc,
-            *weight(w0, "w0", up), *weight(w0_up, "w0_up", up, True), *weight(w1, "w1", down), H, F, _choice(ACTS, act, "act"),
-            _take(topk_idx, "topk_idx", torch.int32, (T, k), dev), _take(topk_w, "topk_w", f32, (T, k), dev),
-            _take(out, "out", f32, (T, H), dev), wsp, wsn)
+            p0, s0, pu, su, p1, s1, H, F, _choice(ACTS, act, "act"), _take(topk_idx, "topk_idx", torch.int32, tk, dev),
+            _take(topk_w, "topk_w", f32, tk, dev), _take(out, "out", f32, (T, H), dev), wsp, wsn)
     return out
