@@ -420,52 +420,53 @@ struct Tile {
       wait_vmcnt<0>();  // (the empty stages' writes to LDS)
       wait_lgkm0();
     } else {
-    Frags f[2];
-    Scales sc, next;
-    issue_scales(0);
-#pragma unroll
-    for (int q = 0; q < LOADS; ++q) load(q, 0);
-#pragma unroll
-    for (int q = 0; q < LOADS; ++q) write(q, 0);  // (waits for the scales too, which went ahead)
-#pragma unroll
-    for (int q = 0; q < LOADS; ++q) load(q, 1);
-    wait_lgkm0();
-    ring_barrier();
-    read(f[0], 0, 0);
-    read_scales(next, 0);
-    constexpr int P0 = (LOADS + 2) / 3, P1 = 2 * P0 < LOADS ? 2 * P0 : LOADS;
-    for (int kt = 0; kt < nk; ++kt) {
-      if (kt % 2 == 0 && kt + 2 < nk) issue_scales(kt + 2);
-      auto pieces = [&](int from, int to) {
-#pragma unroll
-        for (int q = 0; q < LOADS; ++q)
-          if (q >= from && q < to) {
-            write(q, kt + 1);
-            load(q, kt + 2);
-          }
-      };
-      sc = next;
-      blank(sc, kt);
-      read(f[1], kt, 1);
-      pieces(0, P0);
-      multiply(integral_constant<int, 0>{}, f[0], sc);
-      order(integral_constant<int, TM + NB>{}, integral_constant<int, P0>{});
-      read(f[0], kt, 2);
-      pieces(P0, P1);
-      multiply(integral_constant<int, 1>{}, f[1], sc);
-      order(integral_constant<int, TM + NB>{}, integral_constant<int, P1 - P0>{});
-      read(f[1], kt, 3);
-      pieces(P1, LOADS);
-      multiply(integral_constant<int, 2>{}, f[0], sc);
-      order(integral_constant<int, TM + NB>{}, integral_constant<int, LOADS - P1>{});
-      wait_lgkm0();    // this wavefront's reads of stage kt and writes of stage kt + 1 are done
-      ring_barrier();  // so are all others'
+      Frags f[2];
+      Scales sc, next;
+      issue_scales(0);
       __builtin_amdgcn_sched_barrier(0);
-      read(f[0], kt + 1, 0);
-      read_scales(next, kt + 1);
-      multiply(integral_constant<int, 3>{}, f[1], sc);
-      order(integral_constant<int, 2 * (TM + NB)>{}, integral_constant<int, 0>{});
-    }
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) load(q, 0);
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) write(q, 0);  // (waits for the scales too, which went ahead)
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) load(q, 1);
+      wait_lgkm0();
+      ring_barrier();
+      read(f[0], 0, 0);
+      read_scales(next, 0);
+      constexpr int P0 = (LOADS + 2) / 3, P1 = 2 * P0 < LOADS ? 2 * P0 : LOADS;
+      for (int kt = 0; kt < nk; ++kt) {
+        if (kt % 2 == 0 && kt + 2 < nk) issue_scales(kt + 2);
+        auto pieces = [&](int from, int to) {
+#pragma unroll
+          for (int q = 0; q < LOADS; ++q)
+            if (q >= from && q < to) {
+              write(q, kt + 1);
+              load(q, kt + 2);
+            }
+        };
+        sc = next;
+        blank(sc, kt);
+        read(f[1], kt, 1);
+        pieces(0, P0);
+        multiply(integral_constant<int, 0>{}, f[0], sc);
+        order(integral_constant<int, TM + NB>{}, integral_constant<int, P0>{});
+        read(f[0], kt, 2);
+        pieces(P0, P1);
+        multiply(integral_constant<int, 1>{}, f[1], sc);
+        order(integral_constant<int, TM + NB>{}, integral_constant<int, P1 - P0>{});
+        read(f[1], kt, 3);
+        pieces(P1, LOADS);
+        multiply(integral_constant<int, 2>{}, f[0], sc);
+        order(integral_constant<int, TM + NB>{}, integral_constant<int, LOADS - P1>{});
+        wait_lgkm0();    // this wavefront's reads of stage kt and writes of stage kt + 1 are done
+        ring_barrier();  // so are all others'
+        __builtin_amdgcn_sched_barrier(0);
+        read(f[0], kt + 1, 0);
+        read_scales(next, kt + 1);
+        multiply(integral_constant<int, 3>{}, f[1], sc);
+        order(integral_constant<int, 2 * (TM + NB)>{}, integral_constant<int, 0>{});
+      }
     }
     ring_barrier();
 
@@ -706,10 +707,10 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
   } while (0)
 #define MOE_STREAM(MB_)                                                                                    \
   do {                                                                                                     \
-    if (grouped && dual) MOE_LAUNCH((stream_kernel<MB_, 2, true>), kStreamWaves * 64);                  \
-    if (grouped) MOE_LAUNCH((stream_kernel<MB_, 1, true>), kStreamWaves * 64);                          \
-    if (dual) MOE_LAUNCH((stream_kernel<MB_, 2, false>), kStreamWaves * 64);                            \
-    MOE_LAUNCH((stream_kernel<MB_, 1, false>), kStreamWaves * 64);                                      \
+    if (grouped && dual) MOE_LAUNCH((stream_kernel<MB_, 2, true>), kStreamWaves * 64);                     \
+    if (grouped) MOE_LAUNCH((stream_kernel<MB_, 1, true>), kStreamWaves * 64);                             \
+    if (dual) MOE_LAUNCH((stream_kernel<MB_, 2, false>), kStreamWaves * 64);                               \
+    MOE_LAUNCH((stream_kernel<MB_, 1, false>), kStreamWaves * 64);                                         \
   } while (0)
   auto tiles = [&](int bm, int bn) {
     if (grouped) {
@@ -754,7 +755,7 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
     MOE_LAUNCH((stream_kernel<4, 1, false>), kStreamWaves * 64);
   }
   tiles(kinds[best].bm, kinds[best].bn / mats);
-  if (best == 0) MOE_TILE(256, 256, 256, 2, 4, 2);
+  if (best == 0) MOE_TILE(256, 256, 256, 4, 2, 2);  // (2 x 4 wavefronts: half as long runs of a row to store, 113 us instead of 96 at 4096 x 14336 x 2048)
   if (best == 1) MOE_TILE(256, 128, 128, 4, 2, 3);
   if (best == 2) MOE_TILE(128, 128, 128, 4, 2, 4);
   MOE_TILE(64, 64, 128, 2, 2, 5);

@@ -110,6 +110,22 @@ def test_shapes(T, H, F, E, k, mx, act):
     check_out(out, x, idx, gate, w, E)
 
 
+@pytest.mark.parametrize("T,E,k,given", [(64, 1024, 32, False), (64, 1024, 32, True), (1, 1024, 32, False), (64, 32, 32, True)])
+def test_the_most_tokens_experts_and_choices(T, E, k, given):
+    """The routing lists at their longest."""
+    g = gen(T + E)
+    w = Experts(g, E, 128, 128, "gelu", True)
+    x = torch.randn(T, 128, generator=g).to(BF)
+    l = torch.randn(T, E, generator=g)
+    if given:
+        idx, gate = X.route(l.numpy(), k, True)
+        out, idx, gate = run(x, w, idx=torch.from_numpy(idx.astype(np.int32)), gate=torch.from_numpy(gate).float(), num_experts=E)
+    else:
+        out, idx, gate = run(x, w, l, k)
+        assert np.array_equal(idx, X.route(l.numpy(), k, True)[0])
+    check_out(out, x, idx, gate, w, E)
+
+
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("T", [1, 6, 40, 64])
 @pytest.mark.parametrize("e0,El", [(0, 4), (4, 8), (15, 1)])

@@ -259,6 +259,73 @@ def test_linear_large_tiles(M, N, K, act, dt):
     assert bool(((out.double() - ref).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("M,N,K,act", [
+    (2000, 2100, 384, "none"), (1500, 3800, 1152, "none"), (2001, 1990, 384, "swiglu"),     # 256 x 128
+    (2047, 2040, 896, "none"), (1100, 2001, 512, "none"), (1300, 1301, 640, "swiglu"),      # 128 x 128
+    (65, 8000, 384, "none"), (200, 1500, 2176, "swiglu"),                                   # 64 rows
+    (64, 64, 8192, "none"), (33, 50, 6272, "none"), (49, 40, 8192, "swiglu"),               # streamed, 64 rows
+    (32, 500, 4096, "none"), (17, 333, 7168, "swiglu")])                                    # streamed, 32 rows
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_linear_kinds_of_tiles(M, N, K, act, dt):
+    """Rows and columns that end inside a tile, odd row lengths and half stages at its end, bias and residual; against a
+    float64 product on the device."""
+    g = gen(M + N + K)
+    x, w = packed(g, (M, K), 124, 127), packed(g, (N, K), 119, 122)
+    up = packed(g, (N, K), 119, 122) if act == "swiglu" else None
+    b = torch.randint(-4, 5, (N,), generator=g).float()
+    r = (torch.randint(-64, 65, (M, N), generator=g) / 8).to(dt)
+    out, check = guarded((M, N), dt, -7.0)
+    ffi.moe_linear_mxfp4(on(x), on(w), w_up=on(up), bias=b.to(dev()), act=act, residual=r.to(dev()), out=out)
+    check()
+    v = lambda q: torch.from_numpy(vals(q)).to(dev())  # noqa: E731
+    xv = v(x)
+    z, rd = xv @ v(w).T + b.double().to(dev()), r.double().to(dev())
+    if act == "none":  # (multiples of 2^-13 below 2^11: exact in fp32)
+        ref = z + rd
+        assert torch.equal(out.double(), ref if dt == F32 else ref.to(F32).to(BF).double())
+        return
+    plain = torch.nn.functional.silu(z) * (xv @ v(up).T)
+    tol = 1e-6 * plain.abs() + U2 * (plain + rd).abs() + 1e-30
+    tol = tol + (BF_HALF * ((plain + rd).abs() + tol) if dt == BF else 0)
+    assert bool(((out.double() - plain - rd).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("tile_m,T,k,E,N,K", [(256, 900, 4, 8, 1201, 384), (256, 600, 2, 8, 2100, 640), (256, 4000, 4, 8, 1999, 384),
+                                              (128, 900, 2, 8, 2000, 640), (64, 300, 3, 16, 1500, 1152)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_kinds_of_tiles(tile_m, T, k, E, N, K, act, gather):
+    """Experts whose rows end inside a tile, one without any, at sizes that take the larger tiles; exact where there is no
+    activation."""
+    idx = choice("even", T, E - 1, k, T + N)
+    p = permuted(idx, 0, E, tile_m, K)
+    g = gen(N + K)
+    x, w = packed(g, (T if gather else p.R_cap, K), 124, 127), packed(g, (E, N, K), 119, 122)
+    up = packed(g, (E, N, K), 119, 122) if act == "swiglu" else None
+    out, check = guarded((p.R_cap, N), F32, -7.0)
+    ffi.moe_grouped_linear_mxfp4(p, on(x), on(w), w_up=on(up), act=act, gather=gather, out=out)
+    check()
+    src, off, cnt = (t.cpu().numpy() for t in (p.row_src, p.expert_offsets, p.expert_counts))
+    rows = np.concatenate([np.arange(off[e], off[e] + cnt[e]) for e in range(E)])
+    assert len(rows) == T * k and (cnt == 0).any()
+    untouched = torch.ones(p.R_cap, dtype=torch.bool, device=dev())
+    untouched[torch.from_numpy(rows).to(dev())] = False
+    assert bool((out[untouched] == -7.0).all())
+    v = lambda a: torch.from_numpy(a).to(dev())  # noqa: E731
+    xv = vals(x)
+    for e in range(E):
+        if cnt[e] == 0:
+            continue
+        at = np.arange(off[e], off[e] + cnt[e])
+        xe, got = v(xv[src[at] // k if gather else at]), out[off[e]:off[e] + cnt[e]].double()
+        z = xe @ v(X.values(w.codes[e].numpy(), w.scales[e].numpy())).T
+        if up is None:
+            assert torch.equal(got, z)
+        else:
+            want = torch.nn.functional.silu(z) * (xe @ v(X.values(up.codes[e].numpy(), up.scales[e].numpy())).T)
+            assert bool(((got - want).abs() <= 1e-6 * want.abs() + 1e-30).all())
+
+
 @pytest.mark.parametrize("M", [1, 20, 70, 300])
 @pytest.mark.parametrize("K", [128, 384, 1408])
 def test_linear_nan_and_extreme_scales_stay_in_their_rows(M, K):
