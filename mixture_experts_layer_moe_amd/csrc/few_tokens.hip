@@ -318,9 +318,9 @@ __device__ __forceinline__ void each_step(F f) {
 // An item is an entry's 16 R rows of the gate (and up) matrix; a workgroup's wavefronts take turns at groups of its
 // reduction's units and add up through LDS.
 // Rows: fewer leave enough items for the CUs, more share a load of the tokens.
-constexpr int up_rows(bool fp4, bool wide) { return fp4 || wide ? 2 : 1; }
+constexpr int up_rows(bool fp4, bool wide) { return fp4 && wide ? 4 : fp4 || wide ? 2 : 1; }
 // Workgroups a CU holds: as many as leave the registers that the loads in flight need.
-constexpr int up_per_cu(bool fp4, int nmat, bool wide) { return nmat == 2 && (wide || fp4) ? (wide && !fp4 ? 2 : 3) : 4 - wide; }
+constexpr int up_per_cu(bool fp4, int nmat, bool wide) { return nmat == 2 && (wide || fp4) ? (wide ? 2 : 3) : 4 - wide; }
 
 template <bool FP4, int NMAT, bool WIDE>
 __global__ __launch_bounds__(kUpWaves * 64, up_per_cu(FP4, NMAT, WIDE)) void up_kernel(FewArgs a, bool zero) {
@@ -456,11 +456,9 @@ __device__ __forceinline__ void place_term(u32x4& o, u32x4 t) {
 // at the entries' groups of units, and each adds each group's sums to the tokens' in LDS, a copy for each wavefront, so
 // that the order of additions is fixed.  With S = 2 the two workgroups add to out, which the first launch has cleared:
 // two terms make the same sum in either order.
-constexpr int down_rows(bool fp4) { return fp4 ? 2 : 1; }
-
-template <bool FP4, bool WIDE>
-__global__ __launch_bounds__(kDownWaves * 64, WIDE ? 2 : 4) void down_kernel(FewArgs a, int S) {
-  constexpr int R = down_rows(FP4), D = 2, G = kGroup, PITCH = 16 * R + 4, XL = WIDE ? 4 : 1;
+template <bool FP4, bool WIDE, int R>
+__global__ __launch_bounds__(kDownWaves * 64, WIDE || R == 4 ? 2 : 4) void down_kernel(FewArgs a, int S) {
+  constexpr int D = 2, G = kGroup, PITCH = 16 * R + 4, XL = WIDE ? 4 : 1;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   float* sums = reinterpret_cast<float*>(smem);  // [wavefront][token][PITCH]
   const int each = a.T * PITCH;
@@ -588,6 +586,9 @@ __global__ __launch_bounds__(kDownWaves * 64, WIDE ? 2 : 4) void down_kernel(Few
   }
 }
 
+constexpr size_t kLds = 160 << 10;
+size_t down_sums(int T, int R) { return (size_t)kDownWaves * T * (16 * R + 4) * 4; }
+
 int cu_count() {
   int dev = 0, n = 0;
   if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
@@ -595,9 +596,9 @@ int cu_count() {
   return n;
 }
 
-template <bool FP4, int NMAT, bool WIDE>
+template <bool FP4, int NMAT, bool WIDE, int R2>
 hipError_t launch_both(const FewArgs& a, hipStream_t s) {
-  constexpr int R = up_rows(FP4, WIDE), R2 = down_rows(FP4);
+  constexpr int R = up_rows(FP4, WIDE);
   const size_t lists = lists_bytes(a.T, a.k, a.E_loc);
   const int cus = cu_count();
   // Too few column blocks for two workgroups a CU: half of the reduction each.
@@ -608,14 +609,25 @@ hipError_t launch_both(const FewArgs& a, hipStream_t s) {
                      (size_t)kUpWaves * NMAT * R * 1024 + lists, s, a, S == 2);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((down_kernel<FP4, WIDE>), dim3((unsigned)(columns * S)), dim3(kDownWaves * 64),
-                     (size_t)kDownWaves * a.T * (16 * R2 + 4) * 4 + lists, s, a, S);
+  hipLaunchKernelGGL((down_kernel<FP4, WIDE, R2>), dim3((unsigned)(columns * S)), dim3(kDownWaves * 64),
+                     down_sums(a.T, R2) + lists, s, a, S);
   return hipGetLastError();
 }
 
 template <bool FP4, bool WIDE>
 hipError_t launch(const FewArgs& a, hipStream_t s) {
-  return a.w0_up ? launch_both<FP4, 2, WIDE>(a, s) : launch_both<FP4, 1, WIDE>(a, s);
+  const auto with = [&](auto rows) {
+    constexpr int R = decltype(rows)::value;
+    return a.w0_up ? launch_both<FP4, 2, WIDE, R>(a, s) : launch_both<FP4, 1, WIDE, R>(a, s);
+  };
+  if constexpr (FP4) {
+    // The most rows that leave three CUs in four a workgroup, each half of a block's reduction.
+    const auto enough = [&](int R) { return 2 * (a.H / (16 * R)) >= cu_count() / 4 * 3; };
+    if constexpr (!WIDE)
+      if (enough(4) && down_sums(a.T, 4) + lists_bytes(a.T, a.k, a.E_loc) <= kLds) return with(std::integral_constant<int, 4>{});
+    if (enough(2)) return with(std::integral_constant<int, 2>{});
+  }
+  return with(std::integral_constant<int, 1>{});
 }
 
 }  // namespace

@@ -126,6 +126,31 @@ def test_the_most_tokens_experts_and_choices(T, E, k, given):
     check_out(out, x, idx, gate, w, E)
 
 
+@pytest.mark.parametrize("T,H,F,E,k", [(5, 4096, 256, 16, 3), (40, 4096, 128, 4, 2), (9, 7168, 384, 16, 4), (64, 8192, 128, 64, 8),
+                                       (30, 7168, 256, 8, 3), (2, 6144, 1408, 4, 2)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_long_rows(T, H, F, E, k, mx):
+    """Lengths of out that take more columns a workgroup."""
+    g = gen(T + H)
+    w = Experts(g, E, H, F, "swiglu", mx)
+    x = torch.randn(T, H, generator=g).to(BF)
+    out, idx, gate = run(x, w, torch.randn(T, E, generator=g), k)
+    check_out(out, x, idx, gate, w, E)
+
+
+def test_long_rows_beside_the_longest_lists():
+    """A share of many experts: the lists leave less room for the sums."""
+    T, H, E, El, k = 64, 8192, 704, 4, 32
+    g = gen(0)
+    w = Experts(g, El, H, 128, "gelu", True)
+    x = torch.randn(T, H, generator=g).to(BF)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    idx[:, 5] = torch.arange(T) % 5 + 100
+    gate = torch.rand(T, k, generator=g)
+    out, i2, g2 = run(x, w, idx=idx, gate=gate, expert_begin=100, num_experts=E)
+    check_out(out, x, i2, g2, w, El, 100)
+
+
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("T", [1, 6, 40, 64])
 @pytest.mark.parametrize("e0,El", [(0, 4), (4, 8), (15, 1)])
