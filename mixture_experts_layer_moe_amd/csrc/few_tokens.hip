@@ -1,4 +1,5 @@
-// A whole MoE layer for a few tokens (at most 64) in two launches, over bf16 or MXFP4 experts.
+// A whole MoE layer for a few tokens (at most 64) in two launches (three with more than four tokens to route), over bf16
+// or MXFP4 experts.
 //
 //   up    routes the tokens (or takes their experts), then a[t, e] = act(x_t W0_e (, x_t W0up_e)) * g(t, e)
 //   down  out_t = sum over the token's local experts e of a[t, e] W1_e
@@ -153,6 +154,12 @@ __device__ __forceinline__ void route_row(const float* row, int E, int k, bool r
     idx[lane] = mine;
     w[lane] = mine >= 0 ? mine_v / sum : 0.f;
   }
+}
+
+// A wavefront a token: the latency of its loads and of k searches one after another.
+__global__ __launch_bounds__(64) void route_kernel(FewArgs a) {
+  const int t = blockIdx.x;
+  route_row(a.logits + (int64_t)t * a.E, a.E, a.k, a.renormalize, a.topk_idx + t * a.k, a.topk_w + t * a.k);
 }
 
 // Fills the lists; the whole workgroup takes part.  out: the workgroup that hands the routing's results out.
@@ -586,7 +593,7 @@ __global__ __launch_bounds__(kDownWaves * 64, WIDE || R == 4 ? 2 : 4) void down_
   }
 }
 
-constexpr size_t kLds = 160 << 10;
+constexpr size_t kLds = 160 << 10;  // of a workgroup
 size_t down_sums(int T, int R) { return (size_t)kDownWaves * T * (16 * R + 4) * 4; }
 
 int cu_count() {
@@ -621,7 +628,9 @@ hipError_t launch(const FewArgs& a, hipStream_t s) {
     return a.w0_up ? launch_both<FP4, 2, WIDE, R>(a, s) : launch_both<FP4, 1, WIDE, R>(a, s);
   };
   if constexpr (FP4) {
-    // The most rows that leave three CUs in four a workgroup, each half of a block's reduction.
+    // The most rows (fewer loads of the activations) that leave three CUs in four a workgroup, each half of a block's
+    // reduction: four instead of two for out of 7168 1237 us, 1315 (64 tokens, 256 experts of 2048), but of 4096 358 us, 290
+    // (32 tokens, 128 experts of 2048); one instead of two for out of 2048 86 us, 95 (16 tokens, 64 experts of 1408).
     const auto enough = [&](int R) { return 2 * (a.H / (16 * R)) >= cu_count() / 4 * 3; };
     if constexpr (!WIDE)
       if (enough(4) && down_sums(a.T, 4) + lists_bytes(a.T, a.k, a.E_loc) <= kLds) return with(std::integral_constant<int, 4>{});
@@ -634,7 +643,17 @@ hipError_t launch(const FewArgs& a, hipStream_t s) {
 
 size_t few_tokens_ws_bytes(int T, int k, int F) { return (size_t)T * k * F * 4; }
 
-hipError_t launch_few_tokens(const FewArgs& a, hipStream_t s) {
+hipError_t launch_few_tokens(const FewArgs& args, hipStream_t s) {
+  FewArgs a = args;
+  // Every workgroup of the first launch routes for itself, a wavefront a token, if each has one token at most (four tokens
+  // of 2048 x 1408 over 64 experts 76.0 us, 77.7 with a launch for it).  More are routed by a launch of their own, 8 us
+  // (64 tokens of 7168 x 2048 over 256 experts 1141 us, 1236 without it; 5 tokens of 2048 x 1408 88.3, 89.3).
+  if (a.logits && a.T > kUpWaves) {
+    hipLaunchKernelGGL(route_kernel, dim3((unsigned)a.T), dim3(64), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.logits = nullptr;
+  }
   // The wide form where experts have more than three tokens on average.
   const bool wide = a.T > kNarrow && a.T * a.k > 3 * a.E;
   if (a.s0) return wide ? launch<true, true>(a, s) : launch<true, false>(a, s);

@@ -85,17 +85,19 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const u32x4* __restr
   }
 }
 
+// A lane stores 16 bytes, side by side with its neighbours': eight values in bf16, four in fp32 (eight, as two stores of
+// 16 bytes in each 32, 11.0 us instead of 8.1 at 5003 x 1440).
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint32_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales, int64_t units,
-                                                              u32x4* __restrict__ out) {
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const void* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                              int64_t units, u32x4* __restrict__ out) {
   const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
   uint32_t c[kUnits], s[kUnits];
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
     const int64_t u = u0 + q * kThreads;
-    c[q] = u < units ? codes[u] : 0;
-    s[q] = u < units ? scales[u >> 2] : 0;
+    if constexpr (F32) c[q] = u < units ? static_cast<const uint16_t*>(codes)[u] : 0;
+    else c[q] = u < units ? static_cast<const uint32_t*>(codes)[u] : 0;
+    s[q] = u < units ? scales[u >> (F32 ? 3 : 2)] : 0;
   }
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
@@ -104,9 +106,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint32_t* __
     const float scale = scale_of(s[q]);
     if constexpr (F32) {
       const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 1);
-      const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 3);
-      out[2 * u] = __builtin_bit_cast(u32x4, floatx4{a.x, a.y, b.x, b.y});
-      out[2 * u + 1] = __builtin_bit_cast(u32x4, floatx4{d.x, d.y, e.x, e.y});
+      out[u] = __builtin_bit_cast(u32x4, floatx4{a.x, a.y, b.x, b.y});
     } else {
       // (every value has two significant bits: exact in bf16, subnormal ones included)
       const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 1);
@@ -131,12 +131,11 @@ hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t blocks, uint8_
 
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, bool f32, void* out,
                                    hipStream_t s) {
-  const int64_t units = blocks * 4;
+  const int64_t units = blocks * (f32 ? 8 : 4);
   const dim3 grid((unsigned)((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
-  const uint32_t* src = reinterpret_cast<const uint32_t*>(codes);
   u32x4* dst = static_cast<u32x4*>(out);
-  if (f32) hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, s, src, scales, units, dst);
-  else hipLaunchKernelGGL(dequantize_kernel<false>, grid, dim3(kThreads), 0, s, src, scales, units, dst);
+  if (f32) hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, s, codes, scales, units, dst);
+  else hipLaunchKernelGGL(dequantize_kernel<false>, grid, dim3(kThreads), 0, s, codes, scales, units, dst);
   return hipGetLastError();
 }
 
