@@ -37,7 +37,7 @@
  *                               moe_linear, and the experts' products, of two
  *                               such operands
  *   moe_few_tokens              the whole layer for at most 64 tokens in two
- *                               launches, over bf16 or 4-bit experts
+ *                               or three launches, over bf16 or 4-bit experts
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer unless stated otherwise, and
@@ -518,7 +518,7 @@ moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R
                                 void* stream);
 
 /* Bytes of the optional device workspace of moe_linear_mxfp4 on the current
- * device (0 when this size needs none; 0 on invalid arguments). */
+ * device: 0, no size uses one at present (0 on invalid arguments, too). */
 size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
 
 /*
@@ -536,12 +536,11 @@ size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t
  * residual are fp32; each output is rounded once.  Results are deterministic.
  * out and ws must not overlap the inputs or one another (checked; residual ==
  * out excepted).
- * ws / ws_bytes: optional device scratch (NULL / 0 is allowed) of at least
- * moe_linear_mxfp4_workspace_bytes(), which small products split their
- * reduction into; a non-NULL ws that is too small returns MOE_ERR_WORKSPACE.
- * Requires K % 128 == 0; N, K <= 1048576; M <= 2^31 - 1, and at most 4 million
- * tiles of 128 rows and 128 columns (SwiGLU: 64; up to 64 rows: 16 columns);
- * more may return MOE_ERR_UNSUPPORTED.  M == 0: nothing to do.
+ * ws / ws_bytes: device scratch of at least moe_linear_mxfp4_workspace_bytes()
+ * (NULL / 0 is allowed, as for moe_linear).
+ * Requires K % 128 == 0; N, K <= 1048576; M <= 2^31 - 1; products of more than
+ * 4 million blocks of 64 rows and 64 columns may return MOE_ERR_UNSUPPORTED.
+ * M == 0: nothing to do.
  */
 moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
                             const void* w_up_codes, const void* w_up_scales, const float* bias, const float* bias_up,
@@ -565,9 +564,9 @@ moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const voi
  * moe_linear's.  Arithmetic as in moe_linear_mxfp4.  out must not overlap an
  * input (checked).
  * Requires K % 128 == 0; N, K <= 1048576; tile_m in {16, 32, 64, 128, 256};
- * k <= 32 and T * K / 2 <= 2^31 - 1 where rows are gathered; at most 4 million
- * tiles of tile_m (at most 128) rows and 64 columns (tile_m <= 64: 16); more
- * may return MOE_ERR_UNSUPPORTED.
+ * k <= 32 and T * K / 2 <= 2^31 - 1 where rows are gathered; capacities of
+ * more than 4 million blocks of tile_m (at most 64) rows and 64 columns
+ * (tile_m < 64: 16) may return MOE_ERR_UNSUPPORTED.
  */
 moe_status moe_grouped_linear_mxfp4(const void* x_codes, const void* x_scales, const int32_t* row_src, int64_t T, int32_t k,
                                     const int32_t* expert_counts, const int32_t* expert_offsets, const int32_t* tiles,
@@ -585,7 +584,8 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int32_t k, int32_t F);
 
 /*
  * moe_few_tokens -- routing, experts and combine of at most 64 tokens in two
- * launches, each chosen expert's weights read once:
+ * launches (three with logits of more than four tokens), each chosen expert's
+ * weights read once for every 4 or 16 of its tokens:
  *
  *   a[t, e] = act(x[t] . W0[e]^T (, x[t] . W0up[e]^T))           moe_grouped_ffn's activations
  *   out[t, :] = sum over the token's chosen local experts e of g[t, e] * (a[t, e] . W1[e]^T)
@@ -602,9 +602,8 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int32_t k, int32_t F);
  *             the three *_scales NULL; or MXFP4 codes [.., / 2] with their scales [.., / 32]
  *   out       [T, H] fp32 out
  * Weights enter the products exactly, accumulation is fp32, and activations
- * keep 16 bits of mantissa between the two products.  Results are
- * deterministic.  Outputs and ws must not overlap the inputs or one another
- * (checked).
+ * stay in fp32 between the two products.  Results are deterministic.  Outputs
+ * and ws must not overlap the inputs or one another (checked).
  * ws / ws_bytes: device scratch of at least moe_few_tokens_workspace_bytes();
  * nothing in it has to start at zero or is kept for the next call.
  * Requires T <= 64, E <= 1024, k <= 32, H % 128 == 0, F % 128 == 0,

@@ -766,8 +766,6 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
 
 }  // namespace
 
-size_t linear_mxfp4_ws_bytes(int64_t, int, int, int) { return 0; }
-
 hipError_t launch_linear_mxfp4(const MxLinearArgs& a, hipStream_t s) { return launch(Product{a, 0, 0, 1}, false, s); }
 
 hipError_t launch_grouped_linear_mxfp4(const MxLinearArgs& a, hipStream_t s) { return launch(Product{a, 0, 0, 1}, true, s); }

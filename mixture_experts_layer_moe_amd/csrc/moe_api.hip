@@ -532,10 +532,8 @@ moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R
                                                R * (K / 32), out_dtype == MOE_F32, out, static_cast<hipStream_t>(stream)));
 }
 
-size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act) {
-  if (M < 0 || M > INT32_MAX || mxfp4_sizes(N, K, act) != MOE_OK) return 0;
-  return moe::linear_mxfp4_ws_bytes(M, N, K, act);
-}
+// (no size splits its reduction)
+size_t moe_linear_mxfp4_workspace_bytes(int64_t, int32_t, int32_t, int32_t) { return 0; }
 
 moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
                             const void* w_up_codes, const void* w_up_scales, const float* bias, const float* bias_up,
@@ -553,7 +551,6 @@ moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const voi
   const void* ptrs[] = {x_codes, x_scales, w_codes, w_scales, w_up_codes, w_up_scales, bias, bias_up, residual, out, ws};
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
-  if (ws && ws_bytes < moe::linear_mxfp4_ws_bytes(M, N, K, act)) return MOE_ERR_WORKSPACE;
   const size_t mn = (size_t)M * N * (out_dtype == MOE_F32 ? 4 : 2), mk = (size_t)M * K, nk = (size_t)N * K, nb = (size_t)N * 4;
   const Span outs[] = {{out, mn}, {ws, ws_bytes}};
   const Span ins[] = {{x_codes, mk / 2}, {x_scales, mk / 32}, {w_codes, nk / 2}, {w_scales, nk / 32}, {w_up_codes, nk / 2},
@@ -572,7 +569,6 @@ moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const voi
   a.act = act;
   a.out_f32 = out_dtype == MOE_F32;
   a.out = out;
-  a.ws = ws;
   return linear_launched(moe::launch_linear_mxfp4(a, static_cast<hipStream_t>(stream)));
 }
 

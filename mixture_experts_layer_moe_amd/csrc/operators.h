@@ -83,13 +83,11 @@ struct MxLinearArgs {
   int N, K, act;
   bool out_f32;
   void* out;
-  void* ws;
   // Grouped: row tiles of the permutation (counts null: dense).
   const int32_t *counts, *offsets, *tiles, *num_tiles, *row_src;  // row_src null: x's rows are the permuted ones
   int topk, tile_m;
   int64_t tiles_cap, R_cap;
 };
-size_t linear_mxfp4_ws_bytes(int64_t M, int N, int K, int act);
 hipError_t launch_linear_mxfp4(const MxLinearArgs& a, hipStream_t s);
 hipError_t launch_grouped_linear_mxfp4(const MxLinearArgs& a, hipStream_t s);
 
