@@ -201,11 +201,16 @@ __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
 
 // BM rows by BN columns (NMAT = 2: BN of each matrix), WM x WN wavefronts.
 //
-// Two LDS buffers and register-staged codes: while a stage of 256 reduction indices (128 bytes a row: whole cache lines)
-// is multiplied from one buffer, the next stage goes from registers into the other and the registers reload with the one
-// after it.  A stage is four steps, each a matrix instruction of 64 indices per accumulator; a step's fragments are read
+// Codes staged in registers, two LDS buffers (NS = 2): while a stage of 256 reduction indices (128 bytes a row: whole
+// cache lines) is multiplied from one buffer, the next stage goes from registers into the other and the registers reload
+// with the one after it.  A stage is four steps, each a matrix instruction of 64 indices per accumulator; a step's fragments are read
 // during the step before, and the writes and loads are spread over the first three.  When the last step begins the
-// stage has been read: there the workgroup synchronises, and the last step reads the next stage's first fragments.
+// stage has been read: there the workgroup synchronises, and the last step reads the next stage's first fragments.  The
+// 128 x 128 tile takes 72 KB, so that two share a CU: 93 us at 4096 x 14336 x 2048, 131 in a ring of four stages.
+//
+// A ring of NS > 2 stages straight to LDS, for the smallest tiles, whose time is the latency of their stages: 64 x 64 takes
+// 15.0 us at 128 x 4096 x 8192, 24.9 with staged codes.  Three stages, so that two or three tiles share a CU (five: 65 us
+// instead of 51 for gate and up products of 64 experts, 1408 x 2048, with 48 rows each).
 //
 // The scales go straight to LDS for two stages at a time, 16 bytes a row: a row's bytes of one stage would each time be
 // an access of their own to the row's cache line, nearly as many as the codes need (340 us instead of 294 at
@@ -724,20 +729,34 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
   };
   const int mats = dual ? 2 : 1;
   const int nk = (p.a.K + kStage - 1) / kStage;
-  // Tiles: the kind whose rounds over the CUs take least.  A round is a tile's stages and what comes before and after
-  // them, in us as measured on products that fill every CU once (fp32 and bf16 outputs, 4 to 32 stages).
+  // Tiles: the kind that takes least, in us as fitted to 77 products of 64 to 49152 rows, 512 to 14336 indices, bf16 and
+  // fp32 outputs (its choice is 0.2 % above the best kind on average, 6 % at most).  A CU holds one of the two large kinds
+  // at a time, which run in whole rounds.  It holds two or three of the small ones: rounds run into each other, and their
+  // stages overlap but for the latency of a tile alone.
   struct Kind {
     int bm, bn;
-    float stage, fixed;
+    bool whole;
+    float stage, tile, alone, out16, out32, fixed;  // us a stage, a tile, a stage of one tile alone, a MB of out, a launch
   };
-  const Kind kinds[] = {{256, 256, 2.0f, 11.f}, {256, 128, 1.22f, 9.5f}, {128, 128, 0.86f, 5.4f}, {64, dual ? 128 : 64, dual ? 0.45f : 0.31f, 4.f}};
+  const Kind kinds[] = {{256, 256, true, 1.37f, 7.8f, 0.f, 0.15f, 0.18f, 1.8f},
+                        {256, 128, true, 0.94f, 4.1f, 0.f, 0.16f, 0.19f, 2.4f},
+                        {128, 128, false, 0.68f, 0.5f, 0.62f, 0.095f, 0.15f, 5.6f},
+                        {64, dual ? 128 : 64, false, dual ? 0.42f : 0.23f, 0.f, dual ? 0.5f : 0.3f, 0.34f, 0.24f, 4.6f}};
+  const float out_rows = (float)(grouped ? p.a.tiles_cap * rows : rows);
+  const float out_mb = out_rows * p.a.N * (p.a.out_f32 ? 4e-6f : 2e-6f) * (p.a.residual ? 2 : 1);
   int best = 3;
   float least = 0.f;
   for (int i = 3; i >= 0; --i) {
-    if (kinds[i].bm > rows && i < 3) continue;
-    tiles(kinds[i].bm, kinds[i].bn / mats);
-    const float t = ((int64_t)p.mt * p.nt + kCus - 1) / kCus * (nk * kinds[i].stage + kinds[i].fixed);
-    if (i == 3 || t < least) {
+    const Kind& k = kinds[i];
+    if (k.bm > rows && i < 3) continue;
+    tiles(k.bm, k.bn / mats);
+    const int64_t n = (int64_t)p.mt * p.nt;
+    const float x = (float)n / kCus, up = (float)((n + kCus - 1) / kCus), rounds = k.whole ? up : 0.5f * (x + up);
+    const float work = rounds * (nk * k.stage + k.tile), alone = nk * k.alone;
+    const float t = (work > alone ? work : alone) + out_mb * (p.a.out_f32 ? k.out32 : k.out16) + k.fixed;
+    // Grouped, a capacity of at least a round takes the largest square tiles that fit tile_m (64 experts with 192 rows each,
+    // 2048 x 1408, fp32, tile_m 256: 70 us, 86 in tiles of 128; the capacity says little about the tiles that have rows).
+    if (i == 3 || t < least || (grouped && i != 1 && x >= 1.f)) {
       best = i;
       least = t;
     }
@@ -745,8 +764,8 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
   // Few rows: streamed where that takes less, us by the megabyte of codes as measured on 29 MB (17 rows of 4096 x 14336
   // 11.7 us, 20.8 in tiles; of 14336 x 4096 13.3, 10.2 in tiles).  Grouped, tiles are never cut below 64 rows.
   const float mb_codes = (float)p.a.N * p.a.K * mats * 0.5e-6f;
-  if (rows <= 16 || (grouped && rows < 64) || (!grouped && rows <= 32 && 4.f + 0.38f * mb_codes < least) ||
-      (!grouped && rows <= 64 && 5.f + 0.65f * mb_codes < least)) {
+  if (rows <= 16 || (grouped && rows < 64) || (!grouped && rows <= 32 && 5.f + 0.38f * mb_codes < least) ||
+      (!grouped && rows <= 64 && 6.f + 0.65f * mb_codes < least)) {
     const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     tiles(16 * mb, 16);
     if (mb == 1) MOE_STREAM(1);
@@ -756,9 +775,9 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
   }
   tiles(kinds[best].bm, kinds[best].bn / mats);
   if (best == 0) MOE_TILE(256, 256, 256, 4, 2, 2);  // (2 x 4 wavefronts: half as long runs of a row to store, 113 us instead of 96 at 4096 x 14336 x 2048)
-  if (best == 1) MOE_TILE(256, 128, 128, 4, 2, 3);
-  if (best == 2) MOE_TILE(128, 128, 128, 4, 2, 4);
-  MOE_TILE(64, 64, 128, 2, 2, 5);
+  if (best == 1) MOE_TILE(256, 128, 128, 4, 2, 2);
+  if (best == 2) MOE_TILE(128, 128, 128, 4, 2, 2);
+  MOE_TILE(64, 64, 128, 2, 2, 3);
 #undef MOE_LAUNCH
 #undef MOE_TILE
 #undef MOE_STREAM

@@ -260,8 +260,10 @@ def test_linear_large_tiles(M, N, K, act, dt):
 
 
 @pytest.mark.parametrize("M,N,K,act", [
-    (2000, 2100, 384, "none"), (1500, 3800, 1152, "none"), (2001, 1990, 384, "swiglu"),     # 256 x 128
+    (4000, 3990, 1152, "none"), (2001, 3991, 1152, "swiglu"),                               # 256 x 256
+    (1500, 3801, 2176, "none"), (900, 2816, 2944, "swiglu"),                                # 256 x 128
     (2047, 2040, 896, "none"), (1100, 2001, 512, "none"), (1300, 1301, 640, "swiglu"),      # 128 x 128
+    (2000, 2100, 384, "none"), (2001, 1990, 384, "swiglu"),                                 # several to a CU
     (65, 8000, 384, "none"), (200, 1500, 2176, "swiglu"),                                   # 64 rows
     (64, 64, 8192, "none"), (33, 50, 6272, "none"), (49, 40, 8192, "swiglu"),               # streamed, 64 rows
     (32, 500, 4096, "none"), (17, 333, 7168, "swiglu")])                                    # streamed, 32 rows
@@ -291,6 +293,7 @@ def test_linear_kinds_of_tiles(M, N, K, act, dt):
 
 
 @pytest.mark.parametrize("tile_m,T,k,E,N,K", [(256, 900, 4, 8, 1201, 384), (256, 600, 2, 8, 2100, 640), (256, 4000, 4, 8, 1999, 384),
+                                              (256, 150, 2, 8, 1500, 1152), (256, 200, 2, 8, 2001, 2176),
                                               (128, 900, 2, 8, 2000, 640), (64, 300, 3, 16, 1500, 1152)])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 @pytest.mark.parametrize("gather", [True, False])
