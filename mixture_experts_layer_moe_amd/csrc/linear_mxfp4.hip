@@ -774,7 +774,8 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
     MOE_LAUNCH((stream_kernel<4, 1, false>), kStreamWaves * 64);
   }
   tiles(kinds[best].bm, kinds[best].bn / mats);
-  if (best == 0) MOE_TILE(256, 256, 256, 4, 2, 2);  // (2 x 4 wavefronts: half as long runs of a row to store, 113 us instead of 96 at 4096 x 14336 x 2048)
+  // (2 x 4 wavefronts have half as long runs of a row to store: 113 us instead of 96 at 4096 x 14336 x 2048)
+  if (best == 0) MOE_TILE(256, 256, 256, 4, 2, 2);
   if (best == 1) MOE_TILE(256, 128, 128, 4, 2, 2);
   if (best == 2) MOE_TILE(128, 128, 128, 4, 2, 2);
   MOE_TILE(64, 64, 128, 2, 2, 3);
