@@ -8,7 +8,7 @@
 // experts' weights: every weight is loaded once for four (or 16) of its expert's tokens, straight into the matrix
 // instructions' registers, by as many wavefronts as it takes to keep HBM busy; nothing is permuted and no row is padded to
 // a tile.  Measured: 4.5 TB/s of the chosen experts' weights with 64 tokens over 256 MXFP4 experts of 7168 x 2048 (1141
-// us), 4.7 to 5.6 with 13 over 8 bf16 experts of 4096 x 2048 (58 to 70 us); 33 us for one token of 2048 x 1408, six
+// us), 4.7 to 5.6 with 13 over 8 bf16 experts of 4096 x 2048 (58 to 70 us); 32 us for one token of 2048 x 1408, six
 // experts, of which the dependent steps before the first weights are 4 to 5 us a launch.
 //
 // v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and tokens on its 16 columns: a column's result depends on
@@ -181,6 +181,39 @@ __device__ __forceinline__ Lists make_lists(const FewArgs& a, const float* logit
   int32_t* total = reinterpret_cast<int32_t*>(l.w + pairs);
   int32_t* twice = total + 1;  // some token's choice names an expert twice
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // One token: a lane a slot of one wavefront, entries in slot order, without the steps between workgroup barriers (56.6 us
+  // instead of 59.2 for 8 of 256 MXFP4 experts of 7168 x 2048).
+  if (a.T == 1) {
+    if (wave == 0) {
+      if (logits) route_row(logits, a.E, a.k, a.renormalize, l.idx, l.w);
+      const int id = lane >= a.k ? -1 : logits ? l.idx[lane] : a.topk_idx[lane];
+      const float own = lane >= a.k ? 0.f : logits ? l.w[lane] : a.topk_w[lane];
+      const uint32_t e = (uint32_t)id - (uint32_t)a.expert_begin;
+      bool first = id >= 0 && e < (uint32_t)a.E_loc;
+      float w = own;
+      for (int q = 0; q < a.k; ++q) {  // (a choice that names an expert twice has both weights in one row)
+        const bool same = __builtin_amdgcn_readlane(id, q) == id;
+        first = first && !(same && q < lane);
+        if (same && q > lane) w += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, own), q));
+      }
+      const uint64_t firsts = __ballot(first);
+      if (first) {
+        const int r = __popcll(firsts & ((1ull << lane) - 1));
+        l.entry[r] = e | 1u << 16;
+        l.row[r] = r;
+        l.token[r] = 0;
+        l.gate[r] = w;
+      }
+      if (lane == 0) *total = __popcll(firsts);
+      if (logits && out && lane < a.k) {
+        a.topk_idx[lane] = id;
+        a.topk_w[lane] = own;
+      }
+    }
+    __syncthreads();
+    l.n = *total;
+    return l;
+  }
   for (int e = tid; e < a.E_loc; e += THREADS) l.mask[e] = 0;
   if (tid == 0) *twice = 0;
   if (logits) {
