@@ -101,21 +101,39 @@ __device__ __forceinline__ void load_values(const void* p, int64_t at, int left,
   }
 }
 
+// through: the stores pass the caches by.  Where a wavefront writes whole lines that is faster (grouped, 49152 rows of 2048
+// x 1408 in fp32 169 us instead of 187; also with the output read again at once), where rows begin inside a line slower
+// (4096 x 4095 x 1024 in bf16 26 us instead of 22), and for a streamed product's 32 bytes a row too.
 template <int V, bool F32>
-__device__ __forceinline__ void store_values(void* p, int64_t at, int left, const float (&v)[V]) {
+__device__ __forceinline__ void store_values(void* p, int64_t at, int left, const float (&v)[V], bool through) {
   if (left >= V) {
     if constexpr (F32) {
       typedef words<4> quad __attribute__((aligned(4)));
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        *reinterpret_cast<quad*>(static_cast<float*>(p) + at + i) =
-            __builtin_bit_cast(words<4>, floatx4{v[i], v[i + 1], v[i + 2], v[i + 3]});
+      for (int i = 0; i < V; i += 4) {
+        quad* to = reinterpret_cast<quad*>(static_cast<float*>(p) + at + i);
+        const words<4> q = __builtin_bit_cast(words<4>, floatx4{v[i], v[i + 1], v[i + 2], v[i + 3]});
+        if (through) {
+          asm volatile("");  // (keeps the compiler from making one ordinary store of the two)
+          __builtin_nontemporal_store(q, to);
+          asm volatile("");
+        } else {
+          *to = q;
+        }
+      }
     } else {
       typedef words<V / 2> halves __attribute__((aligned(2)));
       words<V / 2> h;
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) h[e] = (uint32_t)f2bf_bits(v[2 * e]) | ((uint32_t)f2bf_bits(v[2 * e + 1]) << 16);
-      *reinterpret_cast<halves*>(static_cast<uint16_t*>(p) + at) = h;
+      halves* to = reinterpret_cast<halves*>(static_cast<uint16_t*>(p) + at);
+      if (through) {
+        asm volatile("");
+        __builtin_nontemporal_store(h, to);
+        asm volatile("");
+      } else {
+        *to = h;
+      }
     }
   } else {
 #pragma unroll
@@ -152,7 +170,7 @@ __device__ __forceinline__ void activate_row(int act, float (&z)[V], const float
 // The epilogue of C rows, V columns each from column n: sums(c, z, u) gives row c's, row(c) its index in out, or -1
 // where there is none.  The rows' residuals are loaded together, ahead of the first store.
 template <int V, bool F32, int C, typename Sums, typename Row>
-__device__ __forceinline__ void finish(const MxLinearArgs& a, int n, Sums sums, Row row) {
+__device__ __forceinline__ void finish(const MxLinearArgs& a, int n, bool through, Sums sums, Row row) {
   const int left = a.N - n;  // columns that exist
   if (left <= 0) return;
   float bz[V], bu[V], res[C][V];
@@ -173,7 +191,7 @@ __device__ __forceinline__ void finish(const MxLinearArgs& a, int n, Sums sums, 
     if (a.residual)
 #pragma unroll
       for (int i = 0; i < V; ++i) z[i] += res[c][i];
-    store_values<V, F32>(a.out, row(c) * a.N + n, left, z);
+    store_values<V, F32>(a.out, row(c) * a.N + n, left, z, through);
   }
 }
 
@@ -210,7 +228,7 @@ __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
 //
 // Bound: LDS.  A stage of the 256 x 256 tile reads 192 KB and writes 64, 2050 cycles at 128 bytes a cycle of the 2700 it
 // takes; its matrix instructions take 1020 of each SIMD.  Measured: 8192 x 8192 x 8192 282 us (3.9 PFLOP/s), 4096 x 14336 x
-// 4096 SwiGLU 261 to 281 us (3.4 to 3.7).
+// 4096 SwiGLU 258 to 270 us (3.6 to 3.7).
 //
 // A ring of NS > 2 stages straight to LDS, for the smallest tiles, whose time is the latency of their stages: 64 x 64 takes
 // 15.0 us at 128 x 4096 x 8192, 24.9 with staged codes.  Three stages, so that two or three tiles share a CU (five: 65 us
@@ -508,7 +526,7 @@ struct Tile {
     constexpr int LPR = WT_N / V, STEP = 64 / LPR, C = 32 / STEP;  // lanes a row, rows at a time
     const int c0 = lane % LPR * V, r = lane / LPR;
     finish<V, F32, C>(
-        a, n0 + c0,
+        a, n0 + c0, a.N % (F32 ? 16 : 32) == 0,
         [&](int c, float (&z)[V], float (&u)[V]) {
           const float* s = sm + (r + c * STEP) * PITCH + c0;
 #pragma unroll
@@ -683,8 +701,8 @@ __device__ __forceinline__ void stream_rows(const Product& p, const Rows& rw, in
       }
     };
     auto row = [&](int) -> int64_t { return r < rw.valid ? rw.row0 + r : -1; };
-    if (a.out_f32) finish<4, true, 1>(a, n0 + g * 4, sums, row);
-    else finish<4, false, 1>(a, n0 + g * 4, sums, row);
+    if (a.out_f32) finish<4, true, 1>(a, n0 + g * 4, false, sums, row);
+    else finish<4, false, 1>(a, n0 + g * 4, false, sums, row);
   }
 }
 
