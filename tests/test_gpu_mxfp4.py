@@ -235,7 +235,7 @@ def test_linear_epilogues(M, N, K, act, dt):
                                        (2048, 4096, 256, "gelu")])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_linear_large_tiles(M, N, K, act, dt):
-    """Products that fill the card with 256 x 256 tiles, against a float64 product on the device."""
+    """Products that fill the card, against a float64 product on the device."""
     g = gen(M + N)
     x, w = packed(g, (M, K), 124, 127), packed(g, (N, K), 119, 122)
     up = packed(g, (N, K), 119, 122) if act == "swiglu" else None
