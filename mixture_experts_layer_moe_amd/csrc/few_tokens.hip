@@ -463,7 +463,8 @@ __global__ __launch_bounds__(kUpWaves * 64, up_per_cu(FP4, NMAT, WIDE)) void up_
 // ---------------------------------------------------------------------------
 // Second launch
 // ---------------------------------------------------------------------------
-// Eight activations as three bf16 terms whose sum they are.  (An infinity or NaN is all in its first term.)
+// Eight activations as three bf16 terms whose sum they are, each of the activation's sign.  The first is zero, infinite or
+// NaN where the activation is; what the others are then does not count (with_rest).
 struct Terms {
   u32x4 t[kTerms];
 };
@@ -477,12 +478,18 @@ __device__ __forceinline__ Terms split(floatx4 lo, floatx4 hi) {
       const uint32_t b0 = __builtin_bit_cast(uint32_t, a[0]), b1 = __builtin_bit_cast(uint32_t, a[1]);
       o.t[c][i >> 1] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);  // the upper halves
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float d = a[e] - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, a[e]) & 0xffff0000u);
-        a[e] = c == 0 && !(fabsf(a[e]) < __builtin_inff()) ? 0.f : d;
-      }
+      for (int e = 0; e < 2; ++e) a[e] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, a[e]) & 0xffff0000u);
     }
   }
+  return o;
+}
+
+// Sums of the first terms' products and of the others'.  Where the first terms' is an infinity or NaN it is the result: an
+// infinite weight, or activation, makes NaN of a later term that is zero (an activation of few bits), or of inf - inf.
+__device__ __forceinline__ floatx4 with_rest(floatx4 first, floatx4 rest) {
+  floatx4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = fabsf(first[i]) < __builtin_inff() ? rest[i] + first[i] : first[i];
   return o;
 }
 
@@ -566,9 +573,12 @@ __global__ __launch_bounds__(kDownWaves * 64, WIDE || R == 4 ? 2 : 4) void down_
     const Group ahead = group(i + kDownWaves);
     sc = next;
     load_scales(next, ahead);
-    floatx4 acc[R];
+    floatx4 acc[R], rest[WIDE ? R : 1];  // wide: the first terms' sums, the others' (narrow: columns of one)
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < R; ++r) {
+      acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (WIDE) rest[r] = acc[r];
+    }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       Terms t;
@@ -591,8 +601,10 @@ __global__ __launch_bounds__(kDownWaves * 64, WIDE || R == 4 ? 2 : 4) void down_
           const bf16x8 f = w[j % D][r].get(T, scales);
           if constexpr (WIDE) {
 #pragma unroll
-            for (int c = 0; c < kTerms; ++c)
-              acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, t.t[c]), acc[r], 0, 0, 0);
+            for (int c = 0; c < kTerms; ++c) {
+              floatx4& to = c == 0 ? acc[r] : rest[r];
+              to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, t.t[c]), to, 0, 0, 0);
+            }
           } else {
             acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, b), acc[r], 0, 0, 0);
           }
@@ -604,10 +616,12 @@ __global__ __launch_bounds__(kDownWaves * 64, WIDE || R == 4 ? 2 : 4) void down_
     const int token = l16 < cur.n ? l.token[cur.first + l16] : 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      floatx4 t = acc[r];
-      if constexpr (!WIDE) {  // the terms' columns, smallest first
-        const u32x4 bits = __builtin_bit_cast(u32x4, t);
-        t = __builtin_bit_cast(floatx4, shifted<8>(bits)) + __builtin_bit_cast(floatx4, shifted<4>(bits)) + t;
+      floatx4 t;
+      if constexpr (WIDE) {
+        t = with_rest(acc[r], rest[r]);
+      } else {  // the terms' columns, smallest first
+        const u32x4 bits = __builtin_bit_cast(u32x4, acc[r]);
+        t = with_rest(acc[r], __builtin_bit_cast(floatx4, shifted<8>(bits)) + __builtin_bit_cast(floatx4, shifted<4>(bits)));
       }
       if (l16 < cur.n) *reinterpret_cast<floatx4*>(mine + token * PITCH + r * 16 + g * 4) += t;
     }
