@@ -11,9 +11,9 @@ the grouped FFN and the combine run as one launch with tile-level signals
 by moe_route_grouped instead of moe_route_topk; with a SharedExpert every token
 also goes through a dense FFN (two moe_linear calls) whose down product is
 added to the combined output.  With experts in MXFP4 (ffi.Mxfp4 weights) the
-tokens and the activations are quantised too and the grouped FFN is two
-moe_grouped_linear_mxfp4 calls; a SharedExpert in MXFP4 runs the same way on
-moe_linear_mxfp4.  With few_tokens=True, for at most 64 tokens, routing,
+tokens, in permute(), and the activations are quantised too and the grouped FFN
+is two moe_grouped_linear_mxfp4 calls; a SharedExpert in MXFP4 runs the same way
+on moe_linear_mxfp4.  With few_tokens=True, for at most 64 tokens, routing,
 experts and combine are one moe_few_tokens call over bf16 or MXFP4 experts,
 whose activations stay in full precision.
 """
@@ -131,7 +131,10 @@ class MoELayer:
         ffi.moe_route_topk(self.logits, self.cfg.k, self.renormalize, self.topk_idx, self.topk_w, stream)
 
     def permute(self, stream=None):
+        """Rows by expert; for experts in MXFP4 indices only, and the tokens quantised."""
         c = self.cfg
+        if self.mxfp4:
+            self.quantize_tokens(stream)
         ffi.moe_permute(self.x, self.topk_idx, self.src_rank, c.E, c.expert_begin, c.n_local,
                         c.num_ranks, self.tile_m, out=self.perm, ws=self.ws, stream=stream,
                         copy_rows=not self.fused_gather)
@@ -165,6 +168,8 @@ class MoELayer:
         """The shared expert's FFN, added to the combined output."""
         s = self.shared
         if self.shared_mxfp4:
+            if not self.mxfp4 or self.few_tokens:  # (else permute() has done it)
+                self.quantize_tokens(stream)
             ffi.moe_linear_mxfp4(self.x_q, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, ws=self.shared_ws[0],
                                  stream=stream, use_workspace=False)
             ffi.moe_mxfp4_quantize(self.shared_h, out=self.shared_q, stream=stream)
@@ -184,8 +189,6 @@ class MoELayer:
                            expert_begin=c.expert_begin, num_experts=c.E, out=self.out, ws=self.few_ws, stream=stream)
 
     def run(self, stream=None) -> torch.Tensor:
-        if self.x_q is not None:
-            self.quantize_tokens(stream)
         if self.few_tokens:
             if self.gating is not None:
                 self.route(stream)
