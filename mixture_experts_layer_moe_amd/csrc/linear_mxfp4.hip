@@ -39,7 +39,7 @@ __device__ __forceinline__ intx8 widen(u32x4 v) { return intx8{(int)v[0], (int)v
 // Which rows and weights a tile has.
 struct Rows {
   int64_t row0;  // first row of out (and of x, unless gathered)
-  int valid;     // rows that exist, <= 0: none
+  int valid;     // rows that exist, 0: none
   int expert;
 };
 
@@ -53,19 +53,29 @@ template <bool GROUPED>
 __device__ __forceinline__ Rows rows_of(const Product& p, int ti, int bm) {
   Rows r;
   if constexpr (GROUPED) {
+    // An entry that names no local expert, or rows outside the capacity, has none: whatever the list holds, nothing beyond
+    // x, the weights and out is touched.
     const int t = ti / p.sub;
     r.expert = p.a.tiles[2 * t];
-    const int first = p.a.tiles[2 * t + 1] + (ti - t * p.sub) * bm;
-    r.row0 = first;
-    r.valid = p.a.offsets[r.expert] + p.a.counts[r.expert] - first;
+    r.row0 = (int64_t)p.a.tiles[2 * t + 1] + (ti - t * p.sub) * bm;
+    r.valid = 0;
+    if ((uint32_t)r.expert >= (uint32_t)p.a.E_loc || r.row0 < 0 || r.row0 >= p.a.R_cap) return r;
+    const int64_t end = (int64_t)p.a.offsets[r.expert] + p.a.counts[r.expert];
+    const int64_t left = (end < p.a.R_cap ? end : p.a.R_cap) - r.row0;
+    r.valid = left < bm ? (int)(left > 0 ? left : 0) : bm;
   } else {
     r.expert = 0;
     r.row0 = (int64_t)ti * bm;
     const int64_t left = p.a.M - r.row0;
     r.valid = left < bm ? (int)left : bm;
   }
-  if (r.valid > bm) r.valid = bm;
   return r;
+}
+
+// Row tiles of the list's entries.
+__device__ __forceinline__ int row_tiles(const Product& p) {
+  const int n = *p.a.num_tiles;
+  return n > 0 ? (n < p.a.tiles_cap ? n : (int)p.a.tiles_cap) * p.sub : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -551,16 +561,12 @@ template <int BM, int BN, int NMAT, int WM, int WN, int NS, bool GROUPED>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
   using T = Tile<BM, BN / NMAT, NMAT, WM, WN, NS>;
   __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
-  int mt = p.mt;
-  if (GROUPED) {
-    const int n = *p.a.num_tiles * p.sub;
-    mt = n < mt ? n : mt;
-  }
+  const int mt = GROUPED ? row_tiles(p) : p.mt;
   if ((int)blockIdx.x >= mt * p.nt) return;
   int ti, tj;
   tile_of(blockIdx.x, mt, p.nt, ti, tj);
   const Rows rw = rows_of<GROUPED>(p, ti, BM);
-  if (rw.valid <= 0) return;
+  if (rw.valid == 0) return;
   T::template run<GROUPED>(smem, p, rw, tj * (BN / NMAT));
 }
 
@@ -710,9 +716,9 @@ template <int MB, int NMAT, bool GROUPED>
 __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(Product p) {
   __shared__ float red[kStreamWaves * NMAT * MB * 256];
   const int ti = blockIdx.x / p.nt, n0 = (int)(blockIdx.x % p.nt) * 16;
-  if (GROUPED && ti >= *p.a.num_tiles * p.sub) return;
+  if (GROUPED && ti >= row_tiles(p)) return;
   const Rows rw = rows_of<GROUPED>(p, ti, 16 * MB);
-  if (rw.valid <= 0) return;
+  if (rw.valid == 0) return;
   if (MB == 1 && rw.valid <= 4) stream_rows<MB, NMAT, GROUPED, MB == 1>(p, rw, n0, red);
   else stream_rows<MB, NMAT, GROUPED, false>(p, rw, n0, red);
 }

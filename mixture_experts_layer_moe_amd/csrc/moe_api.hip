@@ -615,6 +615,7 @@ moe_status moe_grouped_linear_mxfp4(const void* x_codes, const void* x_scales, c
   a.row_src = row_src;
   a.topk = k;
   a.tile_m = tile_m;
+  a.E_loc = E_loc;
   a.tiles_cap = tiles_cap;
   a.R_cap = R_cap;
   return linear_launched(moe::launch_grouped_linear_mxfp4(a, static_cast<hipStream_t>(stream)));

@@ -85,7 +85,7 @@ struct MxLinearArgs {
   void* out;
   // Grouped: row tiles of the permutation (counts null: dense).
   const int32_t *counts, *offsets, *tiles, *num_tiles, *row_src;  // row_src null: x's rows are the permuted ones
-  int topk, tile_m;
+  int topk, tile_m, E_loc;
   int64_t tiles_cap, R_cap;
 };
 hipError_t launch_linear_mxfp4(const MxLinearArgs& a, hipStream_t s);
