@@ -150,6 +150,8 @@ moe_status moe_route_topk(const float* logits, int64_t T, int32_t E, int32_t k,
  * x and x_perm may both be NULL: then only the index outputs are written, for
  * moe_grouped_ffn_gather, which reads the token rows from x itself.
  * ws / ws_bytes: device scratch of at least moe_permute_workspace_bytes().
+ * T == 0 writes no output: num_tiles has to hold 0 before a grouped call reads
+ * it (the Python binding sets it, the counts and the offsets).
  * Requires H % 8 == 0, tile_m in {16, 32, 64, 128, 256},
  * E_loc * num_ranks <= 4096, num_ranks <= 64, k <= 32, T <= 2^26 - 16.
  */

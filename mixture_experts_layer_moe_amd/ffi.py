@@ -189,6 +189,13 @@ def alloc_permuted(T: int, H: int, k: int, E_loc: int, tile_m: int, device, rows
         tile_m=tile_m, R_cap=R_cap, tiles_cap=tcap)
 
 
+def _no_rows(out: Permuted, stream):
+    """What a permutation of no token is: the library launches nothing for it, and the grouped calls read these."""
+    with torch.cuda.stream(stream):  # (None: the current one)
+        for t, v in ((out.expert_counts, 0), (out.expert_offsets, 0), (out.num_tiles, 0), (out.row_src, -1)):
+            t.fill_(v)
+
+
 def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, src_rank: Optional[torch.Tensor], E: int,
                 expert_begin: int, E_loc: int, num_ranks: int, tile_m: int,
                 out: Optional[Permuted] = None, ws: Optional[torch.Tensor] = None,
@@ -212,6 +219,8 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, src_rank: Optional[torc
         _ptr(out.row_src),
         _ptr(out.inv_perm), _ptr(out.tiles), _ptr(out.num_tiles), _ptr(ws), ws.numel(),
         _stream(stream)))
+    if T == 0:
+        _no_rows(out, stream)
     return out
 
 
@@ -227,10 +236,13 @@ def moe_permute_noalloc(x: Optional[torch.Tensor], topk_idx: torch.Tensor, src_r
     if src_rank is not None:
         _need(src_rank, torch.int32, "src_rank")
     T, k = topk_idx.shape
-    return int(lib().moe_permute_noalloc(
+    status = int(lib().moe_permute_noalloc(
         _ptr(x), _ptr(topk_idx), _ptr(src_rank), T, H, k, E, expert_begin, E_loc, num_ranks, tile_m,
         _ptr(out.x_perm), _ptr(out.expert_counts), _ptr(out.expert_offsets), _ptr(out.row_src),
         _ptr(out.inv_perm), _ptr(out.tiles), _ptr(out.num_tiles), _stream(stream)))
+    if T == 0 and status == 0:
+        _no_rows(out, stream)
+    return status
 
 
 def moe_grouped_ffn(p: Permuted, w0: torch.Tensor, w0_up: Optional[torch.Tensor], w1: torch.Tensor,
