@@ -189,7 +189,7 @@ moe_status grouped_ffn_impl(const void* x_perm, const void* x, const int32_t* ro
     if (T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
     if (T * (int64_t)H * 2 > INT32_MAX || T * (int64_t)k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   }
-  if (R_cap == 0 || tiles_cap == 0) return MOE_OK;
+  if (R_cap == 0 || tiles_cap == 0 || (gather && T == 0)) return MOE_OK;
   const void* ptrs[] = {gather ? x : x_perm, expert_counts, expert_offsets, tiles, num_tiles, w0, w1, act_buf, y_perm};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
@@ -244,7 +244,7 @@ moe_status moe_grouped_ffn_gather(const void* x, const int32_t* row_src, int64_t
                                   const void* w0_up, const void* w1, int32_t E_loc, int32_t H, int32_t F,
                                   int32_t act, int32_t tile_m, int64_t R_cap, int64_t tiles_cap, void* act_buf,
                                   float* y_perm, void* ws, size_t ws_bytes, void* stream) {
-  if (!x) return MOE_ERR_INVALID_ARG;
+  if (!x && T != 0) return MOE_ERR_INVALID_ARG;
   return grouped_ffn_impl(nullptr, x, row_src, T, k, expert_counts, expert_offsets, tiles, num_tiles, w0, w0_up, w1,
                           E_loc, H, F, act, tile_m, R_cap, tiles_cap, act_buf, y_perm, ws, ws_bytes, stream);
 }

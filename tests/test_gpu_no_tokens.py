@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("mx", [False, True])
-@pytest.mark.parametrize("kw", [dict(), dict(few_tokens=True), dict(gating=Gating())])
+@pytest.mark.parametrize("kw", [dict(), dict(fused_gather=True), dict(few_tokens=True), dict(gating=Gating())])
 @pytest.mark.parametrize("tile_m", [16, 256])
 def test_layer_without_a_token(kw, mx, tile_m):
     cfg = W.CONFIGS["decode"].with_(T=4, H=256, F=128, E=8, k=2, tile_m=tile_m)
