@@ -603,9 +603,11 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int32_t k, int32_t F);
  *   w0, w0_up, w1   moe_grouped_ffn's weights [E_loc, F, H], [E_loc, F, H] (SwiGLU only), [E_loc, H, F] in bf16, with
  *             the three *_scales NULL; or MXFP4 codes [.., / 2] with their scales [.., / 32]
  *   out       [T, H] fp32 out
- * Weights enter the products exactly, accumulation is fp32, and activations
- * stay in fp32 between the two products.  Results are deterministic.  Outputs
- * and ws must not overlap the inputs or one another (checked).
+ * Weights enter the products exactly, but MXFP4 values that pass bf16's
+ * largest (s > 252) as infinities, as moe_mxfp4_dequantize gives them;
+ * accumulation is fp32, and activations stay in fp32 between the two products.
+ * Results are deterministic.  Outputs and ws must not overlap the inputs or one
+ * another (checked).
  * ws / ws_bytes: device scratch of at least moe_few_tokens_workspace_bytes();
  * nothing in it has to start at zero or is kept for the next call.
  * Requires T <= 64, E <= 1024, k <= 32, H % 128 == 0, F % 128 == 0,

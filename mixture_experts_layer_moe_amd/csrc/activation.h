@@ -1,4 +1,4 @@
-// Device helpers shared by the products' epilogues: buffer resources, bf16 widening, activations.
+// Device helpers shared by the products' kernels: buffer resources, bf16 widening, MXFP4 scales, activations.
 #pragma once
 
 #include "common.h"
@@ -10,6 +10,10 @@ typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
 __device__ __forceinline__ float bf2f(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+
+// The scale of byte s, 2^(s - 127), as the conversions of 4-bit codes (v_cvt_scalef32_*) take it: they read a float's
+// exponent alone, so that 0 is 2^-127 here, and 255 makes NaN.
+__device__ __forceinline__ float mxfp4_scale(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
 
 // Raw buffer resource over [base, base + bytes): out-of-range reads return zero.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {

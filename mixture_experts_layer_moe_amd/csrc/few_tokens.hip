@@ -308,7 +308,7 @@ struct Weights<true> {  // step s: indices 32 (lane / 16) + 8 s + 0..7 of row la
   }
   // scales: the unit's four scale bytes of the row
   __device__ __forceinline__ bf16x8 get(int s, uint32_t scales) const {
-    const float scale = __builtin_bit_cast(float, ((scales >> (8 * ((threadIdx.x >> 4) & 3))) & 255u) << 23);
+    const float scale = mxfp4_scale((scales >> (8 * ((threadIdx.x >> 4) & 3))) & 255u);
     struct { bf16x2 p[4]; } o;
     o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[s], scale, 0);
     o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[s], scale, 1);

@@ -28,9 +28,6 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
 
-// The scale of byte s as the conversions take it (2^-127 is a denormal float).
-__device__ __forceinline__ float scale_of(uint32_t s) { return __builtin_bit_cast(float, s ? s << 23 : 0x00400000u); }
-
 // Eight values as fp32.
 template <bool F32>
 struct Eight {
@@ -72,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const u32x4* __restr
     o = dpp<0x4E>(top);           // quad_perm [2,3,0,1]
     top = o > top ? o : top;
     const uint32_t e = top >> 23, s = e == 255 ? 255 : e > 2 ? e - 2 : 0;
-    const float scale = scale_of(s);
+    const float scale = mxfp4_scale(s);
     uint32_t c = 0;
     if (e != 255) {
       c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[q][0], v[q][1], scale, 0);
@@ -103,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const void* __rest
   for (int q = 0; q < kUnits; ++q) {
     const int64_t u = u0 + q * kThreads;
     if (u >= units) return;
-    const float scale = scale_of(s[q]);
+    const float scale = mxfp4_scale(s[q]);
     if constexpr (F32) {
       const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[q], scale, 1);
       out[u] = __builtin_bit_cast(u32x4, floatx4{a.x, a.y, b.x, b.y});

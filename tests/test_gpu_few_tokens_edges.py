@@ -44,3 +44,58 @@ def test_infinite_weights_of_the_second_product(T, mx, scale):
     np.testing.assert_allclose(out[:, 8], 64 * 128 * scale, rtol=65 * 2.0 ** -23)
     rest = np.delete(out, [5, 6, 7, 8], axis=1)
     assert (rest == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 32])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_scale_bytes_from_end_to_end(T, act):
+    """Blocks of codes under the bytes 0, 1, 252 and 254, brought to one size by the tokens and by the gate weights."""
+    g = F.gen(T)
+    E, H, K = 4, 128, 128
+    ends = np.array([0, 1, 252, 254])
+    w = F.Experts(g, E, H, K, act, True)
+
+    def redo(q, byte):  # byte [..., blocks]; under 254 codes up to 1.5, the largest that bf16 holds
+        c = torch.randint(0, 16, q.shape, generator=g).numpy()
+        c = np.where(np.repeat(byte, 32, axis=-1) == 254, c & 11, c)
+        q.codes.copy_(torch.from_numpy(X.pack(c)))
+        q.scales.copy_(torch.from_numpy(byte.astype(np.uint8)))
+    for q in w.t[:2]:
+        if q is not None:
+            redo(q, np.broadcast_to(ends, (E, K, 4)))
+    redo(w.t[2], np.broadcast_to(ends[:, None, None], (E, H, 4)))   # one byte an expert
+    x = torch.randn(T, H, generator=g).sign().double() * torch.from_numpy(np.exp2(np.minimum(127.0 - ends, 127.0).clip(-126.0)).repeat(32))
+    x = x.to(BF)
+    idx = (torch.arange(T, dtype=torch.int32) % E)[:, None]
+    for first in range(E if T == 1 else 1):
+        e = (idx + first) % E
+        gate = torch.from_numpy(np.array([2.0 ** 100, 2.0 ** 100, 2.0 ** -100, 2.0 ** -100]))[e.long()].float()
+        out, i2, g2 = F.run(x, w, idx=e.to(torch.int32), gate=gate, num_experts=E)
+        ref = F.check_out(out, x, i2, g2, w, E, norm=False)
+        assert (np.linalg.norm(out - ref, axis=1) <= 2e-5 * np.linalg.norm(ref, axis=1)).all() and (np.abs(ref) > 0).any(axis=1).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 32])
+@pytest.mark.parametrize("byte,code,value", [(252, 7, 6 * 2.0 ** 125), (253, 5, 3 * 2.0 ** 126), (253, 6, INF), (253, 7, INF), (254, 3, 1.5 * 2.0 ** 127),
+                                             (254, 4, INF), (254, 15, -INF)])
+def test_values_at_and_past_the_largest_bf16(T, byte, code, value):
+    """MXFP4 values past bf16's largest are infinities in both products, as read back."""
+    d = F.dev()
+    one = lambda: X.quantize(np.ones((1, 128, 128)))  # noqa: E731
+    for which in (0, 1):
+        q = [one(), one()]
+        q[which][0][0, 3, 40], q[which][1][0, 3, 1] = code, byte
+        q[which][0][0, 3, 32:40] = q[which][0][0, 3, 41:64] = 0
+        w0, w1 = (ffi.Mxfp4(torch.from_numpy(X.pack(c)).to(d), torch.from_numpy(s).to(d)) for c, s in q)
+        assert F.n64(ffi.moe_mxfp4_dequantize((w0, w1)[which]))[0, 3, 40] == value
+        x, scale = torch.zeros(T, 128, dtype=BF, device=d), 1.0
+        if which == 0:  # z[3] = 768 or infinite, gelu(z) = z (of -inf: NaN); the others vanish beside it
+            x[:, 40] = 2.0 ** -118
+            want = np.full(128, value * 2.0 ** -118 if value > 0 else np.nan)
+        else:           # every activation is 128 2^-100
+            x[:], scale = 1.0, 2.0 ** -100
+            want = np.full(128, 128.0 * 128 * scale)
+            want[3] = (96 + value) * 128 * scale
+        out = F.n64(ffi.moe_few_tokens(x, w0, None, w1, "gelu", topk_idx=torch.zeros(T, 1, dtype=torch.int32, device=d),
+                                       topk_w=torch.full((T, 1), scale, device=d)))
+        np.testing.assert_allclose(out, np.broadcast_to(want, out.shape), rtol=130 * 2.0 ** -23)
