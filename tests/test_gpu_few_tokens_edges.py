@@ -99,3 +99,54 @@ def test_values_at_and_past_the_largest_bf16(T, byte, code, value):
         out = F.n64(ffi.moe_few_tokens(x, w0, None, w1, "gelu", topk_idx=torch.zeros(T, 1, dtype=torch.int32, device=d),
                                        topk_w=torch.full((T, 1), scale, device=d)))
         np.testing.assert_allclose(out, np.broadcast_to(want, out.shape), rtol=130 * 2.0 ** -23)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_masks_and_ties_in_small_calls(n, renorm):
+    """Rows that leave slots empty, ties and infinities, n tokens a call: routed by one wavefront, by the workgroups of the
+    first launch, or by a launch of their own."""
+    E, k, T = 24, 4, 12
+    g = F.gen(n)
+    w = F.Experts(g, E, 128, 128, "swiglu", False)
+    x = torch.randn(T, 128, generator=g).to(BF)
+    l = torch.randn(T, E, generator=g)
+    l[0] = -INF
+    l[1] = float("nan")
+    l[2, 2:] = -INF
+    l[3, ::2] = float("nan")
+    l[4] = torch.finfo(torch.float32).min
+    l[5, 3:] = torch.finfo(torch.float32).min
+    l[6, 20] = l[6, 7] = INF
+    l[7] = 0.25
+    l[8] = torch.where(torch.arange(E) % 2 == 0, 0.0, -0.0)
+    l[9] = l[9].round()
+    l[10, :] = -INF
+    l[10, 23] = -1000.0
+    ridx, rw = X.route(l.numpy(), k, renorm)
+    for t in range(0, T, n):
+        rows = slice(t, t + n)
+        out, idx, gate = F.run(x[rows], w, l[rows].contiguous(), k, renormalize=renorm)
+        assert np.array_equal(idx, ridx[rows])
+        np.testing.assert_allclose(gate, rw[rows], rtol=4e-6, atol=1e-37)
+        F.check_out(out, x[rows], idx, gate, w, E)
+        assert (out[(idx < 0).all(axis=1)] == 0).all()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 4, 9, 64])
+@pytest.mark.parametrize("e0,El", [(0, 3), (9, 7)])
+def test_a_share_with_logits_over_all_experts(T, e0, El, mx):
+    """Tokens routed here over every expert, of which a few are local."""
+    g = F.gen(T + e0)
+    E, k = 16, 5
+    w = F.Experts(g, El, 256, 128, "swiglu", mx)
+    x = torch.randn(T, 256, generator=g).to(BF)
+    l = torch.randn(T, E, generator=g)
+    l[T // 2, e0:e0 + El] = -20.0                       # no local expert
+    out, idx, gate = F.run(x, w, l, k, expert_begin=e0, num_experts=E)
+    ridx, rw = X.route(l.numpy(), k, True)
+    assert np.array_equal(idx, ridx)
+    np.testing.assert_allclose(gate, rw, rtol=4e-6, atol=1e-37)
+    F.check_out(out, x, idx, gate, w, El, e0)
+    assert (out[T // 2] == 0).all()
