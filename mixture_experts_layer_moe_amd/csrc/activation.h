@@ -1,4 +1,4 @@
-// Device helpers shared by the products' kernels: buffer resources, bf16 widening, MXFP4 scales, activations.
+// Device helpers shared by the kernels: buffer resources, bf16 widening, MXFP4 scales, lane shifts, activations.
 #pragma once
 
 #include "common.h"
@@ -18,6 +18,21 @@ __device__ __forceinline__ float mxfp4_scale(uint32_t s) { return __builtin_bit_
 // Raw buffer resource over [base, base + bytes): out-of-range reads return zero.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// Data-parallel primitive: lanes of the enabled rows of 16 get `v` of the lane that CTRL names, `old` where there is none.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
+}
+// Lanes i of each 16 get lane i + N's, the last N zeros.
+template <int N>
+__device__ __forceinline__ u32x4 shifted(u32x4 v) {
+  if constexpr (N == 0) return v;
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)dpp<0x100 + N>(0, (int)v[i]);  // row_shl:N
+  return o;
 }
 
 // 1 / (1 + e^-z) with the hardware exp2 and reciprocal (about 1 ulp each).

@@ -59,10 +59,6 @@ size_t lists_bytes(int T, int k, int E_loc) {
   return (size_t)E_loc * 12 + (size_t)(E_loc + T * k / kLeastBatch) * 8 + (size_t)T * k * 16 + 32;
 }
 
-template <int CTRL, int ROWS = 0xf>
-__device__ __forceinline__ int dpp(int old, int v) {
-  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
-}
 // Reduction of a wavefront by DPP (rows of 16 lanes, then across them); every lane gets the result.
 template <typename F>
 __device__ __forceinline__ int wave_reduce(int v, int none, F f) {
@@ -335,16 +331,6 @@ struct GroupScales {
 };
 template <int M>
 struct GroupScales<false, M> {};
-
-// Columns i of each 16 get columns i + N.
-template <int N>
-__device__ __forceinline__ u32x4 shifted(u32x4 v) {
-  if constexpr (N == 0) return v;
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)dpp<0x100 + N>(0, (int)v[i]);  // row_shl:N
-  return o;
-}
 
 // Calls f with the steps 0..3 as constants.
 template <typename F>

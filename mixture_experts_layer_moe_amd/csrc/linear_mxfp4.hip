@@ -585,15 +585,6 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(Product p) {
 // else the units' latency (one row of 2048 x 7168 SwiGLU 7.0 us).
 constexpr int kStreamWaves = 4;
 
-template <int N>
-__device__ __forceinline__ u32x4 shifted(u32x4 v) {
-  if constexpr (N == 0) return v;
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], 0x100 + N, 0xf, 0xf, false);  // row_shl:N
-  return o;
-}
-
 template <int MB, int NMAT, bool GROUPED, bool FOUR>
 __device__ __forceinline__ void stream_rows(const Product& p, const Rows& rw, int n0, float* red) {
   constexpr int RED = NMAT * MB * 256;  // floats of a wavefront's sums

@@ -23,11 +23,6 @@ constexpr int kUnits = 4;  // lane units of eight values a thread has in flight
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-}
-
 // Eight values as fp32.
 template <bool F32>
 struct Eight {
@@ -64,9 +59,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const u32x4* __restr
       const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7fffffffu;
       top = m > top ? m : top;
     }
-    uint32_t o = dpp<0xB1>(top);  // quad_perm [1,0,3,2]
+    uint32_t o = (uint32_t)dpp<0xB1>(0, (int)top);  // quad_perm [1,0,3,2]
     top = o > top ? o : top;
-    o = dpp<0x4E>(top);           // quad_perm [2,3,0,1]
+    o = (uint32_t)dpp<0x4E>(0, (int)top);           // quad_perm [2,3,0,1]
     top = o > top ? o : top;
     const uint32_t e = top >> 23, s = e == 255 ? 255 : e > 2 ? e - 2 : 0;
     const float scale = mxfp4_scale(s);
