@@ -514,7 +514,8 @@ moe_status moe_mxfp4_quantize(const void* x, int64_t R, int32_t K, int32_t x_dty
  * moe_mxfp4_dequantize -- the values of codes and scales as out [R, K] of
  * out_dtype: exact, but where 2^(s - 127) times a code passes the type's
  * largest value (s > 252): infinity.  out must not overlap the inputs
- * (checked).  Requires K % 32 == 0, R * K <= 2^36.  R == 0: nothing to do.
+ * (checked).  Requires K % 32 == 0, R * K <= 2^36 (2^36 - 4096 to fp32).
+ * R == 0: nothing to do.
  */
 moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R, int32_t K, int32_t out_dtype, void* out,
                                 void* stream);

@@ -528,8 +528,8 @@ moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R
   const size_t n = (size_t)R * K;
   const Span outs[] = {{out, n * (out_dtype == MOE_F32 ? 4 : 2)}}, ins[] = {{codes, n / 2}, {scales, n / 32}};
   if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
-  return launched(moe::launch_mxfp4_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
-                                               R * (K / 32), out_dtype == MOE_F32, out, static_cast<hipStream_t>(stream)));
+  return linear_launched(moe::launch_mxfp4_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                                      R * (K / 32), out_dtype == MOE_F32, out, static_cast<hipStream_t>(stream)));
 }
 
 // (no size splits its reduction)

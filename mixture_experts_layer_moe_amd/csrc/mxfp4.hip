@@ -124,7 +124,9 @@ hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t blocks, uint8_
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, bool f32, void* out,
                                    hipStream_t s) {
   const int64_t units = blocks * (f32 ? 8 : 4);
-  const dim3 grid((unsigned)((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
+  const int64_t groups = (units + kThreads * kUnits - 1) / (kThreads * kUnits);
+  if (groups * kThreads > UINT32_MAX) return hipErrorNotSupported;  // (a grid holds fewer than 2^32 threads)
+  const dim3 grid((unsigned)groups);
   u32x4* dst = static_cast<u32x4*>(out);
   if (f32) hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, s, codes, scales, units, dst);
   else hipLaunchKernelGGL(dequantize_kernel<false>, grid, dim3(kThreads), 0, s, codes, scales, units, dst);
