@@ -520,8 +520,8 @@ moe_status moe_mxfp4_quantize(const void* x, int64_t R, int32_t K, int32_t x_dty
 moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R, int32_t K, int32_t out_dtype, void* out,
                                 void* stream);
 
-/* Bytes of the optional device workspace of moe_linear_mxfp4 on the current
- * device: 0, no size uses one at present (0 on invalid arguments, too). */
+/* Bytes of the device workspace of moe_linear_mxfp4: 0 for every size and
+ * device, as none uses one (0 on invalid arguments, too). */
 size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t act);
 
 /*
@@ -539,8 +539,8 @@ size_t moe_linear_mxfp4_workspace_bytes(int64_t M, int32_t N, int32_t K, int32_t
  * residual are fp32; each output is rounded once.  Results are deterministic.
  * out and ws must not overlap the inputs or one another (checked; residual ==
  * out excepted).
- * ws / ws_bytes: device scratch of at least moe_linear_mxfp4_workspace_bytes()
- * (NULL / 0 is allowed, as for moe_linear).
+ * ws / ws_bytes: as for moe_linear, checked and not used; NULL / 0 is all that
+ * moe_linear_mxfp4_workspace_bytes() asks for.
  * Requires K % 128 == 0; N, K <= 1048576; M <= 2^31 - 1; products of more than
  * 4 million blocks of 64 rows and 64 columns may return MOE_ERR_UNSUPPORTED.
  * M == 0: nothing to do.

@@ -532,7 +532,7 @@ moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t R
                                                       R * (K / 32), out_dtype == MOE_F32, out, static_cast<hipStream_t>(stream)));
 }
 
-// (no size splits its reduction)
+// (no size splits its reduction, so none needs a buffer; moe_linear_mxfp4 checks the one it is given)
 size_t moe_linear_mxfp4_workspace_bytes(int64_t, int32_t, int32_t, int32_t) { return 0; }
 
 moe_status moe_linear_mxfp4(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
@@ -651,7 +651,7 @@ moe_status moe_few_tokens(const void* x, const float* logits, int64_t T, int32_t
                       {w0_scales, n / 32}, {w0_up_scales, n / 32}, {w1_scales, n / 32}};
   const Span outs[] = {{out, (size_t)T * H * 4}, {ws, ws_bytes}, {topk_idx, tk}, {topk_w, tk}};
   if (clash(outs, ins)) return MOE_ERR_INVALID_ARG;
-  const moe::FewArgs a{static_cast<const uint16_t*>(x), logits, (int)T, E, k, expert_begin, E_loc, H, F, act, renormalize != 0,
+  const moe::FewArgs a{static_cast<const uint16_t*>(x), logits, (int)T, E, k, expert_begin, E_loc, H, F, renormalize != 0,
                        w0, w0_up, w1, static_cast<const uint8_t*>(w0_scales), static_cast<const uint8_t*>(w0_up_scales),
                        static_cast<const uint8_t*>(w1_scales), topk_idx, topk_w, out, ws};
   return launched(moe::launch_few_tokens(a, static_cast<hipStream_t>(stream)));

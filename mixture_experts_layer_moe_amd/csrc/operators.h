@@ -96,9 +96,9 @@ constexpr int kFewTokens = 64;
 struct FewArgs {
   const uint16_t* x;
   const float* logits;  // null: topk_idx and topk_w are given
-  int T, E, k, expert_begin, E_loc, H, F, act;
+  int T, E, k, expert_begin, E_loc, H, F;
   bool renormalize;
-  const void *w0, *w0_up, *w1;           // bf16, or MXFP4 codes
+  const void *w0, *w0_up, *w1;           // bf16, or MXFP4 codes; w0_up null: GELU, else SwiGLU
   const uint8_t *s0, *s0_up, *s1;        // MXFP4 scales, or null
   int32_t* topk_idx;
   float* topk_w;

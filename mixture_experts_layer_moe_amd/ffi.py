@@ -664,16 +664,16 @@ def linear_mxfp4_workspace_bytes(M: int, N: int, K: int, act: str) -> int:
 
 
 def alloc_linear_mxfp4_workspace(M: int, N: int, K: int, act: str, device) -> Optional[torch.Tensor]:
-    """Workspace of moe_linear_mxfp4 on that device (None where this size needs none)."""
-    with torch.cuda.device(device):
-        return _alloc_ws(linear_mxfp4_workspace_bytes(M, N, K, act), device)
+    """Workspace of moe_linear_mxfp4: None, as no size uses one on any device."""
+    return _alloc_ws(linear_mxfp4_workspace_bytes(M, N, K, act), device)
 
 
 def moe_linear_mxfp4(x: Mxfp4, w: Mxfp4, w_up: Optional[Mxfp4] = None, bias: Optional[torch.Tensor] = None,
                      bias_up: Optional[torch.Tensor] = None, act: str = "none", residual: Optional[torch.Tensor] = None,
                      out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                      ws: Optional[torch.Tensor] = None, stream=None, use_workspace: bool = True) -> torch.Tensor:
-    """moe_linear of MXFP4 operands x [M, K], w and w_up [N, K]; out may be residual itself, its type wins over out_dtype."""
+    """moe_linear of MXFP4 operands x [M, K], w and w_up [N, K]; out may be residual itself, its type wins over out_dtype.
+    ws and use_workspace are moe_linear's; no size uses a workspace, so none is made."""
     if stream is not None:
         _same_device(stream, x, w, w_up)
         return _on(stream, moe_linear_mxfp4, x, w, w_up, bias, bias_up, act, residual, out, out_dtype, ws,
@@ -686,8 +686,6 @@ def moe_linear_mxfp4(x: Mxfp4, w: Mxfp4, w_up: Optional[Mxfp4] = None, bias: Opt
         out = torch.empty(mn, dtype=out_dtype, device=xc.device)
     odt = out.dtype
     a = _choice(LINEAR_ACTS, act, "act")
-    if ws is None and use_workspace:
-        ws = alloc_linear_mxfp4_workspace(M, N, K, act, xc.device)
     wsp, wsn = _ws(ws, dev)
     _launch((_lib or lib()).moe_linear_mxfp4, "moe_linear_mxfp4", dev, *_mx(x, "x", (M, Kh), (M, Kb), dev), *_mx(w, "w", nk, nb, dev),
             *_mx(w_up, "w_up", nk, nb, dev, True), _take(bias, "bias", f32, (N,), dev, True),

@@ -111,10 +111,11 @@ class MoELayer:
         self.x_q = ffi.alloc_mxfp4((T, H), dev) if quantized else None
         if shared is not None:
             self.shared_h = torch.empty((T, Fs), dtype=torch.bfloat16, device=dev)
-            alloc = ffi.alloc_linear_mxfp4_workspace if self.shared_mxfp4 else ffi.alloc_linear_workspace
-            self.shared_ws = [alloc(T, Fs, H, cfg.act, dev), alloc(T, H, Fs, "none", dev)]
             if self.shared_mxfp4:
                 self.shared_q = ffi.alloc_mxfp4((T, Fs), dev)
+            else:
+                self.shared_ws = [ffi.alloc_linear_workspace(T, Fs, H, cfg.act, dev),
+                                  ffi.alloc_linear_workspace(T, H, Fs, "none", dev)]
 
     @classmethod
     def from_inputs(cls, cfg: MoEConfig, inputs: dict, **kw) -> "MoELayer":
@@ -170,11 +171,9 @@ class MoELayer:
         if self.shared_mxfp4:
             if not self.mxfp4 or self.few_tokens:  # (else permute() has done it)
                 self.quantize_tokens(stream)
-            ffi.moe_linear_mxfp4(self.x_q, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, ws=self.shared_ws[0],
-                                 stream=stream, use_workspace=False)
+            ffi.moe_linear_mxfp4(self.x_q, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, stream=stream)
             ffi.moe_mxfp4_quantize(self.shared_h, out=self.shared_q, stream=stream)
-            ffi.moe_linear_mxfp4(self.shared_q, s.w1, residual=self.out, out=self.out, ws=self.shared_ws[1],
-                                 stream=stream, use_workspace=False)
+            ffi.moe_linear_mxfp4(self.shared_q, s.w1, residual=self.out, out=self.out, stream=stream)
             return
         ffi.moe_linear(self.x, s.w0, w_up=s.w0_up, act=self.cfg.act, out=self.shared_h, ws=self.shared_ws[0],
                        stream=stream, use_workspace=False)

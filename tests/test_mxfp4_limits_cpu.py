@@ -1,4 +1,8 @@
 """Limits of the 4-bit operators' calls without a GPU; no library call here reaches a kernel launch."""
+import pytest
+
+from mixture_experts_layer_moe_amd import ffi
+
 from test_mxfp4_cpu import L, UNSUPPORTED, dequantize  # noqa: F401
 
 
@@ -7,3 +11,12 @@ def test_dequantize_to_fp32_stays_below_two_to_the_32_threads(L):  # noqa: F811
     assert dequantize(L, R=1 << 31, K=32, dt=1) == UNSUPPORTED
     assert dequantize(L, R=(1 << 31) - 127, K=32, dt=1) == UNSUPPORTED
     assert dequantize(L, R=(1 << 31) + 1, K=32, dt=0) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 8, 128), (1, 2048, 7168), (64, 4096, 14336), (300, 500, 14336), (1000, 1001, 1408), (8192, 8192, 8192)])
+@pytest.mark.parametrize("act", ["none", "gelu", "silu", "swiglu"])
+def test_no_dense_product_needs_a_workspace(M, N, K, act):
+    assert ffi.linear_mxfp4_workspace_bytes(M, N, K, act) == 0
+    assert ffi.alloc_linear_mxfp4_workspace(M, N, K, act, "cuda:0") is None  # (no device is looked at)
+    with pytest.raises(ValueError):
+        ffi.linear_mxfp4_workspace_bytes(M, N, K, "relu")
