@@ -755,6 +755,8 @@ def moe_few_tokens(x: torch.Tensor, w0: Weight, w0_up: Optional[Weight], w1: Wei
     E_loc, F = up[:2]
     if logits is not None:
         E = _matrix(logits, "logits")[1]
+        if num_experts is not None and num_experts != E:
+            raise ValueError(f"logits are over {E} experts, num_experts is {num_experts}")
         if k is None:
             if topk_idx is None:
                 raise ValueError("k is required")
@@ -766,7 +768,10 @@ def moe_few_tokens(x: torch.Tensor, w0: Weight, w0_up: Optional[Weight], w1: Wei
     else:
         if topk_idx is None or topk_w is None:
             raise ValueError("topk_idx and topk_w are required where there are no logits")
-        k = _matrix(topk_idx, "topk_idx")[1]
+        slots = _matrix(topk_idx, "topk_idx")[1]
+        if k is not None and k != slots:
+            raise ValueError(f"topk_idx has {slots} slots a token, k is {k}")
+        k = slots
         E = expert_begin + E_loc if num_experts is None else num_experts
         E = max(E, k)  # (ids beyond the local range name experts elsewhere)
     if out is None:

@@ -150,3 +150,17 @@ def test_a_share_with_logits_over_all_experts(T, e0, El, mx):
     np.testing.assert_allclose(gate, rw, rtol=4e-6, atol=1e-37)
     F.check_out(out, x, idx, gate, w, El, e0)
     assert (out[T // 2] == 0).all()
+
+
+def test_arguments_that_contradict_one_another():
+    d = F.dev()
+    w = F.Experts(F.gen(0), 4, 128, 128, "swiglu", False)
+    x, l = torch.randn(3, 128, device=d).to(BF), torch.randn(3, 8, device=d)
+    idx, gate = ffi.moe_route_topk(l, 2)
+    for bad in (dict(logits=l, k=2, num_experts=9), dict(logits=l, k=2, num_experts=4), dict(logits=l, k=3, topk_idx=idx),
+                dict(topk_idx=idx, topk_w=gate, k=3), dict(topk_idx=idx, topk_w=gate, k=1)):
+        with pytest.raises(ValueError):
+            ffi.moe_few_tokens(x, *w.t, "swiglu", **bad)
+    a = ffi.moe_few_tokens(x, *w.t, "swiglu", logits=l, k=2, num_experts=8)
+    b = ffi.moe_few_tokens(x, *w.t, "swiglu", topk_idx=idx, topk_w=gate, k=2, num_experts=8)
+    torch.testing.assert_close(a, b, rtol=1e-4, atol=1e-6)
