@@ -9,7 +9,10 @@
 // instructions' registers, by as many wavefronts as it takes to keep HBM busy; nothing is permuted and no row is padded to
 // a tile.  Measured: 4.5 TB/s of the chosen experts' weights with 64 tokens over 256 MXFP4 experts of 7168 x 2048 (1141
 // us), 4.7 to 5.6 with 13 over 8 bf16 experts of 4096 x 2048 (58 to 70 us); 32 us for one token of 2048 x 1408, six
-// experts, of which the dependent steps before the first weights are 4 to 5 us a launch.
+// experts, of which the dependent steps before the first weights are 4 to 5 us a launch.  Against routing, permute, grouped
+// products and combine one after another (tile_m 16): 32 us and 58 for that token, 135 and 158 for one over bf16 experts of
+// 7168 x 2048; but 244 and 224 for two of those, and 927 and 559 for 64 tokens over 8 bf16 experts of 4096 x 14336, whose
+// weights are read again for each 16 tokens of an expert.
 //
 // v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and tokens on its 16 columns: a column's result depends on
 // its own token alone, so columns without a token hold anything.  MXFP4 weights are widened in registers to bf16, which
@@ -665,8 +668,8 @@ hipError_t launch(const FewArgs& a, hipStream_t s) {
   };
   if constexpr (FP4) {
     // The most rows (fewer loads of the activations) that leave three CUs in four a workgroup, each half of a block's
-    // reduction: four instead of two for out of 7168 1237 us, 1315 (64 tokens, 256 experts of 2048), but of 4096 358 us, 290
-    // (32 tokens, 128 experts of 2048); one instead of two for out of 2048 86 us, 95 (16 tokens, 64 experts of 1408).
+    // reduction: four instead of two for out of 7168 1139 us, 1203 (64 tokens, 256 experts of 2048), but of 4096 422 us, 353
+    // (32 tokens, 128 experts of 2048); one instead of two for out of 2048 78 us, 88 (16 tokens, 64 experts of 1408).
     const auto enough = [&](int R) { return 2 * (a.H / (16 * R)) >= cu_count() / 4 * 3; };
     if constexpr (!WIDE)
       if (enough(4) && down_sums(a.T, 4) + lists_bytes(a.T, a.k, a.E_loc) <= kLds) return with(std::integral_constant<int, 4>{});

@@ -236,9 +236,11 @@ __device__ __forceinline__ constexpr int swz(int row) { return (row >> 1) & 7; }
 // stage has been read: there the workgroup synchronises, and the last step reads the next stage's first fragments.  The
 // 128 x 128 tile takes 72 KB, so that two share a CU: 93 us at 4096 x 14336 x 2048, 131 in a ring of four stages.
 //
-// Bound: LDS.  A stage of the 256 x 256 tile reads 192 KB and writes 64, 2050 cycles at 128 bytes a cycle of the 2700 it
-// takes; its matrix instructions take 1020 of each SIMD.  Measured: 8192 x 8192 x 8192 282 us (3.9 PFLOP/s), 4096 x 14336 x
-// 4096 SwiGLU 258 to 270 us (3.6 to 3.7).
+// Bound: LDS and the matrix cores alike, and the epilogue.  A stage of the 256 x 256 tile reads 192 KB and writes 64, 2050
+// cycles at 128 bytes a cycle of the 2600 to 2700 it takes, bank conflicts on top (19 % of the cycles in which LDS is active:
+// the scales' reads of four bytes at a pitch of 16); its 64 matrix instructions of 32 cycles take 2048 of each SIMD.  Over a
+// whole launch the matrix cores are 45 % busy, as a tile fills its CU and nothing is multiplied while its results are
+// written.  Measured: 8192 x 8192 x 8192 282 us (3.9 PFLOP/s), 4096 x 14336 x 4096 SwiGLU 249 to 270 us (3.6 to 3.9).
 //
 // A ring of NS > 2 stages straight to LDS, for the smallest tiles, whose time is the latency of their stages: 64 x 64 takes
 // 15.0 us at 128 x 4096 x 8192, 24.9 with staged codes.  Three stages, so that two or three tiles share a CU (five: 65 us
@@ -752,7 +754,7 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
   const int mats = dual ? 2 : 1;
   const int nk = (p.a.K + kStage - 1) / kStage;
   // Tiles: the kind that takes least, in us as fitted to 77 products of 64 to 49152 rows, 512 to 14336 indices, bf16 and
-  // fp32 outputs (its choice is 0.2 % above the best kind on average, 6 % at most).  A CU holds one of the two large kinds
+  // fp32 outputs (its choice is 0.4 % above the best kind on average, 6 % at most, over 71 of them).  A CU holds one of the two large kinds
   // at a time, which run in whole rounds.  It holds two or three of the small ones: rounds run into each other, and their
   // stages overlap but for the latency of a tile alone.
   struct Kind {
@@ -784,7 +786,8 @@ hipError_t launch(const Product& p0, bool grouped, hipStream_t s) {
     }
   }
   // Few rows: streamed where that takes less, us by the megabyte of codes as measured on 29 MB (17 rows of 4096 x 14336
-  // 11.7 us, 20.8 in tiles; of 14336 x 4096 13.3, 10.2 in tiles).  Grouped, tiles are never cut below 64 rows.
+  // 11.7 us, 21.5 in tiles; of 14336 x 4096 13.3, 10.2 in tiles).  Over 30 products of 17 to 64 rows the choice is 3 % above
+  // the best on average, 23 % at most (33 rows of 4096 x 14336: 21.7 in tiles, 17.7 streamed).  Grouped, tiles are never cut below 64 rows.
   const float mb_codes = (float)p.a.N * p.a.K * mats * 0.5e-6f;
   if (rows <= 16 || (grouped && rows < 64) || (!grouped && rows <= 32 && 5.f + 0.38f * mb_codes < least) ||
       (!grouped && rows <= 64 && 6.f + 0.65f * mb_codes < least)) {
