@@ -10,9 +10,9 @@
 // a tile.  Measured: 4.5 TB/s of the chosen experts' weights with 64 tokens over 256 MXFP4 experts of 7168 x 2048 (1141
 // us), 4.7 to 5.6 with 13 over 8 bf16 experts of 4096 x 2048 (58 to 70 us); 32 us for one token of 2048 x 1408, six
 // experts, of which the dependent steps before the first weights are 4 to 5 us a launch.  Against routing, permute, grouped
-// products and combine one after another (tile_m 16): 32 us and 58 for that token, 135 and 158 for one over bf16 experts of
-// 7168 x 2048; but 244 and 224 for two of those, and 927 and 559 for 64 tokens over 8 bf16 experts of 4096 x 14336, whose
-// weights are read again for each 16 tokens of an expert.
+// products and combine one after another, both captured (tile_m 16): 36 us and 61 for that token, 145 and 161 for one over
+// bf16 experts of 7168 x 2048; but 259 and 227 for two of those, and 932 and 564 for 64 tokens over 8 bf16 experts of
+// 4096 x 14336, whose weights are read again for each 16 tokens of an expert.
 //
 // v_mfma_f32_16x16x32_bf16 with 16 weight rows on its rows and tokens on its 16 columns: a column's result depends on
 // its own token alone, so columns without a token hold anything.  MXFP4 weights are widened in registers to bf16, which

@@ -18,8 +18,8 @@ product stores them and from there to 4 bits.
 
 With few_tokens=True, for at most 64 tokens, routing, experts and combine are one
 moe_few_tokens call over bf16 or MXFP4 experts, whose activations stay in full
-precision.  It is the faster form for one token (135 us instead of 158 over 256
-bf16 experts of 7168 x 2048, 51 instead of 84 in MXFP4), and for a few more where
+precision.  It is the faster form for one token (145 us instead of 156 over 256
+bf16 experts of 7168 x 2048, 55 instead of 85 in MXFP4), and for a few more where
 experts are small or few: to 16 tokens over 64 bf16 experts of 2048 x 1408, to 8
 in MXFP4; to 4 over 8 bf16 experts of 4096 x 14336, to 2 in MXFP4.  Beyond that
 the other form reads the weights faster (tile_m 16, or 64 where experts have more
